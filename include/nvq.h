@@ -462,6 +462,137 @@ int nvfp4_gemm_noalloc(const void* X, int x_dtype, int64_t T, int64_t k, int64_t
 int nvq_check_finite(const void* A, int dtype, int64_t rows, int64_t cols, int64_t ld, int32_t* status,
                      void* stream);
 
+/*
+ * ---- mixture of experts: the path around the experts' layers ------------------
+ * A mixture-of-experts layer sends each token to top_k of its E experts, and
+ * every expert is a linear layer of its own (quantized by the *_grouped and
+ * *_batched calls above).  These calls choose the experts, sort the tokens by
+ * expert, multiply the sorted rows with the experts' NVFP4 weights and sum
+ * each token's results, with the gradients of all but the sort:
+ *   moe_topk -> moe_sort -> nvfp4_gemm_grouped -> moe_combine.
+ * A slot is a (token, s) pair, 0 <= s < top_k; a row is a sorted slot.
+ * tok_idx and grp_off are those of hessian_accumulate_grouped, which takes
+ * grp_off on the host.  Sizes that depend on the routing stay on the device.
+ */
+
+/*
+ * moe_topk -- the router: ids[t][s] is the expert of token t's s-th largest
+ * logit (equal logits: the lower expert first), weights[t][s] its softmax
+ * weight, over all E logits or, with renorm != 0, over the chosen ones only.
+ * Softmax sums are fp32 with the row's largest logit subtracted.
+ *
+ *   logits   device [T x ld] of dtype (fp32 or bf16), T >= 0, 1 <= E <= 1024,
+ *            ld >= E; aligned by its elements.
+ *   top_k    1 <= top_k <= min(E, 64).
+ *   ids      device int32 [T x top_k]; weights device fp32 [T x top_k].
+ * A logit of -inf masks its expert, which is then never chosen: slots that no
+ * expert is left for have id -1 and weight 0.  A row with a NaN or +inf is
+ * rejected: its ids are -1 and its weights NaN, which moe_combine carries to
+ * the token's output.
+ */
+int moe_topk(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, int top_k, int renorm, int32_t* ids,
+             float* weights, void* stream);
+
+/*
+ * moe_topk_backward -- gradient of moe_topk's weights with respect to the
+ * logits: with c = sum_s dweights_s weights_s and p the softmax over all E
+ * (over the chosen experts with renorm, p = 0 elsewhere),
+ *   dlogits_j = p_j (sum of dweights_s over the slots with id j - c).
+ *   logits, ids, weights  as given to and written by moe_topk (with renorm
+ *            the logits are not read).
+ *   dweights device fp32 [T x top_k]; slots with id -1 are ignored.
+ *   dlogits  device [T x ldd] of the logits' dtype, ldd >= E; all E columns of
+ *            every row are written (NaN for a rejected row, 0 for one with no
+ *            expert left).  May not overlap logits.
+ */
+int moe_topk_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const int32_t* ids,
+                      const float* weights, const float* dweights, int top_k, int renorm, void* dlogits, int64_t ldd,
+                      void* stream);
+
+/*
+ * moe_sort -- the slots sorted by expert, then by token, then by slot.
+ *   ids      device int32 [T x top_k]; a slot whose id is outside [0, E) (-1
+ *            for one without an expert) gets no row.  T >= 0, top_k >= 1,
+ *            T * top_k < 2^31, 1 <= E <= 1024.
+ *   tok_idx  device int32 [T x top_k]: the token of each row; entries past the
+ *            last row are -1.
+ *   grp_off  device int64 [E + 1]: rows grp_off[e] .. grp_off[e+1] - 1 belong
+ *            to expert e; grp_off[E] is the number of rows.
+ *   pos      device int32 [T x top_k]: the row of each slot, -1 for none.
+ *   ws       device workspace of moe_sort_workspace_size(T, top_k, E) bytes
+ *            (may be NULL when that is 0).
+ * Nothing depends on timing.  T = 0 writes grp_off (zeros) alone.
+ */
+size_t moe_sort_workspace_size(int64_t T, int64_t top_k, int64_t E);
+int moe_sort(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int32_t* tok_idx, int64_t* grp_off, int32_t* pos,
+             void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * nvfp4_gemm_grouped -- nvfp4_gemm of each expert on its rows:
+ *   Y[r] = X[tok_idx[r]] dequant(W_e)^T   for grp_off[e] <= r < grp_off[e+1],
+ * computed as g_e (X Q_e^T) with Q = e2m1 * e4m3 exact in bf16, on the bf16
+ * matrix cores with fp32 accumulation.
+ *
+ *   X        device bf16 [n x ldx], 16-byte aligned, ldx >= k, ldx % 8 == 0.
+ *   tok_idx  device int32 [rows], or NULL: row r of X itself (rows <= n).  A
+ *            row whose token is outside [0, n) is multiplied as zeros.
+ *   rows     capacity of tok_idx and Y (T * top_k); rows from grp_off[G] on
+ *            are neither read nor written.
+ *   grp_off  device int64 [G + 1], non-decreasing, within [0, rows].  (They
+ *            are clamped into that range and never lead outside the buffers;
+ *            decreasing offsets give undefined rows.)
+ *   codes [G x m x k/2] (8-byte aligned), scales [G x m x k/16], g [G]: the
+ *            experts as gptq_nvfp4_quantize_batched writes them.  k % 16 == 0.
+ *            A rejected weight row (scales 0x7F) gives NaN.
+ *   Y        device [rows x ldy] of y_dtype (fp32 or bf16, RNE), ldy >= m.
+ */
+int nvfp4_gemm_grouped(const void* X, int x_dtype, int64_t n, int64_t k, int64_t ldx, const int32_t* tok_idx,
+                       int64_t rows, const int64_t* grp_off, int64_t G, const uint8_t* codes, const uint8_t* scales,
+                       const float* g, int64_t m, void* Y, int y_dtype, int64_t ldy, void* stream);
+
+/*
+ * nvfp4_gemm_grouped_dx -- gradient of nvfp4_gemm_grouped with respect to its
+ * gathered rows (the weights are frozen): dX[r] = dY[r] dequant(W_e), computed
+ * as g_e (dY Q_e) in the same arithmetic.  The tokens' gradient is the sum over
+ * their rows: moe_combine of dX with no weights.
+ *   dY       device bf16 [rows x lddy], lddy >= m; aligned by its elements.
+ *   dX       device [rows x lddx] of dx_dtype (fp32 or bf16), lddx >= k; rows
+ *            from grp_off[G] on are left as they were.
+ *   The rest as for nvfp4_gemm_grouped.
+ */
+int nvfp4_gemm_grouped_dx(const void* dY, int dy_dtype, int64_t rows, int64_t m, int64_t lddy, const int64_t* grp_off,
+                          int64_t G, const uint8_t* codes, const uint8_t* scales, const float* g, int64_t k, void* dX,
+                          int dx_dtype, int64_t lddx, void* stream);
+
+/*
+ * moe_combine -- each token's rows back: out[t] = sum_s weights[t][s] *
+ * Y[pos[t][s]], summed in fp32 in slot order.
+ *   Y        device [rows x ldy] of y_dtype, d columns.
+ *   pos      device int32 [T x top_k] as moe_sort writes it; a slot whose row
+ *            is outside [0, rows) counts as a row of zeros (so a NaN weight
+ *            still gives NaN).
+ *   weights  device fp32 [T x top_k], or NULL: all 1.
+ *   out      device [T x ldo] of out_dtype (fp32 or bf16, RNE).
+ */
+int moe_combine(const void* Y, int y_dtype, int64_t rows, int64_t d, int64_t ldy, const int32_t* pos,
+                const float* weights, int64_t T, int64_t top_k, void* out, int out_dtype, int64_t ldo, void* stream);
+
+/*
+ * moe_combine_backward -- gradients of moe_combine: dY[pos[t][s]] =
+ * weights[t][s] dout[t], dweights[t][s] = <dout[t], Y[pos[t][s]]> (fp32 sums in
+ * a fixed order; 0 for a slot without a row).
+ *   dout     device [T x ldd] of dout_dtype.
+ *   Y        as given to moe_combine; may be NULL when dweights is.
+ *   pos      no row may be named twice (moe_sort never does).
+ *   weights  may be NULL: all 1.
+ *   dY       device [rows x lddy] of y_dtype, or NULL; rows that no slot names
+ *            are left as they were.
+ *   dweights device fp32 [T x top_k], or NULL (not both).
+ */
+int moe_combine_backward(const void* dout, int dout_dtype, int64_t T, int64_t d, int64_t ldd, const void* Y, int y_dtype,
+                         int64_t rows, int64_t ldy, const int32_t* pos, const float* weights, int64_t top_k, void* dY,
+                         int64_t lddy, float* dweights, void* stream);
+
 /* Text of a status code; never NULL. */
 const char* nvq_status_string(int status);
 /* Reason of the most recent failing call on this thread ("" if none). */

@@ -36,6 +36,8 @@ EXPORTS = [
     "nvfp4_global_scale_workspace_size", "nvfp4_global_scale",
     "gptq_nvfp4_workspace_size", "gptq_nvfp4_quantize", "gptq_nvfp4_quantize_batched",
     "nvfp4_dequantize", "nvfp4_gemm_workspace_size", "nvfp4_gemm", "nvfp4_gemm_noalloc", "nvq_check_finite",
+    "moe_topk", "moe_topk_backward", "moe_sort_workspace_size", "moe_sort",
+    "nvfp4_gemm_grouped", "nvfp4_gemm_grouped_dx", "moe_combine", "moe_combine_backward",
     "nvq_status_string", "nvq_last_error",
 ]
 
@@ -77,6 +79,14 @@ def _load():
         "nvfp4_gemm": (I32, [P, I32, I64, I64, I64, P, P, P, I64, P, I32, I64, P, SZ, P]),
         "nvfp4_gemm_noalloc": (I32, [P, I32, I64, I64, I64, P, P, P, I64, P, I32, I64, P]),
         "nvq_check_finite": (I32, [P, I32, I64, I64, I64, P, P]),
+        "moe_topk": (I32, [P, I32, I64, I64, I64, I32, I32, P, P, P]),
+        "moe_topk_backward": (I32, [P, I32, I64, I64, I64, P, P, P, I32, I32, P, I64, P]),
+        "moe_sort_workspace_size": (SZ, [I64, I64, I64]),
+        "moe_sort": (I32, [P, I64, I64, I64, P, P, P, P, SZ, P]),
+        "nvfp4_gemm_grouped": (I32, [P, I32, I64, I64, I64, P, I64, P, I64, P, P, P, I64, P, I32, I64, P]),
+        "nvfp4_gemm_grouped_dx": (I32, [P, I32, I64, I64, I64, P, I64, P, P, P, I64, P, I32, I64, P]),
+        "moe_combine": (I32, [P, I32, I64, I64, I64, P, P, I64, I64, P, I32, I64, P]),
+        "moe_combine_backward": (I32, [P, I32, I64, I64, I64, P, I32, I64, I64, P, P, I64, P, I64, P, P]),
         "nvq_status_string": (ctypes.c_char_p, [I32]),
         "nvq_last_error": (ctypes.c_char_p, []),
     }
@@ -384,3 +394,198 @@ def quantize_layer(W, X, n_cand=16, damp_rel=0.01, flags=0, chol=False):
     res = gptq_nvfp4_quantize(W, U, H, g, n_cand, flags)
     res.update(H=H, U=U, lam=lam, info=info, g=g)
     return res
+
+
+# ---- mixture of experts -------------------------------------------------------
+# moe_topk -> moe_sort -> nvfp4_gemm_grouped -> moe_combine, with the gradients
+# of all but the sort.  Tensors of one call must share a device; the work runs
+# on that device's current stream.
+
+_F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8
+_CODES = {_F32: NVQ_DTYPE_F32, _BF16: NVQ_DTYPE_BF16}
+
+
+def _want(t, name, dtypes, shape, dev=None):
+    """t is a tensor on a HIP device (dev, if given) of one of dtypes and of that shape (None: any size), rows of unit
+    stride and whole rows apart (dense but for the row stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a tensor on a HIP device")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, not one of {dtypes}")
+    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+
+
+def _dense(t, name, dtypes, shape, dev=None):
+    """_want of a contiguous tensor."""
+    _want(t, name, dtypes, shape, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _matrix(t, name, dtypes, shape, dev=None):
+    """_want of a 2-D tensor with unit column stride; returns its row stride."""
+    _want(t, name, dtypes, shape, dev)
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return ld
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, dev, *args):
+    """The library call on dev's current stream, with dev current."""
+    f = getattr(lib, name)
+    if dev.index == torch.cuda.current_device():
+        status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != 0:
+        raise NvqError(name, status, lib.nvq_last_error().decode())
+
+
+def moe_topk(logits, top_k, renorm=True):
+    """The router: (ids int32 [T, top_k], weights fp32 [T, top_k]) of logits [T, E] (bf16 or fp32), each token's largest
+    logits in falling order (ties: the lower expert) and their softmax weights, over the chosen experts (renorm) or all.
+    -inf masks an expert; a slot with no expert left has id -1 and weight 0, a row with a NaN or +inf ids -1 and NaN."""
+    ld = _matrix(logits, "logits", (_F32, _BF16), (None, None))
+    T, E = logits.shape
+    dev = logits.device
+    top_k = int(top_k)
+    ids = torch.empty(T, max(0, top_k), dtype=_I32, device=dev)
+    weights = torch.empty(T, max(0, top_k), dtype=_F32, device=dev)
+    _call("moe_topk", dev, logits.data_ptr(), _CODES[logits.dtype], T, E, ld, top_k, bool(renorm), ids.data_ptr(),
+          weights.data_ptr())
+    return ids, weights
+
+
+def moe_topk_backward(logits, ids, weights, dweights, renorm=True):
+    """Gradient of moe_topk's weights with respect to the logits: [T, E] in the logits' dtype."""
+    ld = _matrix(logits, "logits", (_F32, _BF16), (None, None))
+    T, E = logits.shape
+    dev = logits.device
+    _dense(ids, "ids", (_I32,), (T, None), dev)
+    K = ids.shape[1]
+    _dense(weights, "weights", (_F32,), (T, K), dev)
+    _dense(dweights, "dweights", (_F32,), (T, K), dev)
+    out = torch.empty(T, E, dtype=logits.dtype, device=dev)
+    _call("moe_topk_backward", dev, logits.data_ptr(), _CODES[logits.dtype], T, E, ld, ids.data_ptr(),
+          weights.data_ptr(), dweights.data_ptr(), K, bool(renorm), out.data_ptr(), E)
+    return out
+
+
+def moe_sort(ids, n_experts):
+    """Slots sorted by expert: (tok_idx int32 [T*K], grp_off int64 [E+1], pos int32 [T, K]) of ids int32 [T, K].  Row r of
+    expert e (grp_off[e] <= r < grp_off[e+1]) is token tok_idx[r]; slot (t, s) is row pos[t, s].  Slots whose id is
+    outside [0, n_experts) have pos -1, and tok_idx past the last row is -1.  (hessian_accumulate_grouped takes tok_idx
+    and grp_off.tolist().)"""
+    _dense(ids, "ids", (_I32,), (None, None))
+    T, K = ids.shape
+    E = int(n_experts)
+    dev = ids.device
+    tok_idx = torch.empty(T * K, dtype=_I32, device=dev)
+    grp_off = torch.empty(max(0, E) + 1, dtype=_I64, device=dev)
+    pos = torch.empty(T, K, dtype=_I32, device=dev)
+    need = lib.moe_sort_workspace_size(T, K, E)
+    ws = _workspace(need, dev)
+    _call("moe_sort", dev, ids.data_ptr(), T, K, E, tok_idx.data_ptr(), grp_off.data_ptr(), pos.data_ptr(), _addr(ws),
+          need)
+    return tok_idx, grp_off, pos
+
+
+def _experts(codes, scales, g, grp_off, dev):
+    """(G, m, k) of the experts' tensors, checked."""
+    _dense(codes, "codes", (_U8,), (None, None, None), dev)
+    G, m, kh = codes.shape
+    _dense(scales, "scales", (_U8,), (G, m, kh // 8), dev)
+    _dense(g, "g", (_F32,), (G,), dev)
+    _dense(grp_off, "grp_off", (_I64,), (G + 1,), dev)
+    return G, m, 2 * kh
+
+
+def nvfp4_gemm_grouped(X, codes, scales, g, grp_off, tok_idx=None, out_dtype=torch.float32, Y=None):
+    """Y[r] = X[tok_idx[r]] dequant(W_e)^T for the rows r of each expert e (grp_off[e] <= r < grp_off[e+1]).
+
+    X: [n, k] bf16; codes [G, m, k/2], scales [G, m, k/16], g [G] as gptq_nvfp4_quantize_batched gives them; grp_off and
+    tok_idx from moe_sort (without tok_idx row r of X is row r).  Rows of Y from grp_off[G] on are not written."""
+    ldx = _matrix(X, "X", (_BF16,), (None, None))
+    dev = X.device
+    G, m, k = _experts(codes, scales, g, grp_off, dev)
+    n = X.shape[0]
+    if X.shape[1] != k:
+        raise ValueError(f"X has {X.shape[1]} columns, the experts {k} inputs")
+    rows = n
+    if tok_idx is not None:
+        _dense(tok_idx, "tok_idx", (_I32,), (None,), dev)
+        rows = tok_idx.shape[0]
+    if Y is None:
+        Y = torch.empty(rows, m, dtype=out_dtype, device=dev)
+    ldy = _matrix(Y, "Y", (_F32, _BF16), (rows, m), dev)
+    _call("nvfp4_gemm_grouped", dev, X.data_ptr(), NVQ_DTYPE_BF16, n, k, ldx, _addr(tok_idx), rows, grp_off.data_ptr(), G,
+          codes.data_ptr(), scales.data_ptr(), g.data_ptr(), m, Y.data_ptr(), _CODES[Y.dtype], ldy)
+    return Y
+
+
+def nvfp4_gemm_grouped_dx(dY, codes, scales, g, grp_off, out_dtype=torch.float32, dX=None):
+    """Gradient of nvfp4_gemm_grouped with respect to its rows: dX[r] = dY[r] dequant(W_e), dY [rows, m] bf16.  The tokens'
+    gradient is moe_combine(dX, pos).  Rows from grp_off[G] on are not written."""
+    lddy = _matrix(dY, "dY", (_BF16,), (None, None))
+    dev = dY.device
+    G, m, k = _experts(codes, scales, g, grp_off, dev)
+    rows = dY.shape[0]
+    if dY.shape[1] != m:
+        raise ValueError(f"dY has {dY.shape[1]} columns, the experts {m} outputs")
+    if dX is None:
+        dX = torch.empty(rows, k, dtype=out_dtype, device=dev)
+    lddx = _matrix(dX, "dX", (_F32, _BF16), (rows, k), dev)
+    _call("nvfp4_gemm_grouped_dx", dev, dY.data_ptr(), NVQ_DTYPE_BF16, rows, m, lddy, grp_off.data_ptr(), G,
+          codes.data_ptr(), scales.data_ptr(), g.data_ptr(), k, dX.data_ptr(), _CODES[dX.dtype], lddx)
+    return dX
+
+
+def moe_combine(Y, pos, weights=None, out_dtype=None, out=None):
+    """out[t] = sum_s weights[t, s] * Y[pos[t, s]] (weights None: all 1), Y [rows, d] bf16 or fp32, pos int32 and weights
+    fp32 [T, K].  A pos outside the rows counts as zeros.  out_dtype None: Y's."""
+    ldy = _matrix(Y, "Y", (_F32, _BF16), (None, None))
+    dev = Y.device
+    _dense(pos, "pos", (_I32,), (None, None), dev)
+    T, K = pos.shape
+    if weights is not None:
+        _dense(weights, "weights", (_F32,), (T, K), dev)
+    rows, d = Y.shape
+    if out is None:
+        out = torch.empty(T, d, dtype=out_dtype or Y.dtype, device=dev)
+    ldo = _matrix(out, "out", (_F32, _BF16), (T, d), dev)
+    _call("moe_combine", dev, Y.data_ptr(), _CODES[Y.dtype], rows, d, ldy, pos.data_ptr(), _addr(weights), T, K,
+          out.data_ptr(), _CODES[out.dtype], ldo)
+    return out
+
+
+def moe_combine_backward(dout, Y, pos, weights=None, dY=None):
+    """Gradients of moe_combine: (dY [rows, d] in Y's dtype, dweights fp32 [T, K]).  Rows of dY that no slot of pos names
+    (past moe_sort's last row) are not written; no row may be named twice."""
+    ldd = _matrix(dout, "dout", (_F32, _BF16), (None, None))
+    dev = dout.device
+    T, d = dout.shape
+    ldy = _matrix(Y, "Y", (_F32, _BF16), (None, d), dev)
+    _dense(pos, "pos", (_I32,), (T, None), dev)
+    K = pos.shape[1]
+    if weights is not None:
+        _dense(weights, "weights", (_F32,), (T, K), dev)
+    rows = Y.shape[0]
+    if dY is None:
+        dY = torch.empty(rows, d, dtype=Y.dtype, device=dev)
+    lddy = _matrix(dY, "dY", (Y.dtype,), (rows, d), dev)
+    dw = torch.empty(T, K, dtype=_F32, device=dev)
+    _call("moe_combine_backward", dev, dout.data_ptr(), _CODES[dout.dtype], T, d, ldd, Y.data_ptr(), _CODES[Y.dtype], rows,
+          ldy, pos.data_ptr(), _addr(weights), K, dY.data_ptr(), lddy, dw.data_ptr())
+    return dY, dw

@@ -716,4 +716,168 @@ int nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, const float* g
                     "nvfp4_dequantize");
 }
 
+// ---- mixture of experts: router, sort by expert, experts' products, weighted sum ----
+namespace {
+// [T x top_k] slots of E experts, for the router and its gradient.
+int topk_check(const char* fn, int dtype, int64_t T, int64_t E, int64_t ld, int top_k) {
+  if (!dtype_ok(dtype)) return failp(NVQ_ERR_DTYPE, fn, "dtype %d", dtype);
+  if (T < 0 || T > 0x7FFFFFFF || E < 1 || E > kMoeMaxExperts || ld < E)
+    return failp(NVQ_ERR_SHAPE, fn, "T=%lld E=%lld ld=%lld (need 0<=T<2^31, 1<=E<=%lld, ld>=E)", (long long)T,
+                 (long long)E, (long long)ld, (long long)kMoeMaxExperts);
+  if (top_k < 1 || top_k > E || top_k > kMoeMaxTopK)
+    return failp(NVQ_ERR_VALUE, fn, "top_k=%d (need 1 <= top_k <= min(E, %d))", top_k, kMoeMaxTopK);
+  return NVQ_OK;
+}
+// T top_k, or -1 if it is not a row count that int32 positions can hold.
+int64_t slots(int64_t T, int64_t top_k) {
+  if (T < 0 || top_k < 1 || top_k > 0x7FFFFFFF || T > 0x7FFFFFFF || T * top_k > 0x7FFFFFFF) return -1;
+  return T * top_k;
+}
+// The shared arguments of the experts' products: rows in groups, NVFP4 experts [m x k], one output row per row.
+int experts_check(const char* fn, int64_t rows, const int64_t* grp_off, int64_t G, const uint8_t* codes,
+                  const uint8_t* scales, const float* g, int64_t m, int64_t k, const void* out, int out_dtype,
+                  int64_t ldo, int64_t width) {
+  if (!dtype_ok(out_dtype)) return failp(NVQ_ERR_DTYPE, fn, "output dtype %d", out_dtype);
+  if (rows < 0 || rows > 0x7FFFFFFF || G < 1 || G > 0x7FFFFF || m < 1 || k < 16 || k % 16 != 0 || m > 4000000 ||
+      k > 4000000 || ldo < width)
+    return failp(NVQ_ERR_SHAPE, fn,
+                 "rows=%lld G=%lld m=%lld k=%lld ldo=%lld (need 0<=rows<2^31, 1<=G<2^23, m>0, k>0, k%%16==0, m and k "
+                 "at most 4000000, ldo>=%lld)",
+                 (long long)rows, (long long)G, (long long)m, (long long)k, (long long)ldo, (long long)width);
+  if (rows == 0) return NVQ_OK;
+  if (!grp_off || !codes || !scales || !g || !out)
+    return failp(NVQ_ERR_NULL, fn, "grp_off, codes, scales, g and the output are required");
+  if (!aligned(grp_off, 8) || !aligned(codes, 8) || !aligned(g, 4) || !aligned(out, out_dtype == NVQ_DTYPE_BF16 ? 2 : 4))
+    return failp(NVQ_ERR_ALIGN, fn, "grp_off and codes must be 8-byte aligned, g and the output by their elements");
+  return NVQ_OK;
+}
+size_t elem_size(int dtype) { return dtype == NVQ_DTYPE_BF16 ? 2 : 4; }
+}  // namespace
+
+int moe_topk(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, int top_k, int renorm, int32_t* ids,
+             float* weights, void* stream) {
+  const char* fn = "moe_topk";
+  const int rc = topk_check(fn, dtype, T, E, ld, top_k);
+  if (rc != NVQ_OK || T == 0) return rc;
+  if (!logits || !ids || !weights) return failp(NVQ_ERR_NULL, fn, "logits, ids and weights are required");
+  if (!aligned(logits, elem_size(dtype)) || !aligned(ids, 4) || !aligned(weights, 4))
+    return failp(NVQ_ERR_ALIGN, fn, "logits, ids and weights must be aligned by their elements");
+  return hip_status(moe_topk_launch(logits, dtype == NVQ_DTYPE_BF16, T, E, ld, top_k, renorm != 0, ids, weights,
+                                    (hipStream_t)stream), fn);
+}
+
+int moe_topk_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const int32_t* ids,
+                      const float* weights, const float* dweights, int top_k, int renorm, void* dlogits, int64_t ldd,
+                      void* stream) {
+  const char* fn = "moe_topk_backward";
+  const int rc = topk_check(fn, dtype, T, E, ld, top_k);
+  if (rc != NVQ_OK) return rc;
+  if (ldd < E) return failp(NVQ_ERR_SHAPE, fn, "ldd=%lld (need >= E=%lld)", (long long)ldd, (long long)E);
+  if (T == 0) return NVQ_OK;
+  if (!logits || !ids || !weights || !dweights || !dlogits)
+    return failp(NVQ_ERR_NULL, fn, "logits, ids, weights, dweights and dlogits are required");
+  const size_t es = elem_size(dtype);
+  if (!aligned(logits, es) || !aligned(dlogits, es) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+    return failp(NVQ_ERR_ALIGN, fn, "pointers must be aligned by their elements");
+  return hip_status(moe_topk_backward_launch(logits, dtype == NVQ_DTYPE_BF16, T, E, ld, ids, weights, dweights, top_k,
+                                             renorm != 0, dlogits, ldd, (hipStream_t)stream), fn);
+}
+
+size_t moe_sort_workspace_size(int64_t T, int64_t top_k, int64_t E) {
+  const int64_t n = slots(T, top_k);
+  return n > 0 && E >= 1 && E <= kMoeMaxExperts ? align_up(moe_sort_workspace(n, E)) : 0;
+}
+
+int moe_sort(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int32_t* tok_idx, int64_t* grp_off, int32_t* pos,
+             void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_sort";
+  const int64_t n = slots(T, top_k);
+  if (n < 0 || E < 1 || E > kMoeMaxExperts)
+    return failp(NVQ_ERR_SHAPE, fn, "T=%lld top_k=%lld E=%lld (need T>=0, top_k>0, T*top_k<2^31, 1<=E<=%lld)",
+                 (long long)T, (long long)top_k, (long long)E, (long long)kMoeMaxExperts);
+  if (!grp_off || (n > 0 && (!ids || !tok_idx || !pos)))
+    return failp(NVQ_ERR_NULL, fn, "ids, tok_idx, grp_off and pos are required");
+  if (!aligned(grp_off, 8) || !aligned(ids, 4) || !aligned(tok_idx, 4) || !aligned(pos, 4))
+    return failp(NVQ_ERR_ALIGN, fn, "grp_off must be 8-byte aligned, ids, tok_idx and pos 4-byte");
+  const size_t need = moe_sort_workspace(n, E);
+  if (need && (!ws || ws_bytes < need || !aligned(ws, kAlign)))
+    return failp(NVQ_ERR_WORKSPACE, fn, "workspace needs %zu bytes (256-aligned), got %zu", need, ws_bytes);
+  return hip_status(moe_sort_launch(ids, n, (int)top_k, E, tok_idx, grp_off, pos, ws, (hipStream_t)stream), fn);
+}
+
+int nvfp4_gemm_grouped(const void* X, int x_dtype, int64_t n, int64_t k, int64_t ldx, const int32_t* tok_idx,
+                       int64_t rows, const int64_t* grp_off, int64_t G, const uint8_t* codes, const uint8_t* scales,
+                       const float* g, int64_t m, void* Y, int y_dtype, int64_t ldy, void* stream) {
+  const char* fn = "nvfp4_gemm_grouped";
+  if (x_dtype != NVQ_DTYPE_BF16) return failp(NVQ_ERR_DTYPE, fn, "x_dtype %d (activations must be bf16)", x_dtype);
+  const int rc = experts_check(fn, rows, grp_off, G, codes, scales, g, m, k, Y, y_dtype, ldy, m);
+  if (rc != NVQ_OK) return rc;
+  if (n < 0 || n > 0x7FFFFFFF || ldx < k || ldx % 8 != 0 || (!tok_idx && rows > n) || (rows > 0 && n == 0))
+    return failp(NVQ_ERR_SHAPE, fn,
+                 "n=%lld rows=%lld ldx=%lld k=%lld (need 0<=n<2^31, ldx>=k, ldx%%8==0, rows<=n without tok_idx, and "
+                 "tokens if there are rows)",
+                 (long long)n, (long long)rows, (long long)ldx, (long long)k);
+  if (rows == 0) return NVQ_OK;
+  if (!X) return failp(NVQ_ERR_NULL, fn, "X is NULL");
+  if (!aligned(X, 16)) return failp(NVQ_ERR_ALIGN, fn, "X must be 16-byte aligned");
+  if (!aligned(tok_idx, 4)) return failp(NVQ_ERR_ALIGN, fn, "tok_idx must be 4-byte aligned");
+  return hip_status(nvfp4_gemm_grouped_launch((const uint16_t*)X, n, k, ldx, tok_idx, rows, grp_off, G, codes, scales, g,
+                                              m, Y, y_dtype == NVQ_DTYPE_BF16, ldy, (hipStream_t)stream), fn);
+}
+
+int nvfp4_gemm_grouped_dx(const void* dY, int dy_dtype, int64_t rows, int64_t m, int64_t lddy, const int64_t* grp_off,
+                          int64_t G, const uint8_t* codes, const uint8_t* scales, const float* g, int64_t k, void* dX,
+                          int dx_dtype, int64_t lddx, void* stream) {
+  const char* fn = "nvfp4_gemm_grouped_dx";
+  if (dy_dtype != NVQ_DTYPE_BF16) return failp(NVQ_ERR_DTYPE, fn, "dy_dtype %d (gradients must be bf16)", dy_dtype);
+  const int rc = experts_check(fn, rows, grp_off, G, codes, scales, g, m, k, dX, dx_dtype, lddx, k);
+  if (rc != NVQ_OK) return rc;
+  if (lddy < m) return failp(NVQ_ERR_SHAPE, fn, "lddy=%lld (need >= m=%lld)", (long long)lddy, (long long)m);
+  if (rows == 0) return NVQ_OK;
+  if (!dY) return failp(NVQ_ERR_NULL, fn, "dY is NULL");
+  if (!aligned(dY, 2)) return failp(NVQ_ERR_ALIGN, fn, "dY must be 2-byte aligned");
+  return hip_status(nvfp4_gemm_grouped_dx_launch((const uint16_t*)dY, rows, m, lddy, grp_off, G, codes, scales, g, k, dX,
+                                                 dx_dtype == NVQ_DTYPE_BF16, lddx, (hipStream_t)stream), fn);
+}
+
+int moe_combine(const void* Y, int y_dtype, int64_t rows, int64_t d, int64_t ldy, const int32_t* pos,
+                const float* weights, int64_t T, int64_t top_k, void* out, int out_dtype, int64_t ldo, void* stream) {
+  const char* fn = "moe_combine";
+  if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype)) return failp(NVQ_ERR_DTYPE, fn, "y_dtype %d, out_dtype %d", y_dtype, out_dtype);
+  if (slots(T, top_k) < 0 || rows < 0 || rows > 0x7FFFFFFF || d < 1 || ldy < d || ldo < d)
+    return failp(NVQ_ERR_SHAPE, fn,
+                 "T=%lld top_k=%lld rows=%lld d=%lld ldy=%lld ldo=%lld (need T>=0, top_k>0, T*top_k<2^31, "
+                 "0<=rows<2^31, d>0, ldy>=d, ldo>=d)",
+                 (long long)T, (long long)top_k, (long long)rows, (long long)d, (long long)ldy, (long long)ldo);
+  if (T == 0) return NVQ_OK;
+  if ((rows > 0 && !Y) || !pos || !out) return failp(NVQ_ERR_NULL, fn, "Y, pos and out are required");
+  if (!aligned(Y, elem_size(y_dtype)) || !aligned(out, elem_size(out_dtype)) || !aligned(pos, 4) || !aligned(weights, 4))
+    return failp(NVQ_ERR_ALIGN, fn, "pointers must be aligned by their elements");
+  return hip_status(moe_combine_launch(Y, y_dtype == NVQ_DTYPE_BF16, rows, d, ldy, pos, weights, T, (int)top_k, out,
+                                       out_dtype == NVQ_DTYPE_BF16, ldo, (hipStream_t)stream), fn);
+}
+
+int moe_combine_backward(const void* dout, int dout_dtype, int64_t T, int64_t d, int64_t ldd, const void* Y, int y_dtype,
+                         int64_t rows, int64_t ldy, const int32_t* pos, const float* weights, int64_t top_k, void* dY,
+                         int64_t lddy, float* dweights, void* stream) {
+  const char* fn = "moe_combine_backward";
+  if (!dtype_ok(y_dtype) || !dtype_ok(dout_dtype)) return failp(NVQ_ERR_DTYPE, fn, "dout_dtype %d, y_dtype %d", dout_dtype, y_dtype);
+  if (slots(T, top_k) < 0 || rows < 0 || rows > 0x7FFFFFFF || d < 1 || ldd < d || (dweights && ldy < d) || (dY && lddy < d))
+    return failp(NVQ_ERR_SHAPE, fn,
+                 "T=%lld top_k=%lld rows=%lld d=%lld ldd=%lld ldy=%lld lddy=%lld (need T>=0, top_k>0, T*top_k<2^31, "
+                 "0<=rows<2^31, d>0, leading dimensions >= d)",
+                 (long long)T, (long long)top_k, (long long)rows, (long long)d, (long long)ldd, (long long)ldy,
+                 (long long)lddy);
+  if (!dY && !dweights) return failp(NVQ_ERR_NULL, fn, "dY or dweights is required");
+  if (T == 0) return NVQ_OK;
+  if (!dout || !pos || (rows > 0 && dweights && !Y)) return failp(NVQ_ERR_NULL, fn, "dout and pos are required, and Y for dweights");
+  const size_t es = elem_size(y_dtype);
+  if (!aligned(dout, elem_size(dout_dtype)) || !aligned(Y, es) || !aligned(dY, es) || !aligned(pos, 4) ||
+      !aligned(weights, 4) || !aligned(dweights, 4))
+    return failp(NVQ_ERR_ALIGN, fn, "pointers must be aligned by their elements");
+  return hip_status(moe_combine_backward_launch(dout, dout_dtype == NVQ_DTYPE_BF16, T, d, ldd, Y,
+                                                y_dtype == NVQ_DTYPE_BF16, rows, ldy, pos, weights, (int)top_k, dY, lddy,
+                                                dweights, (hipStream_t)stream), fn);
+}
+
 }  // extern "C"

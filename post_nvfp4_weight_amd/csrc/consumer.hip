@@ -21,6 +21,7 @@
 #include <mutex>
 
 #include "common.h"
+#include "dequant.h"
 #include "kernels.h"
 
 namespace nvq {
@@ -30,33 +31,11 @@ namespace {
 constexpr int CT = 128, CK = 64, CLD = CK + 8;
 constexpr int CBUF = 2 * CT * CLD;   // bf16 elements of one buffer: X tile, then Q tile
 
-typedef float f32x2c __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2c __attribute__((ext_vector_type(2)));
-
-// Byte B of word (two codes, low nibble first) under block scale value s ->
-// packed bf16 pair of e2m1 * s.  The E2M1 decode is the hardware's FP4
-// conversion at scale 1 (its scale operand applies only a power of two, so
-// the E4M3 scale is multiplied in fp32; the product has at most 6
-// significant bits and is exact, as is its bf16 conversion).
 // E4M3 value of code c (0..126) without branches: (m + 8 min(e, 1)) 2^(max(e, 1) - 10)
 // for c = 8 e + m, which is m 2^-9 for e = 0 and (1 + m/8) 2^(e-7) otherwise.
 __device__ __forceinline__ float scale_value(uint32_t c) {
   const uint32_t e = (c >> 3) & 15, m = c & 7;
   return (float)(m + 8 * min(e, 1u)) * __uint_as_float((max(e, 1u) + 117) << 23);
-}
-
-template <int B>
-__device__ __forceinline__ uint32_t dq_byte(uint32_t word, float s) {
-  const f32x2c v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, B);
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2c{v.x * s, v.y * s}, bf16x2c));
-}
-__device__ __forceinline__ uint32_t dq_byte(uint32_t word, float s, int b) {   // b known after unrolling
-  switch (b) {
-    case 0: return dq_byte<0>(word, s);
-    case 1: return dq_byte<1>(word, s);
-    case 2: return dq_byte<2>(word, s);
-    default: return dq_byte<3>(word, s);
-  }
 }
 
 // OUT: 0 fp32 Y, 1 bf16 Y, 2 fp32 partial sums of k-split blockIdx.z (no g)

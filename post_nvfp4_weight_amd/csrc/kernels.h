@@ -184,4 +184,31 @@ hipError_t nvfp4_gemm_launch(const uint16_t* X, int64_t T, int64_t k, int64_t ld
                              const uint8_t* scales, const float* g, int64_t m, void* Y, int out_bf16, int64_t ldy,
                              float* ws, hipStream_t s);
 
+// ---- mixture of experts (arguments checked by the caller; see include/nvq.h) ----
+constexpr int64_t kMoeMaxExperts = 1024;   // of the router and the sort
+constexpr int kMoeMaxTopK = 64;            // of the router (one lane per slot)
+hipError_t moe_topk_launch(const void* logits, int bf16, int64_t T, int64_t E, int64_t ld, int K, int renorm,
+                           int32_t* ids, float* weights, hipStream_t s);
+hipError_t moe_topk_backward_launch(const void* logits, int bf16, int64_t T, int64_t E, int64_t ld, const int32_t* ids,
+                                    const float* weights, const float* dweights, int K, int renorm, void* dlogits,
+                                    int64_t ldd, hipStream_t s);
+// n = T K assignments.
+size_t moe_sort_workspace(int64_t n, int64_t E);
+hipError_t moe_sort_launch(const int32_t* ids, int64_t n, int K, int64_t E, int32_t* tok_idx, int64_t* grp_off,
+                           int32_t* pos, void* ws, hipStream_t s);
+hipError_t moe_combine_launch(const void* Y, int y_bf16, int64_t rows, int64_t d, int64_t ldy, const int32_t* pos,
+                              const float* weights, int64_t T, int K, void* out, int out_bf16, int64_t ldo,
+                              hipStream_t s);
+hipError_t moe_combine_backward_launch(const void* dout, int dout_bf16, int64_t T, int64_t d, int64_t ldd, const void* Y,
+                                       int y_bf16, int64_t rows, int64_t ldy, const int32_t* pos, const float* weights,
+                                       int K, void* dY, int64_t lddy, float* dw, hipStream_t s);
+hipError_t nvfp4_gemm_grouped_launch(const uint16_t* X, int64_t n, int64_t k, int64_t ldx, const int32_t* tok_idx,
+                                     int64_t rows, const int64_t* grp_off, int64_t G, const uint8_t* codes,
+                                     const uint8_t* scales, const float* g, int64_t m, void* Y, int out_bf16,
+                                     int64_t ldy, hipStream_t s);
+hipError_t nvfp4_gemm_grouped_dx_launch(const uint16_t* dY, int64_t rows, int64_t m, int64_t lddy,
+                                        const int64_t* grp_off, int64_t G, const uint8_t* codes, const uint8_t* scales,
+                                        const float* g, int64_t k, void* dX, int out_bf16, int64_t lddx,
+                                        hipStream_t s);
+
 }  // namespace nvq
