@@ -402,53 +402,58 @@ def quantize_layer(W, X, n_cand=16, damp_rel=0.01, flags=0, chol=False):
 # on that device's current stream.
 
 _F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8
+_FLOATS = (_F32, _BF16)
 _CODES = {_F32: NVQ_DTYPE_F32, _BF16: NVQ_DTYPE_BF16}
 
 
-def _want(t, name, dtypes, shape, dev=None):
-    """t is a tensor on a HIP device (dev, if given) of one of dtypes and of that shape (None: any size), rows of unit
-    stride and whole rows apart (dense but for the row stride)."""
+def _want(t, name, dtypes, shape, dev):
+    """Raises unless t is a tensor on HIP device number dev (None: any) of one of dtypes and of that shape (None: any size)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a tensor on a HIP device")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, not one of {dtypes}")
     if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
 
 
-def _dense(t, name, dtypes, shape, dev=None):
-    """_want of a contiguous tensor."""
-    _want(t, name, dtypes, shape, dev)
-    if not t.is_contiguous():
+def _dense(t, name, dtype, shape, dev):
+    """t must be a contiguous tensor of that dtype and shape on device number dev."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        _want(t, name, (dtype,), shape, dev)
         raise ValueError(f"{name} must be contiguous")
 
 
-def _matrix(t, name, dtypes, shape, dev=None):
-    """_want of a 2-D tensor with unit column stride; returns its row stride."""
+def _matrix(t, name, dtypes, shape, dev):
+    """t must be a 2-D tensor of unit column stride (_want's checks); returns its row stride."""
     _want(t, name, dtypes, shape, dev)
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
         raise ValueError(f"{name} must have unit column stride")
-    ld = t.stride(0) if rows > 1 else cols
-    if ld < cols:
+    if rows <= 1:
+        return cols
+    if s0 < cols:
         raise ValueError(f"{name} must not have overlapping rows")
-    return ld
+    return s0
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(name, dev, *args):
-    """The library call on dev's current stream, with dev current."""
-    f = getattr(lib, name)
-    if dev.index == torch.cuda.current_device():
-        status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(f, name, dev, *args):
+    """The library call on the current stream of device number dev, with that device current."""
+    if dev == torch.cuda.current_device():
+        status = f(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = f(*args, _raw_stream(dev))
     if status != 0:
         raise NvqError(name, status, lib.nvq_last_error().decode())
 
@@ -457,28 +462,28 @@ def moe_topk(logits, top_k, renorm=True):
     """The router: (ids int32 [T, top_k], weights fp32 [T, top_k]) of logits [T, E] (bf16 or fp32), each token's largest
     logits in falling order (ties: the lower expert) and their softmax weights, over the chosen experts (renorm) or all.
     -inf masks an expert; a slot with no expert left has id -1 and weight 0, a row with a NaN or +inf ids -1 and NaN."""
-    ld = _matrix(logits, "logits", (_F32, _BF16), (None, None))
+    ld = _matrix(logits, "logits", _FLOATS, (None, None), None)
     T, E = logits.shape
-    dev = logits.device
     top_k = int(top_k)
-    ids = torch.empty(T, max(0, top_k), dtype=_I32, device=dev)
-    weights = torch.empty(T, max(0, top_k), dtype=_F32, device=dev)
-    _call("moe_topk", dev, logits.data_ptr(), _CODES[logits.dtype], T, E, ld, top_k, bool(renorm), ids.data_ptr(),
+    ids = logits.new_empty((T, max(0, top_k)), dtype=_I32)
+    weights = logits.new_empty((T, max(0, top_k)), dtype=_F32)
+    _call(lib.moe_topk, "moe_topk", logits.get_device(), logits.data_ptr(), _CODES[logits.dtype], T, E, ld, top_k, bool(renorm), ids.data_ptr(),
           weights.data_ptr())
     return ids, weights
 
 
 def moe_topk_backward(logits, ids, weights, dweights, renorm=True):
     """Gradient of moe_topk's weights with respect to the logits: [T, E] in the logits' dtype."""
-    ld = _matrix(logits, "logits", (_F32, _BF16), (None, None))
+    ld = _matrix(logits, "logits", _FLOATS, (None, None), None)
     T, E = logits.shape
-    dev = logits.device
-    _dense(ids, "ids", (_I32,), (T, None), dev)
+    dev = logits.get_device()
+    _want(ids, "ids", (_I32,), (T, None), dev)
     K = ids.shape[1]
-    _dense(weights, "weights", (_F32,), (T, K), dev)
-    _dense(dweights, "dweights", (_F32,), (T, K), dev)
-    out = torch.empty(T, E, dtype=logits.dtype, device=dev)
-    _call("moe_topk_backward", dev, logits.data_ptr(), _CODES[logits.dtype], T, E, ld, ids.data_ptr(),
+    _dense(ids, "ids", _I32, (T, K), dev)
+    _dense(weights, "weights", _F32, (T, K), dev)
+    _dense(dweights, "dweights", _F32, (T, K), dev)
+    out = logits.new_empty((T, E))
+    _call(lib.moe_topk_backward, "moe_topk_backward", dev, logits.data_ptr(), _CODES[logits.dtype], T, E, ld, ids.data_ptr(),
           weights.data_ptr(), dweights.data_ptr(), K, bool(renorm), out.data_ptr(), E)
     return out
 
@@ -488,27 +493,29 @@ def moe_sort(ids, n_experts):
     expert e (grp_off[e] <= r < grp_off[e+1]) is token tok_idx[r]; slot (t, s) is row pos[t, s].  Slots whose id is
     outside [0, n_experts) have pos -1, and tok_idx past the last row is -1.  (hessian_accumulate_grouped takes tok_idx
     and grp_off.tolist().)"""
-    _dense(ids, "ids", (_I32,), (None, None))
+    _want(ids, "ids", (_I32,), (None, None), None)
     T, K = ids.shape
     E = int(n_experts)
-    dev = ids.device
-    tok_idx = torch.empty(T * K, dtype=_I32, device=dev)
-    grp_off = torch.empty(max(0, E) + 1, dtype=_I64, device=dev)
-    pos = torch.empty(T, K, dtype=_I32, device=dev)
+    dev = ids.get_device()
+    _dense(ids, "ids", _I32, (T, K), dev)
+    tok_idx = ids.new_empty(T * K)
+    grp_off = ids.new_empty(max(0, E) + 1, dtype=_I64)
+    pos = ids.new_empty((T, K))
     need = lib.moe_sort_workspace_size(T, K, E)
-    ws = _workspace(need, dev)
-    _call("moe_sort", dev, ids.data_ptr(), T, K, E, tok_idx.data_ptr(), grp_off.data_ptr(), pos.data_ptr(), _addr(ws),
+    ws = _workspace(need, ids.device)
+    _call(lib.moe_sort, "moe_sort", dev, ids.data_ptr(), T, K, E, tok_idx.data_ptr(), grp_off.data_ptr(), pos.data_ptr(), _addr(ws),
           need)
     return tok_idx, grp_off, pos
 
 
 def _experts(codes, scales, g, grp_off, dev):
     """(G, m, k) of the experts' tensors, checked."""
-    _dense(codes, "codes", (_U8,), (None, None, None), dev)
+    _want(codes, "codes", (_U8,), (None, None, None), dev)
     G, m, kh = codes.shape
-    _dense(scales, "scales", (_U8,), (G, m, kh // 8), dev)
-    _dense(g, "g", (_F32,), (G,), dev)
-    _dense(grp_off, "grp_off", (_I64,), (G + 1,), dev)
+    _dense(codes, "codes", _U8, (G, m, kh), dev)
+    _dense(scales, "scales", _U8, (G, m, kh // 8), dev)
+    _dense(g, "g", _F32, (G,), dev)
+    _dense(grp_off, "grp_off", _I64, (G + 1,), dev)
     return G, m, 2 * kh
 
 
@@ -517,20 +524,21 @@ def nvfp4_gemm_grouped(X, codes, scales, g, grp_off, tok_idx=None, out_dtype=tor
 
     X: [n, k] bf16; codes [G, m, k/2], scales [G, m, k/16], g [G] as gptq_nvfp4_quantize_batched gives them; grp_off and
     tok_idx from moe_sort (without tok_idx row r of X is row r).  Rows of Y from grp_off[G] on are not written."""
-    ldx = _matrix(X, "X", (_BF16,), (None, None))
-    dev = X.device
+    ldx = _matrix(X, "X", (_BF16,), (None, None), None)
+    dev = X.get_device()
     G, m, k = _experts(codes, scales, g, grp_off, dev)
     n = X.shape[0]
     if X.shape[1] != k:
         raise ValueError(f"X has {X.shape[1]} columns, the experts {k} inputs")
     rows = n
     if tok_idx is not None:
-        _dense(tok_idx, "tok_idx", (_I32,), (None,), dev)
+        _want(tok_idx, "tok_idx", (_I32,), (None,), dev)
         rows = tok_idx.shape[0]
+        _dense(tok_idx, "tok_idx", _I32, (rows,), dev)
     if Y is None:
-        Y = torch.empty(rows, m, dtype=out_dtype, device=dev)
-    ldy = _matrix(Y, "Y", (_F32, _BF16), (rows, m), dev)
-    _call("nvfp4_gemm_grouped", dev, X.data_ptr(), NVQ_DTYPE_BF16, n, k, ldx, _addr(tok_idx), rows, grp_off.data_ptr(), G,
+        Y = X.new_empty((rows, m), dtype=out_dtype)
+    ldy = _matrix(Y, "Y", _FLOATS, (rows, m), dev)
+    _call(lib.nvfp4_gemm_grouped, "nvfp4_gemm_grouped", dev, X.data_ptr(), NVQ_DTYPE_BF16, n, k, ldx, _addr(tok_idx), rows, grp_off.data_ptr(), G,
           codes.data_ptr(), scales.data_ptr(), g.data_ptr(), m, Y.data_ptr(), _CODES[Y.dtype], ldy)
     return Y
 
@@ -538,16 +546,16 @@ def nvfp4_gemm_grouped(X, codes, scales, g, grp_off, tok_idx=None, out_dtype=tor
 def nvfp4_gemm_grouped_dx(dY, codes, scales, g, grp_off, out_dtype=torch.float32, dX=None):
     """Gradient of nvfp4_gemm_grouped with respect to its rows: dX[r] = dY[r] dequant(W_e), dY [rows, m] bf16.  The tokens'
     gradient is moe_combine(dX, pos).  Rows from grp_off[G] on are not written."""
-    lddy = _matrix(dY, "dY", (_BF16,), (None, None))
-    dev = dY.device
+    lddy = _matrix(dY, "dY", (_BF16,), (None, None), None)
+    dev = dY.get_device()
     G, m, k = _experts(codes, scales, g, grp_off, dev)
     rows = dY.shape[0]
     if dY.shape[1] != m:
         raise ValueError(f"dY has {dY.shape[1]} columns, the experts {m} outputs")
     if dX is None:
-        dX = torch.empty(rows, k, dtype=out_dtype, device=dev)
-    lddx = _matrix(dX, "dX", (_F32, _BF16), (rows, k), dev)
-    _call("nvfp4_gemm_grouped_dx", dev, dY.data_ptr(), NVQ_DTYPE_BF16, rows, m, lddy, grp_off.data_ptr(), G,
+        dX = dY.new_empty((rows, k), dtype=out_dtype)
+    lddx = _matrix(dX, "dX", _FLOATS, (rows, k), dev)
+    _call(lib.nvfp4_gemm_grouped_dx, "nvfp4_gemm_grouped_dx", dev, dY.data_ptr(), NVQ_DTYPE_BF16, rows, m, lddy, grp_off.data_ptr(), G,
           codes.data_ptr(), scales.data_ptr(), g.data_ptr(), k, dX.data_ptr(), _CODES[dX.dtype], lddx)
     return dX
 
@@ -555,17 +563,18 @@ def nvfp4_gemm_grouped_dx(dY, codes, scales, g, grp_off, out_dtype=torch.float32
 def moe_combine(Y, pos, weights=None, out_dtype=None, out=None):
     """out[t] = sum_s weights[t, s] * Y[pos[t, s]] (weights None: all 1), Y [rows, d] bf16 or fp32, pos int32 and weights
     fp32 [T, K].  A pos outside the rows counts as zeros.  out_dtype None: Y's."""
-    ldy = _matrix(Y, "Y", (_F32, _BF16), (None, None))
-    dev = Y.device
-    _dense(pos, "pos", (_I32,), (None, None), dev)
+    ldy = _matrix(Y, "Y", _FLOATS, (None, None), None)
+    dev = Y.get_device()
+    _want(pos, "pos", (_I32,), (None, None), dev)
     T, K = pos.shape
+    _dense(pos, "pos", _I32, (T, K), dev)
     if weights is not None:
-        _dense(weights, "weights", (_F32,), (T, K), dev)
+        _dense(weights, "weights", _F32, (T, K), dev)
     rows, d = Y.shape
     if out is None:
-        out = torch.empty(T, d, dtype=out_dtype or Y.dtype, device=dev)
-    ldo = _matrix(out, "out", (_F32, _BF16), (T, d), dev)
-    _call("moe_combine", dev, Y.data_ptr(), _CODES[Y.dtype], rows, d, ldy, pos.data_ptr(), _addr(weights), T, K,
+        out = Y.new_empty((T, d), dtype=out_dtype or Y.dtype)
+    ldo = _matrix(out, "out", _FLOATS, (T, d), dev)
+    _call(lib.moe_combine, "moe_combine", dev, Y.data_ptr(), _CODES[Y.dtype], rows, d, ldy, pos.data_ptr(), _addr(weights), T, K,
           out.data_ptr(), _CODES[out.dtype], ldo)
     return out
 
@@ -573,19 +582,20 @@ def moe_combine(Y, pos, weights=None, out_dtype=None, out=None):
 def moe_combine_backward(dout, Y, pos, weights=None, dY=None):
     """Gradients of moe_combine: (dY [rows, d] in Y's dtype, dweights fp32 [T, K]).  Rows of dY that no slot of pos names
     (past moe_sort's last row) are not written; no row may be named twice."""
-    ldd = _matrix(dout, "dout", (_F32, _BF16), (None, None))
-    dev = dout.device
+    ldd = _matrix(dout, "dout", _FLOATS, (None, None), None)
+    dev = dout.get_device()
     T, d = dout.shape
-    ldy = _matrix(Y, "Y", (_F32, _BF16), (None, d), dev)
-    _dense(pos, "pos", (_I32,), (T, None), dev)
+    ldy = _matrix(Y, "Y", _FLOATS, (None, d), dev)
+    _want(pos, "pos", (_I32,), (T, None), dev)
     K = pos.shape[1]
+    _dense(pos, "pos", _I32, (T, K), dev)
     if weights is not None:
-        _dense(weights, "weights", (_F32,), (T, K), dev)
+        _dense(weights, "weights", _F32, (T, K), dev)
     rows = Y.shape[0]
     if dY is None:
-        dY = torch.empty(rows, d, dtype=Y.dtype, device=dev)
+        dY = Y.new_empty((rows, d))
     lddy = _matrix(dY, "dY", (Y.dtype,), (rows, d), dev)
-    dw = torch.empty(T, K, dtype=_F32, device=dev)
-    _call("moe_combine_backward", dev, dout.data_ptr(), _CODES[dout.dtype], T, d, ldd, Y.data_ptr(), _CODES[Y.dtype], rows,
+    dw = dout.new_empty((T, K), dtype=_F32)
+    _call(lib.moe_combine_backward, "moe_combine_backward", dev, dout.data_ptr(), _CODES[dout.dtype], T, d, ldd, Y.data_ptr(), _CODES[Y.dtype], rows,
           ldy, pos.data_ptr(), _addr(weights), K, dY.data_ptr(), lddy, dw.data_ptr())
     return dY, dw

@@ -18,148 +18,241 @@ __device__ __forceinline__ void store_f(uint16_t* p, float v) {
   *p = __builtin_bit_cast(uint16_t, b);
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+// Reductions over LPT = 16 (a DPP row) or 64 lanes, the result in every lane:
+// rotations inside a row, then the row and half swaps.  All are vector
+// instructions; the LDS-unit shuffles that __shfl_xor compiles to took the
+// 256-expert router (65536 tokens) 56 us, this form with 16 lanes per token TOPK_US.
+template <int N>
+__device__ __forceinline__ uint32_t ror16(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, false);
+}
+template <int LPT, typename F>
+__device__ __forceinline__ uint32_t group_reduce(uint32_t v, F f) {
+  v = f(v, ror16<8>(v));
+  v = f(v, ror16<4>(v));
+  v = f(v, ror16<2>(v));
+  v = f(v, ror16<1>(v));
+  if (LPT == 64) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = f(r[0], r[1]);
+    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = f(h[0], h[1]);
+  }
   return v;
 }
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+template <int LPT>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  return group_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int LPT>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  return group_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+template <int LPT>
+__device__ __forceinline__ float group_sum(float v) {
+  return __uint_as_float(group_reduce<LPT>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+template <int LPT>
+__device__ __forceinline__ bool group_any(bool x) {
+  const uint64_t all = __ballot(x);
+  if (LPT == 64) return all != 0;
+  return (all >> (threadIdx.x & 48)) & 0xFFFF;
 }
 
 // ---- router -------------------------------------------------------------------
-// One wave per token; lane l holds the EPL consecutive logits from l * EPL, so
-// the lowest index among equal logits is in the lowest lane.  Each of the K
-// rounds takes the wave's largest remaining logit, then the lowest lane and
-// the lowest element of it that holds that value.  A -inf logit is never
-// chosen; a row with a NaN or +inf is rejected.  Weights are a softmax with
-// the row's largest logit subtracted, sums in fp32.
-template <typename L, int EPL>
+// Elements of a token's row in LPT lanes of EPL: vectors of VW consecutive
+// elements (16 bytes at most), one per lane, then the next LPT vectors.
+template <typename L, int LPT, int EPL>
+struct RowLayout {
+  static constexpr int kMost = 16 / (int)sizeof(L);
+  static constexpr int VW = EPL < kMost ? EPL : kMost;
+  static __device__ __forceinline__ int index(int lane, int i) { return (i / VW) * (LPT * VW) + lane * VW + i % VW; }
+};
+// The lane's elements as fp32, -inf past E.  VEC: whole vectors (E and the row
+// stride multiples of VW, rows aligned to them).
+template <typename L, int LPT, int EPL, bool VEC>
+__device__ __forceinline__ void load_row(const L* row, int E, int lane, float (&v)[EPL]) {
+  using R = RowLayout<L, LPT, EPL>;
+#pragma unroll
+  for (int c = 0; c < EPL / R::VW; ++c) {
+    const int e0 = R::index(lane, c * R::VW);
+    if (VEC) {
+      struct alignas(sizeof(L) * R::VW) Vec { L x[R::VW]; };
+      Vec x = {};
+      if (e0 < E) x = *(const Vec*)(row + e0);
+#pragma unroll
+      for (int i = 0; i < R::VW; ++i) v[c * R::VW + i] = e0 < E ? load_f(&x.x[i]) : -__builtin_inff();
+    } else {
+#pragma unroll
+      for (int i = 0; i < R::VW; ++i) v[c * R::VW + i] = e0 + i < E ? load_f(row + e0 + i) : -__builtin_inff();
+    }
+  }
+}
+
+// LPT lanes per token.  Logits become unsigned keys in the same order (-0 as
+// +0); a bf16 key keeps 16 bits of value and holds 65535 - index below them,
+// so that the largest key is the largest logit of the lowest index, and one
+// maximum a round finds both.  An fp32 round takes the largest key, then the
+// lowest index that holds it.  A chosen element's key becomes 0.  A -inf logit is
+// never chosen (no key above that of -inf is left); a row with a NaN or +inf
+// is rejected.  Weights are a softmax with the row's largest logit
+// subtracted, sums in fp32.
+// What bounds it: 65536 tokens of 256 bf16 logits are 38 MB, 7 us at the copy
+// rate; the rounds' vector instructions cost about twice that.  One token
+// per wave (LPT 64) has a quarter of the elements per lane and a shorter
+// chain, for few tokens, many experts or more than 16 slots.
+constexpr uint32_t kNegInfKey = 0x007FFFFFu;   // ~bits of -inf
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);   // -0 + 0 = +0
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+// Of a packed bf16 key: the low 16 bits of the value are 0 again.
+template <bool PACKED>
+__device__ __forceinline__ float logit_of(uint32_t k) {
+  return PACKED ? __uint_as_float(__float_as_uint(key_value(k)) & 0xFFFF0000u) : key_value(k);
+}
+
+template <typename L, int LPT, int EPL, bool VEC>
 __global__ __launch_bounds__(256) void topk_kernel(const L* __restrict__ logits, int64_t T, int E, int64_t ld, int K,
                                                    int renorm, int32_t* __restrict__ ids,
                                                    float* __restrict__ weights) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= T) return;
-  const float ninf = -__builtin_inff();
-  const L* row = logits + t * ld;
-  float v[EPL];
+  using R = RowLayout<L, LPT, EPL>;
+  constexpr bool kPacked = sizeof(L) == 2;
+  const int lane = threadIdx.x % LPT;
+  const int64_t t = (int64_t)blockIdx.x * (256 / LPT) + threadIdx.x / LPT;
+  const int64_t row = t < T ? t : T - 1;   // lanes without a token repeat the last one and write nothing
+  uint32_t key[EPL];
+  float rest = 0.0f;   // sum over all experts
+  uint32_t best;
   bool bad = false;
+  {
+    float v[EPL];
+    load_row<L, LPT, EPL, VEC>(logits + row * ld, E, lane, v);
+    uint32_t own = 0;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane * EPL + i;
-    v[i] = e < E ? load_f(row + e) : ninf;
-    bad |= !(v[i] < __builtin_inff());
-  }
-  if (__ballot(bad)) {
-    if (lane < K) {
-      ids[t * K + lane] = -1;
-      weights[t * K + lane] = __builtin_nanf("");
+    for (int i = 0; i < EPL; ++i) {
+      bad |= !(v[i] < __builtin_inff());
+      key[i] = order_key(v[i]);
+      if (kPacked) key[i] = (key[i] & 0xFFFF0000u) | (0xFFFFu - (uint32_t)R::index(lane, i));
+      own = max(own, key[i]);
     }
-    return;
-  }
-  float own = ninf;   // largest of the lane's remaining logits
+    bad = group_any<LPT>(bad);
+    best = group_max<LPT>(own);
+    if (!renorm) {
+      const float top = logit_of<kPacked>(best);
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) own = fmaxf(own, v[i]);
-  float top = 0.0f, total = 0.0f, myval = ninf;
+      for (int i = 0; i < EPL; ++i) rest += expf(v[i] - top);
+      rest = group_sum<LPT>(rest);
+    }
+  }
+  const uint32_t none = kPacked ? kNegInfKey | 0xFFFFu : kNegInfKey;   // keys up to this are -inf
+  const float top = logit_of<kPacked>(best);
+  float myval = -__builtin_inff();
   int myid = -1;
   for (int s = 0; s < K; ++s) {
-    const float best = wave_max(own);
-    if (s == 0) {
-      top = best == ninf ? 0.0f : best;
-      if (!renorm) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) total += expf(v[i] - top);
-        total = wave_sum(total);
-      }
-    }
-    if (best == ninf) break;
-    const int src = __ffsll((unsigned long long)__ballot(own == best)) - 1;
-    int at = 0;
-#pragma unroll
-    for (int i = EPL - 1; i >= 0; --i) at = v[i] == best ? i : at;
-    const int id = __shfl(lane * EPL + at, src);
-    if (lane == src) {
-      own = ninf;
+    // (a group with nothing left or a rejected row goes on with the wave and takes nothing)
+    const bool take = best > none && !bad;
+    uint32_t id, own = 0;
+    if (kPacked) {
+      id = 0xFFFFu - (best & 0xFFFFu);
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        v[i] = i == at ? ninf : v[i];
-        own = fmaxf(own, v[i]);
+        key[i] = key[i] == best ? 0u : key[i];
+        own = max(own, key[i]);
+      }
+    } else {
+      uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = EPL - 1; i >= 0; --i) at = key[i] == best ? (uint32_t)R::index(0, i) : at;
+      at += at != 0xFFFFFFFFu ? lane * R::VW : 0;
+      id = group_min<LPT>(at);
+      const int gone = at == id ? (int)id - lane * R::VW : -1;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        key[i] = R::index(0, i) == gone ? 0u : key[i];
+        own = max(own, key[i]);
       }
     }
-    if (lane == s) {
-      myval = best;
-      myid = id;
+    if (lane == s && take) {
+      myval = logit_of<kPacked>(best);
+      myid = (int)id;
     }
+    best = group_max<LPT>(own);
   }
-  const float ex = expf(myval - top);   // 0 for a slot that no expert filled
-  if (renorm) total = wave_sum(ex);
-  if (lane < K) {
+  const float ex = myid >= 0 ? expf(myval - top) : 0.0f;
+  const float total = renorm ? group_sum<LPT>(ex) : rest;
+  if (lane < K && t < T) {
     ids[t * K + lane] = myid;
-    weights[t * K + lane] = myid >= 0 ? ex / total : 0.0f;
+    weights[t * K + lane] = bad ? __builtin_nanf("") : myid >= 0 ? ex / total : 0.0f;
   }
 }
 
 // Gradient of the router: with c = sum_s dw_s w_s, d logit_j is
-// p_j (sum of dw_s over the slots with id j - c), p_j the softmax over all
-// experts, or with renorm the same over the chosen experts only (w_s in the
-// place of p_j).  One wave per token, lanes as in topk_kernel.
-template <typename L, int EPL>
+// p_j (dw of the slot with id j, if there is one, - c), p_j the softmax over
+// all experts, or with renorm the same over the chosen experts only (w_s in
+// the place of p_j).  LPT lanes per token as in topk_kernel; the slots' terms
+// reach their experts' lanes through a row of LDS.
+template <typename L, int LPT, int EPL, bool VEC>
 __global__ __launch_bounds__(256) void topk_backward_kernel(const L* __restrict__ logits, int64_t T, int E, int64_t ld,
                                                             const int32_t* __restrict__ ids,
                                                             const float* __restrict__ weights,
                                                             const float* __restrict__ dweights, int K, int renorm,
                                                             L* __restrict__ dlogits, int64_t ldd) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= T) return;
+  using R = RowLayout<L, LPT, EPL>;
+  __shared__ __attribute__((aligned(16))) float term[256 / LPT][LPT * EPL];
+  const int lane = threadIdx.x % LPT;
+  const int64_t t = (int64_t)blockIdx.x * (256 / LPT) + threadIdx.x / LPT;
+  if (t >= T) return;   // whole groups; nothing below crosses them
+  float* mine = term[threadIdx.x / LPT];
   const int myid = lane < K ? ids[t * K + lane] : -1;
   const float myw = lane < K ? weights[t * K + lane] : 0.0f;
   const float mydw = lane < K ? dweights[t * K + lane] : 0.0f;
-  // a rejected row (ids -1) has NaN weights, and so a NaN gradient; an empty one has none
+  // a rejected row (ids -1) has NaN weights, and so a NaN gradient; an empty slot has none
   const bool taken = myid >= 0 && myid < E;
-  const float c = wave_sum(lane < K && (taken || !(myw == 0.0f)) ? mydw * myw : 0.0f);
-  float p[EPL], d[EPL];
+  const float c = group_sum<LPT>(taken || myw != 0.0f ? mydw * myw : 0.0f);
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) d[i] = 0.0f;
-  if (renorm) {
+  for (int i = 0; i < EPL; ++i) mine[i * LPT + lane] = 0.0f;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // a group is part of one wave, whose LDS operations run in order
+  if (taken) mine[myid] = renorm ? myw * (mydw - c) : mydw;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  float p[EPL], total = 0.0f, top = 0.0f;
+  if (!renorm) {
+    load_row<L, LPT, EPL, VEC>(logits + t * ld, E, lane, p);
+    uint32_t own = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) p[i] = c != c ? c : 0.0f;
-  } else {
-    float top = -__builtin_inff(), total = 0.0f;
-    const L* row = logits + t * ld;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane * EPL + i;
-      p[i] = e < E ? load_f(row + e) : -__builtin_inff();
-      top = fmaxf(top, p[i]);
-    }
-    top = wave_max(top);
+    for (int i = 0; i < EPL; ++i) own = max(own, order_key(p[i]));   // (a NaN comes out as NaN, or meets one in c)
+    top = key_value(group_max<LPT>(own));
     top = top == -__builtin_inff() ? 0.0f : top;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) total += p[i] = expf(p[i] - top);
-    total = wave_sum(total);
-    const float r = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) p[i] *= r;
-  }
-  for (int s = 0; s < K; ++s) {
-    const int id = __shfl(myid, s);
-    const float w = __shfl(myw, s), dw = __shfl(mydw, s);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (id == lane * EPL + i) {
-        if (renorm) d[i] += w * (dw - c);
-        else d[i] += dw;
-      }
+    total = group_sum<LPT>(total);
+    total = total == 0.0f ? 1.0f : total;
   }
   L* out = dlogits + t * ldd;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane * EPL + i;
-    if (e < E) store_f(out + e, renorm ? d[i] + p[i] : p[i] * (d[i] - c));
+  for (int v = 0; v < EPL / R::VW; ++v) {
+    const int e0 = R::index(lane, v * R::VW);
+    float r[R::VW];
+#pragma unroll
+    for (int i = 0; i < R::VW; ++i) {
+      const float d = mine[e0 + i];
+      r[i] = renorm ? (c != c ? c : d) : p[v * R::VW + i] / total * (d - c);
+    }
+    if (VEC) {
+      struct alignas(sizeof(L) * R::VW) Vec { L x[R::VW]; } x;
+#pragma unroll
+      for (int i = 0; i < R::VW; ++i) store_f(&x.x[i], r[i]);
+      if (e0 < E) *(Vec*)(out + e0) = x;
+    } else {
+#pragma unroll
+      for (int i = 0; i < R::VW; ++i)
+        if (e0 + i < E) store_f(out + e0 + i, r[i]);
+    }
   }
 }
 
@@ -169,7 +262,7 @@ __global__ __launch_bounds__(256) void topk_backward_kernel(const L* __restrict_
 // take consecutive chunks of SORT_CHUNK assignments, the waves of a block
 // consecutive parts of its chunk; ranks inside 64 assignments come from ballots
 // over the bits of the expert number, so nothing depends on timing.
-constexpr int SORT_T = 1024, SORT_W = SORT_T / 64, SORT_CHUNK = 4096;
+constexpr int SORT_T = 1024, SORT_W = SORT_T / 64, SORT_CHUNK = 8192;
 
 // LDS counts cnt[w][e] of wave w's part [b, e) of the assignments.
 __device__ __forceinline__ void sort_count(const int32_t* ids, int64_t beg, int64_t end, int E, int* cnt) {
@@ -205,8 +298,22 @@ __device__ __forceinline__ int block_exclusive(int v, int* part, int* total) {
   return before + x - v;
 }
 
+// i / K for 0 <= i < 2^31 as a multiplication: with s = ceil(log2 K) and
+// mul = ceil(2^(31 + s) / K), i mul / 2^(31 + s) exceeds i / K by less than
+// i / 2^(31 + s) < 1 / K, which never reaches the next whole number.
+struct DivK {
+  uint32_t mul, shift;
+};
+DivK div_by(uint32_t k) {
+  DivK d{0, 31};
+  while (((uint64_t)1 << (d.shift - 31)) < k) ++d.shift;
+  d.mul = (uint32_t)((((uint64_t)1 << d.shift) + k - 1) / k);
+  return d;
+}
+__device__ __forceinline__ int32_t div_k(int64_t i, DivK d) { return (int32_t)(((uint64_t)i * d.mul) >> d.shift); }
+
 // cnt[w][e] holds the row of wave w's next assignment of expert e.
-__device__ __forceinline__ void sort_place(const int32_t* ids, int64_t beg, int64_t end, int K, int E, int* cnt,
+__device__ __forceinline__ void sort_place(const int32_t* ids, int64_t beg, int64_t end, DivK K, int E, int* cnt,
                                            int32_t* tok_idx, int32_t* pos) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   int bits = 1;
@@ -232,7 +339,7 @@ __device__ __forceinline__ void sort_place(const int32_t* ids, int64_t beg, int6
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (i < end) {
       pos[i] = row;
-      if (ok) tok_idx[row] = (int32_t)(i / K);
+      if (ok) tok_idx[row] = div_k(i, K);
     }
   }
 }
@@ -246,7 +353,7 @@ __device__ __forceinline__ void wave_part(int64_t beg, int64_t end, int64_t* b, 
 }
 
 // Few assignments: one workgroup does it all.
-__global__ __launch_bounds__(SORT_T) void sort_small_kernel(const int32_t* __restrict__ ids, int64_t n, int K, int E,
+__global__ __launch_bounds__(SORT_T) void sort_small_kernel(const int32_t* __restrict__ ids, int64_t n, DivK K, int E,
                                                             int32_t* __restrict__ tok_idx, int64_t* __restrict__ grp_off,
                                                             int32_t* __restrict__ pos) {
   extern __shared__ int cnt[];   // SORT_W * E
@@ -289,17 +396,26 @@ __global__ __launch_bounds__(SORT_T) void sort_hist_kernel(const int32_t* __rest
 }
 
 // ... their exclusive sums over the chunks in place, and each expert's total
-// (64 experts per workgroup, each wave a range of chunks) ...
+// (64 experts per workgroup, each wave a range of chunks, SCAN_U counts in
+// flight at once) ...
+constexpr int SCAN_U = 16;
 __global__ __launch_bounds__(SORT_T) void sort_scan_kernel(int32_t* __restrict__ hist, int nb, int E,
                                                            int32_t* __restrict__ total) {
   __shared__ int sum[SORT_W][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e = blockIdx.x * 64 + lane;
   const int per = (nb + SORT_W - 1) / SORT_W;
-  const int b0 = std::min(nb, wave * per), b1 = std::min(nb, b0 + per);
-  int s = 0;
-  if (e < E)
-    for (int b = b0; b < b1; ++b) s += hist[(int64_t)b * E + e];
+  const int b0 = min(nb, wave * per), b1 = min(nb, b0 + per);
+  int c[SCAN_U], s = 0;
+  auto load = [&](int b) {
+#pragma unroll
+    for (int u = 0; u < SCAN_U; ++u) c[u] = e < E && b + u < b1 ? hist[(int64_t)(b + u) * E + e] : 0;
+  };
+  for (int b = b0; b < b1; b += SCAN_U) {
+    load(b);
+#pragma unroll
+    for (int u = 0; u < SCAN_U; ++u) s += c[u];
+  }
   sum[wave][lane] = s;
   __syncthreads();
   int run = 0, all = 0;
@@ -308,16 +424,20 @@ __global__ __launch_bounds__(SORT_T) void sort_scan_kernel(int32_t* __restrict__
     all += sum[w][lane];
   }
   if (e >= E) return;
-  for (int b = b0; b < b1; ++b) {
-    const int c = hist[(int64_t)b * E + e];
-    hist[(int64_t)b * E + e] = run;
-    run += c;
+  for (int b = b0; b < b1; b += SCAN_U) {
+    if (per > SCAN_U) load(b);   // else c still holds them
+#pragma unroll
+    for (int u = 0; u < SCAN_U; ++u)
+      if (b + u < b1) {
+        hist[(int64_t)(b + u) * E + e] = run;
+        run += c[u];
+      }
   }
   if (wave == 0) total[e] = all;
 }
 
 // ... and the rows.
-__global__ __launch_bounds__(SORT_T) void sort_place_kernel(const int32_t* __restrict__ ids, int64_t n, int K, int E,
+__global__ __launch_bounds__(SORT_T) void sort_place_kernel(const int32_t* __restrict__ ids, int64_t n, DivK K, int E,
                                                             const int32_t* __restrict__ hist,
                                                             const int32_t* __restrict__ total,
                                                             int32_t* __restrict__ tok_idx,
@@ -348,75 +468,177 @@ __global__ __launch_bounds__(SORT_T) void sort_place_kernel(const int32_t* __res
 }
 
 // ---- a token's experts summed ------------------------------------------------------
-template <typename Y, typename O>
-__global__ __launch_bounds__(256) void combine_kernel(const Y* __restrict__ y, int64_t rows, int64_t d, int64_t ldy,
-                                                      const int32_t* __restrict__ pos, const float* __restrict__ w,
-                                                      int64_t T, int K, O* __restrict__ out, int64_t ldo) {
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x)
-    for (int64_t c = threadIdx.x; c < d; c += 256) {
-      float s = 0.0f;
-      for (int j = 0; j < K; ++j) {
-        const int64_t r = pos[t * K + j];
-        const float v = (uint64_t)r < (uint64_t)rows ? load_f(y + r * ldy + c) : 0.0f;
-        s = fmaf(w ? w[t * K + j] : 1.0f, v, s);
-      }
-      store_f(out + t * ldo + c, s);
-    }
+// Elements move in vectors of VW (16 bytes of the wider type when rows and
+// strides allow it, else one).
+template <typename E, int VW>
+struct alignas(sizeof(E) * VW) VecOf { E x[VW]; };
+template <typename E, int VW>
+__device__ __forceinline__ void load_vec(const E* p, float (&v)[VW]) {
+  const VecOf<E, VW> x = *(const VecOf<E, VW>*)p;
+#pragma unroll
+  for (int i = 0; i < VW; ++i) v[i] = load_f(&x.x[i]);
+}
+template <typename E, int VW>
+__device__ __forceinline__ void store_vec(E* p, const float (&v)[VW]) {
+  VecOf<E, VW> x;
+#pragma unroll
+  for (int i = 0; i < VW; ++i) store_f(&x.x[i], v[i]);
+  *(VecOf<E, VW>*)p = x;
 }
 
-template <typename G, typename Y>
-__global__ __launch_bounds__(256) void combine_backward_kernel(const G* __restrict__ dout, int64_t T, int64_t d,
-                                                               int64_t ldd, const Y* __restrict__ y, int64_t rows,
-                                                               int64_t ldy, const int32_t* __restrict__ pos,
-                                                               const float* __restrict__ w, int K, Y* __restrict__ dy,
-                                                               int64_t lddy, float* __restrict__ dw) {
-  __shared__ float part[4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t i = blockIdx.x; i < T * K; i += gridDim.x) {
-    const int64_t t = i / K, r = pos[i];
-    const bool ok = (uint64_t)r < (uint64_t)rows;
-    const float wt = w ? w[i] : 1.0f;
-    float s = 0.0f;
-    if (ok)
-      for (int64_t c = threadIdx.x; c < d; c += 256) {
-        const float g = load_f(dout + t * ldd + c);
-        if (dw) s = fmaf(g, load_f(y + r * ldy + c), s);
-        if (dy) store_f(dy + r * lddy + c, wt * g);
-      }
-    if (dw) {
-      s = wave_sum(s);
-      if (lane == 0) part[wave] = s;
-      __syncthreads();
-      if (threadIdx.x == 0) dw[i] = part[0] + part[1] + part[2] + part[3];
-      __syncthreads();
+// One thread per vector of a token's columns: blockDim = (columns, tokens).
+// KC slots' loads are in flight together; sums run in slot order.  Bound by
+// reading the rows once: COMBINE_NOTE
+constexpr int KC = 8;
+template <typename Y, typename O, int VW>
+__global__ __launch_bounds__(256) void combine_kernel(const Y* __restrict__ y, int64_t rows, int64_t nv, int64_t ldy,
+                                                      const int32_t* __restrict__ pos, const float* __restrict__ w,
+                                                      int64_t T, int K, O* __restrict__ out, int64_t ldo,
+                                                      int col_blocks) {
+  const int64_t v = (int64_t)(blockIdx.x % col_blocks) * blockDim.x + threadIdx.x;
+  const int64_t t = (int64_t)(blockIdx.x / col_blocks) * blockDim.y +
+                    __builtin_amdgcn_readfirstlane(threadIdx.y);   // the same in a whole wave: blockDim.x is 64 or more
+  if (v >= nv || t >= T) return;
+  const int64_t c = v * VW;
+  float sum[VW];
+#pragma unroll
+  for (int i = 0; i < VW; ++i) sum[i] = 0.0f;
+  for (int s0 = 0; s0 < K; s0 += KC) {
+    float wt[KC], x[KC][VW];
+#pragma unroll
+    for (int j = 0; j < KC; ++j) {
+      const int64_t i = t * K + s0 + j;
+      const int64_t r = s0 + j < K ? pos[i] : -1;
+      wt[j] = s0 + j < K ? (w ? w[i] : 1.0f) : 0.0f;
+#pragma unroll
+      for (int q = 0; q < VW; ++q) x[j][q] = 0.0f;
+      if ((uint64_t)r < (uint64_t)rows) load_vec<Y, VW>(y + r * ldy + c, x[j]);
     }
+#pragma unroll
+    for (int j = 0; j < KC; ++j)
+#pragma unroll
+      for (int q = 0; q < VW; ++q) sum[q] = fmaf(wt[j], x[j][q], sum[q]);
   }
+  store_vec<O, VW>(out + t * ldo + c, sum);
+}
+
+// Its gradients: a workgroup of NW waves per token, dout's row read once for
+// KC slots at a time; each lane sums its columns' products, then lanes and
+// waves are added in a fixed order.
+template <typename G, typename Y, int VW, int NW>
+__global__ __launch_bounds__(64 * NW) void combine_backward_kernel(const G* __restrict__ dout, int64_t T, int64_t nv,
+                                                                   int64_t ldd, const Y* __restrict__ y, int64_t rows,
+                                                                   int64_t ldy, const int32_t* __restrict__ pos,
+                                                                   const float* __restrict__ w, int K,
+                                                                   Y* __restrict__ dy, int64_t lddy,
+                                                                   float* __restrict__ dw) {
+  __shared__ float part[NW][KC];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x;
+  for (int s0 = 0; s0 < K; s0 += KC) {
+    int64_t r[KC];
+    float wt[KC], dot[KC];
+#pragma unroll
+    for (int j = 0; j < KC; ++j) {
+      const int64_t i = t * K + s0 + j;
+      r[j] = s0 + j < K ? pos[i] : -1;
+      if ((uint64_t)r[j] >= (uint64_t)rows) r[j] = -1;
+      wt[j] = s0 + j < K ? (w ? w[i] : 1.0f) : 0.0f;
+      dot[j] = 0.0f;
+    }
+    for (int64_t v = threadIdx.x; v < nv; v += 64 * NW) {
+      const int64_t c = v * VW;
+      float g[VW], x[KC][VW];
+      load_vec<G, VW>(dout + t * ldd + c, g);
+      if (dw) {
+#pragma unroll
+        for (int j = 0; j < KC; ++j) {
+#pragma unroll
+          for (int q = 0; q < VW; ++q) x[j][q] = 0.0f;
+          if (r[j] >= 0) load_vec<Y, VW>(y + r[j] * ldy + c, x[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+          if (r[j] >= 0) {
+#pragma unroll
+            for (int q = 0; q < VW; ++q) dot[j] = fmaf(g[q], x[j][q], dot[j]);
+          }
+      }
+      if (dy)
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+          if (r[j] >= 0) {
+            float o[VW];
+#pragma unroll
+            for (int q = 0; q < VW; ++q) o[q] = wt[j] * g[q];
+            store_vec<Y, VW>(dy + r[j] * lddy + c, o);
+          }
+    }
+    if (!dw) continue;
+#pragma unroll
+    for (int j = 0; j < KC; ++j) {
+      const float d = group_sum<64>(dot[j]);
+      if (lane == 0) part[wave][j] = d;
+    }
+    __syncthreads();
+    if (threadIdx.x < KC && s0 + (int)threadIdx.x < K) {
+      float d = 0.0f;
+#pragma unroll
+      for (int x = 0; x < NW; ++x) d += part[x][threadIdx.x];
+      dw[t * K + s0 + threadIdx.x] = d;
+    }
+    __syncthreads();
+  }
+}
+
+// Calls f(LPT, EPL, VEC) with the constants for E experts in rows whose start
+// and stride are multiples of `unit` elements: 16 lanes per token when there
+// are tokens enough to fill the device that way, at most 256 experts and 16 slots.
+constexpr int64_t kTopkWaves = 8192;   // tokens from which 16 lanes per token are taken
+template <typename L, typename F>
+hipError_t topk_dispatch(int64_t T, int E, int K, uintptr_t addr, int64_t ld, F f) {
+  const bool row16 = T >= kTopkWaves && E <= 256 && K <= 16;
+  const int lanes = row16 ? 16 : 64;
+  int epl = 1;
+  while (epl * lanes < E) epl *= 2;
+  const int vw = std::min<int>(epl, 16 / (int)sizeof(L));
+  const bool vec = E % vw == 0 && ld % vw == 0 && addr % (vw * sizeof(L)) == 0;
+#define NVQ_TOPK_CASE(LPT, EPL) \
+  if (lanes == LPT && epl == EPL) return vec ? f.template operator()<LPT, EPL, true>() : f.template operator()<LPT, EPL, false>()
+  NVQ_TOPK_CASE(16, 1);
+  NVQ_TOPK_CASE(16, 2);
+  NVQ_TOPK_CASE(16, 4);
+  NVQ_TOPK_CASE(16, 8);
+  NVQ_TOPK_CASE(16, 16);
+  NVQ_TOPK_CASE(64, 1);
+  NVQ_TOPK_CASE(64, 2);
+  NVQ_TOPK_CASE(64, 4);
+  NVQ_TOPK_CASE(64, 8);
+  NVQ_TOPK_CASE(64, 16);
+#undef NVQ_TOPK_CASE
+  return hipErrorInvalidValue;
 }
 
 template <typename L>
 hipError_t topk_run(const L* logits, int64_t T, int E, int64_t ld, int K, int renorm, int32_t* ids, float* weights,
                     hipStream_t s) {
-  const dim3 grid((unsigned)((T + 3) / 4)), block(256);
-  const int epl = (E + 63) / 64;
-  if (epl <= 1) hipLaunchKernelGGL((topk_kernel<L, 1>), grid, block, 0, s, logits, T, E, ld, K, renorm, ids, weights);
-  else if (epl <= 2) hipLaunchKernelGGL((topk_kernel<L, 2>), grid, block, 0, s, logits, T, E, ld, K, renorm, ids, weights);
-  else if (epl <= 4) hipLaunchKernelGGL((topk_kernel<L, 4>), grid, block, 0, s, logits, T, E, ld, K, renorm, ids, weights);
-  else if (epl <= 8) hipLaunchKernelGGL((topk_kernel<L, 8>), grid, block, 0, s, logits, T, E, ld, K, renorm, ids, weights);
-  else hipLaunchKernelGGL((topk_kernel<L, 16>), grid, block, 0, s, logits, T, E, ld, K, renorm, ids, weights);
-  return hipGetLastError();
+  return topk_dispatch<L>(T, E, K, (uintptr_t)logits, ld, [&]<int LPT, int EPL, bool VEC>() {
+    const int64_t per = 256 / LPT;
+    hipLaunchKernelGGL((topk_kernel<L, LPT, EPL, VEC>), dim3((unsigned)((T + per - 1) / per)), dim3(256), 0, s, logits,
+                       T, E, ld, K, renorm, ids, weights);
+    return hipGetLastError();
+  });
 }
 
 template <typename L>
 hipError_t topk_backward_run(const L* logits, int64_t T, int E, int64_t ld, const int32_t* ids, const float* w,
                              const float* dw, int K, int renorm, L* dl, int64_t ldd, hipStream_t s) {
-  const dim3 grid((unsigned)((T + 3) / 4)), block(256);
-  const int epl = (E + 63) / 64;
-  if (epl <= 1) hipLaunchKernelGGL((topk_backward_kernel<L, 1>), grid, block, 0, s, logits, T, E, ld, ids, w, dw, K, renorm, dl, ldd);
-  else if (epl <= 2) hipLaunchKernelGGL((topk_backward_kernel<L, 2>), grid, block, 0, s, logits, T, E, ld, ids, w, dw, K, renorm, dl, ldd);
-  else if (epl <= 4) hipLaunchKernelGGL((topk_backward_kernel<L, 4>), grid, block, 0, s, logits, T, E, ld, ids, w, dw, K, renorm, dl, ldd);
-  else if (epl <= 8) hipLaunchKernelGGL((topk_backward_kernel<L, 8>), grid, block, 0, s, logits, T, E, ld, ids, w, dw, K, renorm, dl, ldd);
-  else hipLaunchKernelGGL((topk_backward_kernel<L, 16>), grid, block, 0, s, logits, T, E, ld, ids, w, dw, K, renorm, dl, ldd);
-  return hipGetLastError();
+  return topk_dispatch<L>(T, E, K, (uintptr_t)logits | (uintptr_t)dl, ld | ldd, [&]<int LPT, int EPL, bool VEC>() {
+    const int64_t per = 256 / LPT;
+    hipLaunchKernelGGL((topk_backward_kernel<L, LPT, EPL, VEC>), dim3((unsigned)((T + per - 1) / per)), dim3(256), 0, s,
+                       logits, T, E, ld, ids, w, dw, K, renorm, dl, ldd);
+    return hipGetLastError();
+  });
 }
 
 int64_t sort_blocks(int64_t n) { return (n + SORT_CHUNK - 1) / SORT_CHUNK; }
@@ -447,7 +669,7 @@ hipError_t moe_sort_launch(const int32_t* ids, int64_t n, int K, int64_t E, int3
                            int32_t* pos, void* ws, hipStream_t s) {
   const size_t lds = (size_t)SORT_W * E * sizeof(int);
   if (n <= kSortSmall) {
-    hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(SORT_T), lds, s, ids, n, K, (int)E, tok_idx, grp_off, pos);
+    hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(SORT_T), lds, s, ids, n, div_by(K), (int)E, tok_idx, grp_off, pos);
     return hipGetLastError();
   }
   const int nb = (int)sort_blocks(n);
@@ -455,45 +677,81 @@ hipError_t moe_sort_launch(const int32_t* ids, int64_t n, int K, int64_t E, int3
   int32_t* total = hist + (int64_t)nb * E;
   hipLaunchKernelGGL(sort_hist_kernel, dim3(nb), dim3(SORT_T), E * sizeof(int), s, ids, n, (int)E, hist);
   hipLaunchKernelGGL(sort_scan_kernel, dim3((unsigned)((E + 63) / 64)), dim3(SORT_T), 0, s, hist, nb, (int)E, total);
-  hipLaunchKernelGGL(sort_place_kernel, dim3(nb), dim3(SORT_T), lds, s, ids, n, K, (int)E, hist, total, tok_idx, grp_off,
-                     pos);
+  hipLaunchKernelGGL(sort_place_kernel, dim3(nb), dim3(SORT_T), lds, s, ids, n, div_by(K), (int)E, hist, total, tok_idx,
+                     grp_off, pos);
   return hipGetLastError();
+}
+
+// Elements per vector: 16 bytes of the wider type if every row starts on a
+// multiple of it and the columns are whole vectors, else 1.
+static int vec_width(bool bf16_only, int64_t d, int64_t strides, uintptr_t bf16_addr, uintptr_t f32_addr) {
+  const int vw = bf16_only ? 8 : 4;
+  return d % vw == 0 && strides % vw == 0 && bf16_addr % (2 * vw) == 0 && f32_addr % (4 * vw) == 0 ? vw : 1;
 }
 
 hipError_t moe_combine_launch(const void* Y, int y_bf16, int64_t rows, int64_t d, int64_t ldy, const int32_t* pos,
                               const float* weights, int64_t T, int K, void* out, int out_bf16, int64_t ldo,
                               hipStream_t s) {
-  const dim3 grid((unsigned)std::min<int64_t>(T, 1 << 20)), block(256);
-#define NVQ_COMBINE(YT, OT)                                                                                    \
-  hipLaunchKernelGGL((combine_kernel<YT, OT>), grid, block, 0, s, (const YT*)Y, rows, d, ldy, pos, weights, T, K, \
-                     (OT*)out, ldo)
-  if (y_bf16) {
-    if (out_bf16) NVQ_COMBINE(uint16_t, uint16_t);
-    else NVQ_COMBINE(uint16_t, float);
+  const int vw = vec_width(y_bf16 && out_bf16, d, ldy | ldo, (y_bf16 ? (uintptr_t)Y : 0) | (out_bf16 ? (uintptr_t)out : 0),
+                           (y_bf16 ? 0 : (uintptr_t)Y) | (out_bf16 ? 0 : (uintptr_t)out));
+  const int64_t nv = d / vw;
+  int bx = 64;   // columns of a workgroup; at least a wave, so that a wave's slots are uniform
+  while (bx < 256 && bx < nv) bx *= 2;
+  const int by = 256 / bx;
+  const int64_t cb = (nv + bx - 1) / bx, blocks = cb * ((T + by - 1) / by);
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)blocks), block(bx, by);
+#define NVQ_COMBINE(YT, OT, VW)                                                                                    \
+  hipLaunchKernelGGL((combine_kernel<YT, OT, VW>), grid, block, 0, s, (const YT*)Y, rows, nv, ldy, pos, weights, T, K, \
+                     (OT*)out, ldo, (int)cb)
+  if (y_bf16 && out_bf16) {
+    if (vw > 1) NVQ_COMBINE(uint16_t, uint16_t, 8);
+    else NVQ_COMBINE(uint16_t, uint16_t, 1);
+  } else if (y_bf16) {
+    if (vw > 1) NVQ_COMBINE(uint16_t, float, 4);
+    else NVQ_COMBINE(uint16_t, float, 1);
+  } else if (out_bf16) {
+    if (vw > 1) NVQ_COMBINE(float, uint16_t, 4);
+    else NVQ_COMBINE(float, uint16_t, 1);
   } else {
-    if (out_bf16) NVQ_COMBINE(float, uint16_t);
-    else NVQ_COMBINE(float, float);
+    if (vw > 1) NVQ_COMBINE(float, float, 4);
+    else NVQ_COMBINE(float, float, 1);
   }
 #undef NVQ_COMBINE
+  return hipGetLastError();
+}
+
+template <typename G, typename Y, int VW>
+static hipError_t combine_backward_run(const G* dout, int64_t T, int64_t nv, int64_t ldd, const Y* y, int64_t rows,
+                                       int64_t ldy, const int32_t* pos, const float* w, int K, Y* dy, int64_t lddy,
+                                       float* dw, hipStream_t s) {
+#define NVQ_COMBINE_BWD(NW)                                                                                         \
+  hipLaunchKernelGGL((combine_backward_kernel<G, Y, VW, NW>), dim3((unsigned)T), dim3(64 * NW), 0, s, dout, T, nv, ldd, \
+                     y, rows, ldy, pos, w, K, dy, lddy, dw)
+  // one wave per token once the tokens fill the device; more for few tokens with long rows
+  if (T >= 4096 || nv <= 64) NVQ_COMBINE_BWD(1);
+  else if (T >= 512 || nv <= 256) NVQ_COMBINE_BWD(4);
+  else NVQ_COMBINE_BWD(16);
+#undef NVQ_COMBINE_BWD
   return hipGetLastError();
 }
 
 hipError_t moe_combine_backward_launch(const void* dout, int dout_bf16, int64_t T, int64_t d, int64_t ldd, const void* Y,
                                        int y_bf16, int64_t rows, int64_t ldy, const int32_t* pos, const float* weights,
                                        int K, void* dY, int64_t lddy, float* dw, hipStream_t s) {
-  const dim3 grid((unsigned)std::min<int64_t>(T * K, 1 << 20)), block(256);
-#define NVQ_COMBINE_BWD(GT, YT)                                                                                  \
-  hipLaunchKernelGGL((combine_backward_kernel<GT, YT>), grid, block, 0, s, (const GT*)dout, T, d, ldd, (const YT*)Y, \
-                     rows, ldy, pos, weights, K, (YT*)dY, lddy, dw)
-  if (dout_bf16) {
-    if (y_bf16) NVQ_COMBINE_BWD(uint16_t, uint16_t);
-    else NVQ_COMBINE_BWD(uint16_t, float);
-  } else {
-    if (y_bf16) NVQ_COMBINE_BWD(float, uint16_t);
-    else NVQ_COMBINE_BWD(float, float);
-  }
-#undef NVQ_COMBINE_BWD
-  return hipGetLastError();
+  const uintptr_t ya = (uintptr_t)Y | (uintptr_t)dY;
+  const int vw = vec_width(dout_bf16 && y_bf16, d, ldd | (Y ? ldy : 0) | (dY ? lddy : 0),
+                           (dout_bf16 ? (uintptr_t)dout : 0) | (y_bf16 ? ya : 0),
+                           (dout_bf16 ? 0 : (uintptr_t)dout) | (y_bf16 ? 0 : ya));
+  const int64_t nv = d / vw;
+#define NVQ_RUN(GT, YT, VW)                                                                                            \
+  combine_backward_run<GT, YT, VW>((const GT*)dout, T, nv, ldd, (const YT*)Y, rows, ldy, pos, weights, K, (YT*)dY, lddy, \
+                                   dw, s)
+  if (dout_bf16 && y_bf16) return vw > 1 ? NVQ_RUN(uint16_t, uint16_t, 8) : NVQ_RUN(uint16_t, uint16_t, 1);
+  if (dout_bf16) return vw > 1 ? NVQ_RUN(uint16_t, float, 4) : NVQ_RUN(uint16_t, float, 1);
+  if (y_bf16) return vw > 1 ? NVQ_RUN(float, uint16_t, 4) : NVQ_RUN(float, uint16_t, 1);
+  return vw > 1 ? NVQ_RUN(float, float, 4) : NVQ_RUN(float, float, 1);
+#undef NVQ_RUN
 }
 
 }  // namespace nvq
