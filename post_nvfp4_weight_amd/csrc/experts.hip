@@ -7,7 +7,6 @@
 // most row tiles that any offsets can give, and each workgroup finds its
 // expert from them.
 #include <algorithm>
-#include <cstdlib>
 
 #include "common.h"
 #include "dequant.h"
@@ -33,12 +32,12 @@ struct RowTile {
 // workgroup, false if there is none.  The tiles are dealt to the 8 XCDs
 // (blockIdx.x mod 8) in contiguous runs, so that the tiles that share an
 // expert's weights or a row tile's activations share an L2.  Called by a whole
-// workgroup of NT threads.
+// workgroup of NT threads with 512 bytes of LDS.
 template <int NT>
 __device__ __forceinline__ bool find_tile(const int64_t* off, int64_t G, int64_t rows, int bt, int64_t ncol,
-                                          RowTile* out) {
-  __shared__ int64_t wsum[NT / 64];
-  __shared__ RowTile found;
+                                          char* lds, RowTile* out) {
+  int64_t* wsum = (int64_t*)lds;             // NT / 64
+  RowTile& found = *(RowTile*)(lds + 256);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t b = 0, e = 0, first = 0, cnt = 0;
   // Tiles of experts x0 + thread, and the sum over all of this turn's.
@@ -84,6 +83,7 @@ __device__ __forceinline__ bool find_tile(const int64_t* off, int64_t G, int64_t
   __syncthreads();
   *out = found;
   out->col = id - tile * ncol;
+  __syncthreads();   // lds is free again
   return true;
 }
 
@@ -105,16 +105,16 @@ __device__ __forceinline__ constexpr int waitcnt_vm_lgkm0(int n) { return (n & 1
 //   ahead into a ring of three buffers, 16-byte pieces swizzled by
 //   (row / 2) % 8: the 16 rows that are read at once then touch all 64 banks.
 //   Codes: 128 k at a time (a chunk, two steps), 64 bytes per channel, copied
-//   to LDS of the wave's own two chunks ahead, pieces swizzled by
+//   to LDS of the wave's own, a ring of CR chunks, pieces swizzled by
 //   (channel / 4) % 4 for the same reason.  (Loaded to registers instead, 32
 //   bytes per channel and load, they took the address unit twice the cycles.)
 //   Scales: 8 bytes per channel and chunk to registers, one chunk ahead.
-template <int NW, int RF, int CF>
+template <int NW, int RF, int CF, int CR>
 struct Tile {
   static constexpr int kRows = 32 * RF, kCols = 32 * CF * NW;
   static constexpr int kXBuf = kRows * 128, kCBuf = CF * 32 * 64;   // bytes of one buffer (of a wave's codes)
   static constexpr int kXLoads = 4 * RF / NW, kCLoads = 2 * CF;     // copies per step, per chunk
-  static constexpr int kLds = 3 * kXBuf + 3 * NW * kCBuf;
+  static constexpr int kLds = 3 * kXBuf + CR * NW * kCBuf;
   static_assert(4 * RF % NW == 0, "whole copies per wave");
 };
 
@@ -152,38 +152,40 @@ __device__ __forceinline__ void copy_lds(char* __restrict__ dst, const void* src
 }
 
 // What a wave's steps share.
-template <int NW, int RF, int CF>
+template <int NW, int RF, int CF, int CR>
 struct Wave {
-  uint32_t xoff[Tile<NW, RF, CF>::kXLoads];   // its copies' byte offsets from X
-  uint32_t coff[Tile<NW, RF, CF>::kCLoads];   // and from its codes
+  uint32_t xoff[Tile<NW, RF, CF, CR>::kXLoads];   // its copies' byte offsets from X
+  uint32_t coff[Tile<NW, RF, CF, CR>::kCLoads];   // and from its codes
   int xrd[4], crd[2];                         // LDS offsets of product j's row fragment, of step t's codes
   int h;
 };
 
 // Step T of a chunk: its four products on xb, the activations of two steps on
-// into xd and (T = 0) the codes of two chunks on into cd; cb and cn are this
-// chunk's codes and the next's.  The buffers are distinct, which the restrict
+// into xd and (T = 0) the codes of CR - 1 chunks on into cd; cb and cn are
+// this chunk's codes and the next's.  The buffers are distinct, which the restrict
 // qualifiers state, so that reads need not wait for the copies in flight.
-template <int NW, int RF, int CF, int T, bool WIDE>
+template <int NW, int RF, int CF, int CR, int T, bool WIDE>
 __device__ __forceinline__ void product_step(const char* __restrict__ xb, const char* __restrict__ xn,
                                              char* __restrict__ xd, const char* __restrict__ cb,
                                              const char* __restrict__ cn, char* __restrict__ cd, const uint16_t* xsrc,
                                              uint32_t xbound, bool in, const uint8_t* csrc, uint32_t cbound,
-                                             const Wave<NW, RF, CF>& w, const u32x2 (&sc)[CF], const u32x2 (&sn)[CF],
+                                             const Wave<NW, RF, CF, CR>& w, const u32x2 (&sc)[CF], const u32x2 (&sn)[CF],
                                              u32x4 (&cw)[CF], bf16x8 (&xa)[RF], u32x4 (&qa)[2][CF],
                                              f32x16 (&acc)[RF][CF]) {
-  using TL = Tile<NW, RF, CF>;
+  using TL = Tile<NW, RF, CF, CR>;
   constexpr int NX = TL::kXLoads, NC = TL::kCLoads;
   u32x4 cnext[CF];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int p = j & 1;
     if (j == 2) {
-      // The next step's codes.  Behind those of the next chunk were issued three
-      // steps' activations, one chunk's codes and one chunk's scales.
-      if (T == 1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(3 * NX + NC + (WIDE ? CF : 0)));
+      // The next step's codes.  Behind those of the next chunk were issued, with
+      // a ring of three, three steps' activations, one chunk's codes and one
+      // chunk's scales; with a ring of two, this step's activations.
+      if (T == 1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(CR == 3 ? 3 * NX + NC + (WIDE ? CF : 0) : NX));
 #pragma unroll
-      for (int f = 0; f < CF; ++f) cnext[f] = *(const u32x4*)((T == 0 ? cb : cn) + f * 2048 + w.crd[T ^ 1]);
+      for (int f = 0; f < CF; ++f)
+        cnext[f] = *(const u32x4*)((T == 0 ? cb : CR == 3 ? cn : cd) + f * 2048 + w.crd[T ^ 1]);
       __builtin_amdgcn_sched_barrier(0);
     }
     if (j == 3) {
@@ -223,20 +225,79 @@ __device__ __forceinline__ void product_step(const char* __restrict__ xb, const 
   for (int f = 0; f < CF; ++f) cw[f] = cnext[f];
 }
 
+// A wave's accumulators times g to rows [tl.r0, tl.r1) of out, channels from
+// o0 on (below width); rows without a token as zeros.
+// Accumulator: lane l, register r -> channel 8 (r / 4) + 4 h + r % 4, row c.
+// 32 rows at a time go through LDS of the wave's own (what the workgroup held
+// there is not needed behind the barrier), so that a row's channels leave in
+// 16-byte pieces side by side: stored from the registers, 8 bytes per row,
+// they took the 16384-token product 0.15 to 0.28 ms of 2.1.
+template <int NW, int RF, int CF, int OUT_BF16, int LDS>
+__device__ __forceinline__ void store_tile(char* smem, const f32x16 (&acc)[RF][CF], const RowTile& tl, float g,
+                                           const int32_t* __restrict__ tok_idx, int64_t n, int64_t o0, int64_t width,
+                                           void* __restrict__ out, int64_t ldo, bool vec_out) {
+  const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+  asm volatile("s_barrier" ::: "memory");
+  constexpr int ES = OUT_BF16 ? 2 : 4, ROW = 32 * CF * ES + 16, PR = 32 * CF * ES / 16;   // 16-byte pieces per row
+  static_assert(NW * 32 * ROW <= LDS, "output staging");
+  char* st = smem + wave * 32 * ROW;
+#pragma unroll
+  for (int i = 0; i < RF; ++i) {
+    const int64_t row0 = tl.r0 + 32 * i, trow = row0 + c;
+    const bool token = !tok_idx || trow >= tl.r1 || (tok_idx[trow] >= 0 && tok_idx[trow] < n);
+#pragma unroll
+    for (int f = 0; f < CF; ++f)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = token ? acc[i][f][4 * r4 + r] * g : 0.0f;
+        char* p = st + c * ROW + (32 * f + 8 * r4 + 4 * h) * ES;
+        if (OUT_BF16) {
+          typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+          *(bf16x4*)p = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        } else {
+          *(f32x4*)p = f32x4{v[0], v[1], v[2], v[3]};
+        }
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int q = 0; q < 32 * PR / 64; ++q) {
+      const int e = q * 64 + lane, r = e / PR, piece = e % PR;
+      const u32x4 v = *(const u32x4*)(st + r * ROW + piece * 16);
+      const int64_t row = row0 + r, o = o0 + piece * (16 / ES);
+      if (row >= tl.r1) continue;
+      if (vec_out && o + 16 / ES <= width) {
+        *(u32x4*)((char*)out + (row * ldo + o) * ES) = v;
+      } else {
+#pragma unroll
+        for (int x = 0; x < 16 / ES; ++x)
+          if (o + x < width) {
+            if (OUT_BF16) ((uint16_t*)out)[row * ldo + o + x] = (uint16_t)(v[x >> 1] >> (16 * (x & 1)));
+            else ((uint32_t*)out)[row * ldo + o + x] = v[x];
+          }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
 // Rows without a token (their number is outside [0, n)) read token 0's and
 // are stored as zeros.
-template <int NW, int RF, int CF, int OUT_BF16>
+template <int NW, int RF, int CF, int CR, int OUT_BF16>
 __device__ __forceinline__ void tile_product(char* smem, const RowTile& tl, const uint16_t* __restrict__ X, int64_t n,
                                              int64_t k, int64_t ldx, const int32_t* __restrict__ tok_idx,
                                              const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                              float g, int64_t m, void* __restrict__ Y, int64_t ldy, bool vec_out) {
-  using TL = Tile<NW, RF, CF>;
+  using TL = Tile<NW, RF, CF, CR>;
   constexpr int NX = TL::kXLoads, NC = TL::kCLoads;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5;
   const int64_t kb = k / 16;
   const int64_t o0 = tl.col * TL::kCols + wave * 32 * CF;
-  Wave<NW, RF, CF> w;
+  Wave<NW, RF, CF, CR> w;
   w.h = h;
 
   // Copy q of a step brings rows 8 (NW q + wave) + lane / 8.
@@ -276,8 +337,8 @@ __device__ __forceinline__ void tile_product(char* smem, const RowTile& tl, cons
       for (int r = 0; r < 16; ++r) acc[i][f][r] = 0.0f;
 
   char *x0 = smem, *x1 = smem + TL::kXBuf, *x2 = smem + 2 * TL::kXBuf;   // steps st, st + 1, st + 2
-  char* cl = smem + 3 * TL::kXBuf + wave * 3 * TL::kCBuf;
-  char *c0 = cl, *c1 = cl + TL::kCBuf, *c2 = cl + 2 * TL::kCBuf;         // chunks ch, ch + 1, ch + 2
+  char* cl = smem + 3 * TL::kXBuf + wave * CR * TL::kCBuf;
+  char *c0 = cl, *c1 = cl + TL::kCBuf, *c2 = cl + (CR - 1) * TL::kCBuf;   // chunks ch, ch + 1, ch + CR - 1
   const int xw = wave * 1024;
   u32x2 sc[CF], sn[CF];
   u32x4 cw[CF], qa[2][CF];
@@ -288,10 +349,10 @@ __device__ __forceinline__ void tile_product(char* smem, const RowTile& tl, cons
   copy_lds<NC, 1024>(c0, codes, cbound(0), w.coff, true);
   copy_lds<NX, NW * 1024>(x0 + xw, X, bound(0), w.xoff, inside(0));
   __builtin_amdgcn_sched_barrier(0);
-  copy_lds<NC, 1024>(c1, codes + 64, cbound(1), w.coff, true);
+  if (CR == 3) copy_lds<NC, 1024>(c1, codes + 64, cbound(1), w.coff, true);
   copy_lds<NX, NW * 1024>(x1 + xw, X + 64, bound(1), w.xoff, inside(1));
   __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm(NX + NC));   // step 0's and chunk 0's have landed
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(CR == 3 ? NX + NC : NX));   // step 0's and chunk 0's have landed
   asm volatile("s_barrier" ::: "memory");
 #pragma unroll
   for (int i = 0; i < RF; ++i) xa[i] = *(const bf16x8*)(x0 + i * 4096 + w.xrd[0]);
@@ -309,9 +370,9 @@ __device__ __forceinline__ void tile_product(char* smem, const RowTile& tl, cons
     const int64_t st = 2 * ch;
     load_scales<CF, !WIDE>(scales + (ch + 1) * 8, srow, kb - 8 * (ch + 1), sn);
     __builtin_amdgcn_sched_barrier(0);
-    product_step<NW, RF, CF, 0, WIDE>(x0, x1, x2 + xw, c0, c1, c2, X + (st + 2) * 64, bound(st + 2), WIDE || inside(st + 2),
-                                      codes + (ch + 2) * 64, cbound(ch + 2), w, sc, sn, cw, xa, qa, acc);
-    product_step<NW, RF, CF, 1, WIDE>(x1, x2, x0 + xw, c0, c1, c2, X + (st + 3) * 64, bound(st + 3), WIDE || inside(st + 3),
+    product_step<NW, RF, CF, CR, 0, WIDE>(x0, x1, x2 + xw, c0, c1, c2, X + (st + 2) * 64, bound(st + 2), WIDE || inside(st + 2),
+                                      codes + (ch + CR - 1) * 64, cbound(ch + CR - 1), w, sc, sn, cw, xa, qa, acc);
+    product_step<NW, RF, CF, CR, 1, WIDE>(x1, x2, x0 + xw, c0, c1, c2, X + (st + 3) * 64, bound(st + 3), WIDE || inside(st + 3),
                                       codes, 0, w, sc, sn, cw, xa, qa, acc);
 #pragma unroll
     for (int f = 0; f < CF; ++f) sc[f] = sn[f];
@@ -320,50 +381,31 @@ __device__ __forceinline__ void tile_product(char* smem, const RowTile& tl, cons
     x2 = x1;
     x1 = x;
     c0 = c1;
-    c1 = c2;
+    c1 = CR == 3 ? c2 : cc;
     c2 = cc;
   };
   int ch = 0;
   for (; ch < whole - 1; ++ch) chunk.template operator()<true>(ch);
   for (; ch < nchunks; ++ch) chunk.template operator()<false>(ch);
-  // The copies issued for steps past the end still write LDS (zeros): none may
-  // be in flight once the workgroup's LDS is released.
-  __builtin_amdgcn_s_waitcnt(0);
-
-  // Accumulator: lane l, register r -> channel 8 (r / 4) + 4 h + r % 4, row c.
-#pragma unroll
-  for (int i = 0; i < RF; ++i) {
-    const int64_t row = tl.r0 + 32 * i + c;
-    if (row >= tl.r1) continue;
-    const bool token = !tok_idx || (tok_idx[row] >= 0 && tok_idx[row] < n);
-#pragma unroll
-    for (int f = 0; f < CF; ++f)
-#pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        const int64_t o = o0 + 32 * f + 8 * r4 + 4 * h;
-        float v[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = token ? acc[i][f][4 * r4 + r] * g : 0.0f;
-        if (vec_out && o + 4 <= m) {
-          if (OUT_BF16) {
-            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-            *(bf16x4*)((__bf16*)Y + row * ldy + o) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-          } else {
-            *(f32x4*)((float*)Y + row * ldy + o) = f32x4{v[0], v[1], v[2], v[3]};
-          }
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (o + r < m) {
-              if (OUT_BF16) ((__bf16*)Y)[row * ldy + o + r] = (__bf16)v[r];
-              else ((float*)Y)[row * ldy + o + r] = v[r];
-            }
-        }
-      }
-  }
+  // (store_tile first waits for the copies issued for steps past the end, which
+  // still write LDS.)
+  store_tile<NW, RF, CF, OUT_BF16, TL::kLds>(smem, acc, tl, g, tok_idx, n, o0, m, Y, ldy, vec_out);
 }
 
-template <int NW, int RF, int CF, int OUT_BF16>
+// Calls f with the number of 32-row blocks that hold rows of the tile, at most RF: a
+// tile at an expert's end does not multiply the blocks it has no rows for.
+template <int RF, typename F>
+__device__ __forceinline__ void for_row_blocks(const RowTile& tl, F f) {
+  if constexpr (RF > 1) {
+    if (tl.r1 - tl.r0 <= 32 * (RF - 1)) {
+      for_row_blocks<RF - 1>(tl, f);
+      return;
+    }
+  }
+  f.template operator()<RF>();
+}
+
+template <int NW, int RF, int CF, int CR, int OUT_BF16>
 __global__ __launch_bounds__(64 * NW, 2) void grouped_gemm_kernel(const uint16_t* __restrict__ X, int64_t n, int64_t k,
                                                                   int64_t ldx, const int32_t* __restrict__ tok_idx,
                                                                   int64_t rows, const int64_t* __restrict__ off,
@@ -371,102 +413,292 @@ __global__ __launch_bounds__(64 * NW, 2) void grouped_gemm_kernel(const uint16_t
                                                                   const uint8_t* __restrict__ scales,
                                                                   const float* __restrict__ gs, int64_t m,
                                                                   void* __restrict__ Y, int64_t ldy, int vec_out) {
-  using TL = Tile<NW, RF, CF>;
+  using TL = Tile<NW, RF, CF, CR>;
   __shared__ __attribute__((aligned(1024))) char smem[TL::kLds];
   RowTile tl;
-  if (!find_tile<64 * NW>(off, G, rows, TL::kRows, (m + TL::kCols - 1) / TL::kCols, &tl)) return;
-  tile_product<NW, RF, CF, OUT_BF16>(smem, tl, X, n, k, ldx, tok_idx, codes + tl.expert * m * (k / 2),
-                                     scales + tl.expert * m * (k / 16), gs[tl.expert], m, Y, ldy, vec_out != 0);
+  if (!find_tile<64 * NW>(off, G, rows, TL::kRows, (m + TL::kCols - 1) / TL::kCols, smem, &tl)) return;
+  for_row_blocks<RF>(tl, [&]<int R>() {
+    tile_product<NW, R, CF, CR, OUT_BF16>(smem, tl, X, n, k, ldx, tok_idx, codes + tl.expert * m * (k / 2),
+                                          scales + tl.expert * m * (k / 16), gs[tl.expert], m, Y, ldy, vec_out != 0);
+  });
 }
 
-constexpr int ET = 128, EK = 64, ELD = EK + 8, EBUF = 2 * ET * ELD;
+// ---- the gradient of the rows ---------------------------------------------------
+// dX[r] = g dY[r] Q: 32 RF rows x 32 CF NW input channels per workgroup, as
+// above with the sum over m, in steps of 64.  A lane needs 8 codes of one input
+// channel under 8 output channels, which lie in 8 rows of the matrix: the
+// step's 64 m x 128 bytes of codes go to LDS as they are (16-byte pieces
+// swizzled by (m / 2) % 8) and are read with ds_read_b64_tr_b4, which gives lane i of 16 the
+// 16 nibbles of column i out of 16 rows of 16 (the width of a scale block).
+// So of a step, product j = 2 u + v takes m = 32 u + 16 h + 8 v .. + 7, and a
+// lane's 8 codes come under 8 different scales, which are staged transposed,
+// [block][m].  dY's rows are copied like the activations when m and their
+// stride are multiples of 8 (DMA), else through registers, zeros past m.
+template <int NW, int RF, int CF>
+struct GradTile {
+  static constexpr int kRows = 32 * RF, kCols = 32 * CF * NW, kStride = kCols / 2;   // bytes of codes per m
+  static constexpr int kYBuf = kRows * 128, kCBuf = 64 * kStride, kSBuf = 64 * kCols / 16;
+  static constexpr int kYLoads = 4 * RF / NW, kCLoads = kCBuf / 1024 / NW;
+  static constexpr int kLds = 3 * (kYBuf + kCBuf + kSBuf);
+  static_assert(kStride == 128 && NW == 4, "the swizzle and the copies' shapes");
+};
 
-// The gradient of the rows: 128 rows x 128 input channels per workgroup, the
-// sum over m in steps of 64.  A weight tile of 64 m x 128 k is expanded and
-// stored transposed, [k][m], so that both operands are read as above.
-template <int OUT_BF16>
-__global__ __launch_bounds__(256) void grouped_dx_kernel(const uint16_t* __restrict__ dY, int64_t rows, int64_t m,
-                                                         int64_t lddy, const int64_t* __restrict__ off, int64_t G,
-                                                         const uint8_t* __restrict__ codes,
-                                                         const uint8_t* __restrict__ scales,
-                                                         const float* __restrict__ gs, int64_t k,
-                                                         void* __restrict__ dX, int64_t lddx) {
-  __shared__ __attribute__((aligned(16))) uint16_t smem[EBUF];
-  RowTile tl;
-  if (!find_tile<256>(off, G, rows, ET, (k + ET - 1) / ET, &tl)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wr = wave >> 1, wc = wave & 1;
-  const int64_t o0 = tl.col * ET;
-  const int64_t kb = k / 16;
-  codes += tl.expert * m * (k / 2);
-  scales += tl.expert * m * kb;
-  f32x16 acc[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-  uint16_t* Ds = smem;
-  uint16_t* Qs = smem + ET * ELD;
-  const int arow = wr * 64 + (lane & 31), brow = wc * 64 + (lane & 31), koff = 8 * (lane >> 5);
-  for (int64_t m0 = 0; m0 < m; m0 += EK) {
-    // dY: 128 rows x 64 m, element by element (rows of dY have any alignment)
-    for (int q = 0; q < 32; ++q) {
-      const int e = q * 256 + tid, r = e >> 6, c = e & 63;
-      const bool ok = tl.r0 + r < tl.r1 && m0 + c < m;
-      Ds[r * ELD + c] = ok ? dY[(tl.r0 + r) * lddy + m0 + c] : (uint16_t)0;
-    }
-    // weights: 64 m x 8 blocks, 2 blocks per thread
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int e = q * 256 + tid, r = e >> 3, b = e & 7;
-      const int64_t blk = o0 / 16 + b;
-      const bool ok = m0 + r < m && blk < kb;
-      u32x2 cv{0u, 0u};
-      float sb = 0.0f;
-      if (ok) {
-        cv = *(const u32x2*)(codes + (m0 + r) * (k / 2) + blk * 8);
-        sb = e4m3_byte<0>(scales[(m0 + r) * kb + blk]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t p = dq_byte(cv[j >> 2], sb, j & 3);
-        Qs[(16 * b + 2 * j) * ELD + r] = (uint16_t)p;
-        Qs[(16 * b + 2 * j + 1) * ELD + r] = (uint16_t)(p >> 16);
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int ks = 0; ks < EK; ks += 16) {
-      bf16x8 a[2], b[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        a[t] = *(const bf16x8*)(Ds + (arow + 32 * t) * ELD + ks + koff);
-        b[t] = *(const bf16x8*)(Qs + (brow + 32 * t) * ELD + ks + koff);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
-    }
-    __syncthreads();
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ u32x2 read_tr4(const char* p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr4_b64_v2i32((__attribute__((address_space(3))) i32x2*)p));
+}
+// Codes m, m + 1 (byte `piece` of word) under their scales (byte pair `piece` % 2 of sw).
+__device__ __forceinline__ uint32_t dq_pair(uint32_t word, uint32_t sw, int piece) {
+  const f32x2c s = (piece & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)sw, true) : __builtin_amdgcn_cvt_pk_f32_fp8((int)sw, false);
+  f32x2c v;
+  switch (piece) {
+    case 0: v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 0); break;
+    case 1: v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 1); break;
+    case 2: v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 2); break;
+    default: v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 3); break;
   }
-  const float g = gs[tl.expert];
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2c{v.x * s.x, v.y * s.y}, bf16x2c));
+}
+
+// The codes and scales of product pair u of a step, for CF groups of 32 channels.
+template <int CF>
+struct GradCodes {
+  u32x2 w[CF];
+  u32x4 s[CF];
+};
+template <int CF>
+__device__ __forceinline__ void read_grad_codes(const char* cb, const char* sb, int u, const int (&crd)[CF],
+                                                const int (&srd)[CF], GradCodes<CF>& q) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int f = 0; f < CF; ++f) {
+    q.w[f] = read_tr4(cb + u * 4096 + crd[f]);
+    q.s[f] = *(const u32x4*)(sb + u * 32 + srd[f]);
+  }
+}
+
+// A thread's part of one step's dY through registers (not DMA): RF pieces.
+template <int RF>
+struct GradRows {
+  u32x4 v[RF];
+};
+
+// One step: its four products, the copies of two steps on, and to LDS what
+// registers hold of the next step.  yb, cb, sb: this step's buffers, n: the
+// next step's, d: two steps on; all distinct.
+template <int NW, int RF, int CF, bool DMA>
+__device__ __forceinline__ void gradient_step(const char* __restrict__ yb, const char* __restrict__ cb,
+                                              const char* __restrict__ sb, const char* __restrict__ yn,
+                                              const char* __restrict__ cn, const char* __restrict__ sn,
+                                              char* __restrict__ yw, char* __restrict__ sw, char* __restrict__ yd,
+                                              char* __restrict__ cd, const uint16_t* ysrc, uint32_t ybound,
+                                              const uint8_t* csrc, uint32_t cbound,
+                                              const uint32_t (&yoff)[GradTile<NW, RF, CF>::kYLoads],
+                                              const uint32_t (&coff)[GradTile<NW, RF, CF>::kCLoads], bool in,
+                                              const int (&yrd)[4], const int (&crd)[CF], const int (&srd)[CF],
+                                              GradCodes<CF>& q, bf16x8 (&ya)[RF], u32x4 (&qa)[2][CF],
+                                              f32x16 (&acc)[RF][CF], uint32_t& sreg, GradRows<RF>& yreg, auto load_next) {
+  using TL = GradTile<NW, RF, CF>;
+  constexpr int NY = DMA ? TL::kYLoads : 0, NC = TL::kCLoads;
+  GradCodes<CF> q1;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+  for (int j = 0; j < 4; ++j) {
+    const int p = j & 1;
+    if (j == 0) {
+      // What registers hold of the next step to LDS, then the loads and copies of the step behind it.
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int64_t orow = tl.r0 + wr * 64 + i * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        const int64_t col = o0 + wc * 64 + j * 32 + (lane & 31);
-        if (orow < tl.r1 && col < k) {
-          const float v = acc[i][j][r] * g;
-          if (OUT_BF16) ((__bf16*)dX)[orow * lddx + col] = (__bf16)v;
-          else ((float*)dX)[orow * lddx + col] = v;
-        }
+      for (int b = 0; b < 4; ++b) sw[b * 64] = (char)(sreg >> (8 * b));
+      if (!DMA)
+#pragma unroll
+        for (int r = 0; r < RF; ++r) *(u32x4*)(yw + r * NW * 1024) = yreg.v[r];
+      read_grad_codes<CF>(cb, sb, 1, crd, srd, q1);
+      __builtin_amdgcn_sched_barrier(0);
+      load_next();
+      __builtin_amdgcn_sched_barrier(0);
+      if (DMA) copy_lds<TL::kYLoads, NW * 1024>(yd, ysrc, ybound, yoff, in);
+      copy_lds<NC, NW * 1024>(cd, csrc, cbound, coff, true);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (j == 3) {
+      // The next step's copies: behind them were issued this step's and at least one register load.
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(NY + NC + 1));
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      read_grad_codes<CF>(cn, sn, 0, crd, srd, q);
+    }
+#pragma unroll
+    for (int i = 0; i < RF; ++i) {
+#pragma unroll
+      for (int f = 0; f < CF; ++f)
+        acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, qa[p][f]), ya[i], acc[i][f], 0, 0, 0);
+      ya[i] = j < 3 ? *(const bf16x8*)(yb + i * 4096 + yrd[(j + 1) & 3]) : *(const bf16x8*)(yn + i * 4096 + yrd[0]);
+#pragma unroll
+      for (int e = i * 4 * CF / RF; e < (i + 1) * 4 * CF / RF; ++e) {
+        const int f = e / 4, piece = e % 4, v = (j + 1) & 1;
+        // product j + 1: pair 0 or 1 of this step, or pair 0 of the next
+        const GradCodes<CF>& c = j == 1 || j == 2 ? q1 : q;
+        qa[p ^ 1][f][piece] = dq_pair(c.w[f][v], c.s[f][2 * v + (piece >> 1)], piece);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+template <int NW, int RF, int CF, bool DMA, int OUT_BF16>
+__device__ __forceinline__ void tile_gradient(char* smem, const RowTile& tl, const uint16_t* __restrict__ dY, int64_t m,
+                                              int64_t lddy, const uint8_t* __restrict__ codes,
+                                              const uint8_t* __restrict__ scales, float g, int64_t k,
+                                              void* __restrict__ dX, int64_t lddx, bool vec_out) {
+  using TL = GradTile<NW, RF, CF>;
+  constexpr int NC = TL::kCLoads;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 31, h = lane >> 5;
+  const int64_t kb = k / 16;
+  const int64_t t0 = tl.col * TL::kCols, o0 = t0 + wave * 32 * CF;   // the tile's and the wave's first channel
+
+  // Copy q of a step: rows 8 (NW q + wave) + lane / 8 of dY (of the step's m for codes), 16-byte piece `piece`.
+  const int piece = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4)), mk = 8 * piece;
+  const int64_t rows = tl.r1 - tl.r0;
+  dY += tl.r0 * lddy;
+  uint32_t yoff[TL::kYLoads], coff[NC];
+#pragma unroll
+  for (int q = 0; q < TL::kYLoads; ++q)
+    yoff[q] = (uint32_t)(min((int64_t)(8 * (NW * q + wave) + (lane >> 3)), rows - 1) * lddy + mk) * 2;
+#pragma unroll
+  for (int q = 0; q < NC; ++q) coff[q] = (uint32_t)((8 * (NW * q + wave) + (lane >> 3)) * (k / 2)) + 16 * piece;
+  // Bytes from step st on, of the tile's rows (below 2^32: checked on the host) and of the expert's codes.
+  auto ybound = [&](int64_t st) { return (uint32_t)max((int64_t)0, ((rows - 1) * lddy + m - 64 * st) * 2); };
+  auto inside = [&](int64_t st) { return st * 64 + mk < m; };
+  auto cbound = [&](int64_t st) {
+    return (uint32_t)min(max((int64_t)0, (m - 64 * st) * (k / 2) - t0 / 2), (int64_t)0xFFFFFF00);
+  };
+  auto csrc = [&](int64_t st) { return codes + 64 * st * (k / 2) + t0 / 2; };
+  // Scales: the thread brings 4 blocks of row tid / 4 of the step; zeros past m.
+  const int sm = tid >> 2, sq = (tid & 3) * 4;
+  auto load_scale = [&](int64_t st) {
+    const int64_t mm = st * 64 + sm, b0 = t0 / 16 + sq;
+    uint32_t v = 0;
+    if (kb % 4 == 0) {   // whole words inside the row
+      const bool ok = mm < m && b0 < kb;
+      v = *(const u32_any*)(scales + (ok ? mm * kb + b0 : 0));
+      v = ok ? v : 0;
+    } else {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const bool ok = mm < m && b0 + b < kb;
+        const uint32_t x = scales[ok ? mm * kb + b0 + b : 0];
+        v |= (ok ? x : 0) << (8 * b);
+      }
+    }
+    return v;
+  };
+  auto load_rows = [&](int64_t st, GradRows<RF>& y) {
+#pragma unroll
+    for (int q = 0; q < RF; ++q) {
+      const int64_t r = 8 * (NW * q + wave) + (lane >> 3), mm = st * 64 + mk;
+      const uint16_t* p = dY + min(r, rows - 1) * lddy + mm;
+      y.v[q] = u32x4{0u, 0u, 0u, 0u};
+      if (mm + 8 <= m) {
+        y.v[q] = *(const u32x4_a2*)p;
+      } else {
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (mm + x < m) y.v[q][x >> 1] |= (uint32_t)p[x] << (16 * (x & 1));
+      }
+    }
+  };
+
+  int yrd[4], crd[CF], srd[CF];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) yrd[j] = c * 128 + (((4 * (j >> 1) + 2 * h + (j & 1)) ^ ((c >> 1) & 7)) * 16);
+#pragma unroll
+  for (int f = 0; f < CF; ++f) {
+    crd[f] = (16 * h + (lane & 15)) * 128 + ((wave * CF + f) ^ ((lane & 15) >> 1)) * 16 + 8 * (c >> 4);
+    srd[f] = (wave * 2 * CF + 2 * f + (c >> 4)) * 64 + 16 * h;
+  }
+
+  f32x16 acc[RF][CF];
+#pragma unroll
+  for (int i = 0; i < RF; ++i)
+#pragma unroll
+    for (int f = 0; f < CF; ++f)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][f][r] = 0.0f;
+
+  // Steps st, st + 1, st + 2 in turn.
+  char *y0 = smem, *y1 = y0 + TL::kYBuf, *y2 = y1 + TL::kYBuf;
+  char *c0 = smem + 3 * TL::kYBuf, *c1 = c0 + TL::kCBuf, *c2 = c1 + TL::kCBuf;
+  char *s0 = smem + 3 * (TL::kYBuf + TL::kCBuf), *s1 = s0 + TL::kSBuf, *s2 = s1 + TL::kSBuf;
+  const int wo = wave * 1024, yo = wo + lane * 16, so = sq * 64 + sm;
+  const int nsteps = (int)((m + 63) / 64);
+  GradRows<RF> yreg;
+  uint32_t sreg = load_scale(0);
+  if (!DMA) load_rows(0, yreg);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) s0[so + b * 64] = (char)(sreg >> (8 * b));
+  if (!DMA)
+#pragma unroll
+    for (int q = 0; q < RF; ++q) *(u32x4*)(y0 + yo + q * NW * 1024) = yreg.v[q];
+  sreg = load_scale(1);
+  if (!DMA) load_rows(1, yreg);
+  __builtin_amdgcn_sched_barrier(0);
+  if (DMA) copy_lds<TL::kYLoads, NW * 1024>(y0 + wo, dY, ybound(0), yoff, inside(0));
+  copy_lds<NC, NW * 1024>(c0 + wo, csrc(0), cbound(0), coff, true);
+  __builtin_amdgcn_sched_barrier(0);
+  if (DMA) copy_lds<TL::kYLoads, NW * 1024>(y1 + wo, dY + 64, ybound(1), yoff, inside(1));
+  copy_lds<NC, NW * 1024>(c1 + wo, csrc(1), cbound(1), coff, true);
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((DMA ? TL::kYLoads : 0) + NC));   // step 0's have landed
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  GradCodes<CF> q;
+  u32x4 qa[2][CF];
+  bf16x8 ya[RF];
+  read_grad_codes<CF>(c0, s0, 0, crd, srd, q);
+#pragma unroll
+  for (int i = 0; i < RF; ++i) ya[i] = *(const bf16x8*)(y0 + i * 4096 + yrd[0]);
+#pragma unroll
+  for (int f = 0; f < CF; ++f)
+#pragma unroll
+    for (int p = 0; p < 4; ++p) qa[0][f][p] = dq_pair(q.w[f][0], q.s[f][p >> 1], p);
+
+  for (int st = 0; st < nsteps; ++st) {
+    gradient_step<NW, RF, CF, DMA>(y0, c0, s0, y1, c1, s1, y1 + yo, s1 + so, y2 + wo, c2 + wo, dY + 64 * (int64_t)(st + 2),
+                                   ybound(st + 2), csrc(st + 2), cbound(st + 2), yoff, coff, inside(st + 2), yrd, crd, srd, q,
+                                   ya, qa, acc, sreg, yreg, [&]() {
+                                     sreg = load_scale(st + 2);
+                                     if (!DMA) load_rows(st + 2, yreg);
+                                   });
+    char *y = y0, *cc = c0, *ss = s0;
+    y0 = y1;
+    y1 = y2;
+    y2 = y;
+    c0 = c1;
+    c1 = c2;
+    c2 = cc;
+    s0 = s1;
+    s1 = s2;
+    s2 = ss;
+  }
+  store_tile<NW, RF, CF, OUT_BF16, TL::kLds>(smem, acc, tl, g, nullptr, 0, o0, k, dX, lddx, vec_out);
+}
+
+template <int NW, int RF, int CF, bool DMA, int OUT_BF16>
+__global__ __launch_bounds__(64 * NW, 2) void grouped_dx_kernel(const uint16_t* __restrict__ dY, int64_t rows, int64_t m,
+                                                                int64_t lddy, const int64_t* __restrict__ off, int64_t G,
+                                                                const uint8_t* __restrict__ codes,
+                                                                const uint8_t* __restrict__ scales,
+                                                                const float* __restrict__ gs, int64_t k,
+                                                                void* __restrict__ dX, int64_t lddx, int vec_out) {
+  using TL = GradTile<NW, RF, CF>;
+  __shared__ __attribute__((aligned(1024))) char smem[TL::kLds];
+  RowTile tl;
+  if (!find_tile<64 * NW>(off, G, rows, TL::kRows, (k + TL::kCols - 1) / TL::kCols, smem, &tl)) return;
+  for_row_blocks<RF>(tl, [&]<int R>() {
+    tile_gradient<NW, R, CF, DMA, OUT_BF16>(smem, tl, dY, m, lddy, codes + tl.expert * m * (k / 2),
+                                            scales + tl.expert * m * (k / 16), gs[tl.expert], k, dX, lddx, vec_out != 0);
+  });
 }
 
 // Workgroups for every row tile of height bt that rows over G experts can
@@ -482,28 +714,23 @@ hipError_t nvfp4_gemm_grouped_launch(const uint16_t* X, int64_t n, int64_t k, in
                                      int64_t rows, const int64_t* grp_off, int64_t G, const uint8_t* codes,
                                      const uint8_t* scales, const float* g, int64_t m, void* Y, int out_bf16,
                                      int64_t ldy, hipStream_t s) {
-  const int vec = ldy % 4 == 0 && (uintptr_t)Y % (out_bf16 ? 8 : 16) == 0;
-#define NVQ_GROUPED(NW, RF, CF)                                                                                      \
+  const int vec = ldy % (out_bf16 ? 8 : 4) == 0 && (uintptr_t)Y % 16 == 0;
+#define NVQ_GROUPED(NW, RF, CF, CR)                                                                                      \
   do {                                                                                                               \
-    using TL = Tile<NW, RF, CF>;                                                                                     \
+    using TL = Tile<NW, RF, CF, CR>;                                                                                     \
     const int64_t blocks = most_tiles(rows, G, TL::kRows, (m + TL::kCols - 1) / TL::kCols);                          \
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;                                                            \
     if (out_bf16)                                                                                                    \
-      hipLaunchKernelGGL((grouped_gemm_kernel<NW, RF, CF, 1>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, X, n, k, \
+      hipLaunchKernelGGL((grouped_gemm_kernel<NW, RF, CF, CR, 1>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, X, n, k, \
                          ldx, tok_idx, rows, grp_off, G, codes, scales, g, m, Y, ldy, vec);                          \
     else                                                                                                             \
-      hipLaunchKernelGGL((grouped_gemm_kernel<NW, RF, CF, 0>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, X, n, k, \
+      hipLaunchKernelGGL((grouped_gemm_kernel<NW, RF, CF, CR, 0>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, X, n, k, \
                          ldx, tok_idx, rows, grp_off, G, codes, scales, g, m, Y, ldy, vec);                          \
   } while (0)
   const int64_t avg = rows / std::min(rows, G);
-  const char* force = getenv("NVQ_RF");
-  const int f = force ? atoi(force) : avg >= 96 ? 4 : avg >= 16 ? 2 : 1;
-  if (f == 4) NVQ_GROUPED(8, 4, 2);
-  else if (f == 2) NVQ_GROUPED(8, 2, 2);
-  else if (f == 5) NVQ_GROUPED(4, 4, 1);
-  else if (f == 3) NVQ_GROUPED(4, 2, 1);
-  else if (f == 6) NVQ_GROUPED(4, 1, 2);
-  else NVQ_GROUPED(4, 1, 1);
+  const int f = avg >= 4 ? 4 : 1;
+  if (f == 4) NVQ_GROUPED(4, 4, 2, 2);
+  else NVQ_GROUPED(4, 1, 1, 3);
 #undef NVQ_GROUPED
   return hipGetLastError();
 }
@@ -512,15 +739,29 @@ hipError_t nvfp4_gemm_grouped_dx_launch(const uint16_t* dY, int64_t rows, int64_
                                         const int64_t* grp_off, int64_t G, const uint8_t* codes, const uint8_t* scales,
                                         const float* g, int64_t k, void* dX, int out_bf16, int64_t lddx,
                                         hipStream_t s) {
-  const int64_t blocks = most_tiles(rows, G, ET, (k + ET - 1) / ET);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks);
-  if (out_bf16)
-    hipLaunchKernelGGL(grouped_dx_kernel<1>, grid, dim3(256), 0, s, dY, rows, m, lddy, grp_off, G, codes, scales, g, k,
-                       dX, lddx);
-  else
-    hipLaunchKernelGGL(grouped_dx_kernel<0>, grid, dim3(256), 0, s, dY, rows, m, lddy, grp_off, G, codes, scales, g, k,
-                       dX, lddx);
+  const int vec = lddx % (out_bf16 ? 8 : 4) == 0 && (uintptr_t)dX % 16 == 0;
+  const bool dma = m % 8 == 0 && lddy % 8 == 0 && (uintptr_t)dY % 16 == 0 && lddy < (1 << 23);
+#define NVQ_DX(RF, DMA)                                                                                             \
+  do {                                                                                                              \
+    using TL = GradTile<4, RF, 2>;                                                                                  \
+    const int64_t blocks = most_tiles(rows, G, TL::kRows, (k + TL::kCols - 1) / TL::kCols);                         \
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;                                                           \
+    if (out_bf16)                                                                                                   \
+      hipLaunchKernelGGL((grouped_dx_kernel<4, RF, 2, DMA, 1>), dim3((unsigned)blocks), dim3(256), 0, s, dY, rows, m, \
+                         lddy, grp_off, G, codes, scales, g, k, dX, lddx, vec);                                     \
+    else                                                                                                            \
+      hipLaunchKernelGGL((grouped_dx_kernel<4, RF, 2, DMA, 0>), dim3((unsigned)blocks), dim3(256), 0, s, dY, rows, m, \
+                         lddy, grp_off, G, codes, scales, g, k, dX, lddx, vec);                                     \
+  } while (0)
+  const int64_t avg = rows / std::min(rows, G);
+  if (avg >= 24) {
+    if (dma) NVQ_DX(4, true);
+    else NVQ_DX(4, false);
+  } else {
+    if (dma) NVQ_DX(2, true);
+    else NVQ_DX(2, false);
+  }
+#undef NVQ_DX
   return hipGetLastError();
 }
 
