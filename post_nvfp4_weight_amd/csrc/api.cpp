@@ -812,10 +812,11 @@ int nvfp4_gemm_grouped(const void* X, int x_dtype, int64_t n, int64_t k, int64_t
   if (x_dtype != NVQ_DTYPE_BF16) return failp(NVQ_ERR_DTYPE, fn, "x_dtype %d (activations must be bf16)", x_dtype);
   const int rc = experts_check(fn, rows, grp_off, G, codes, scales, g, m, k, Y, y_dtype, ldy, m);
   if (rc != NVQ_OK) return rc;
-  if (n < 0 || n > 0x7FFFFFFF || ldx < k || ldx % 8 != 0 || (!tok_idx && rows > n) || (rows > 0 && n == 0))
+  if (n < 0 || n > 0x7FFFFFFF || ldx < k || ldx % 8 != 0 || ldx > (1ll << 35) / std::max<int64_t>(n, 1) ||
+      (!tok_idx && rows > n) || (rows > 0 && n == 0))
     return failp(NVQ_ERR_SHAPE, fn,
-                 "n=%lld rows=%lld ldx=%lld k=%lld (need 0<=n<2^31, ldx>=k, ldx%%8==0, rows<=n without tok_idx, and "
-                 "tokens if there are rows)",
+                 "n=%lld rows=%lld ldx=%lld k=%lld (need 0<=n<2^31, ldx>=k, ldx%%8==0, n*ldx<=2^35, rows<=n without "
+                 "tok_idx, and tokens if there are rows)",
                  (long long)n, (long long)rows, (long long)ldx, (long long)k);
   if (rows == 0) return NVQ_OK;
   if (!X) return failp(NVQ_ERR_NULL, fn, "X is NULL");

@@ -16,78 +16,90 @@ namespace nvq {
 
 namespace {
 
-// Row range [*b, *e) of expert x, clamped into [0, rows], so that no offsets lead out of the buffers.
-__device__ __forceinline__ void group_range(const int64_t* off, int64_t x, int64_t rows, int64_t* b, int64_t* e) {
-  *b = min(max(off[x], (int64_t)0), rows);
-  *e = min(max(off[x + 1], *b), rows);
-}
-
 struct RowTile {
   int64_t expert, r0, r1;   // rows [r0, r1), r1 at most r0 + the tile height and within the expert's rows
   int64_t col;              // column tile
 };
 
-// Row tiles of height bt over all experts in order, times ncol column tiles
+// Inclusive sum over the wave's lanes (row shifts, then the rows' last lanes to the rows behind).
+__device__ __forceinline__ int wave_inclusive(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
+// Row tiles of height BT over all experts in order, times ncol column tiles
 // each (column tiles of a row tile next to each other): the one of this
 // workgroup, false if there is none.  The tiles are dealt to the 8 XCDs
 // (blockIdx.x mod 8) in contiguous runs, so that the tiles that share an
-// expert's weights or a row tile's activations share an L2.  Called by a whole
-// workgroup of NT threads with 512 bytes of LDS.
-template <int NT>
-__device__ __forceinline__ bool find_tile(const int64_t* off, int64_t G, int64_t rows, int bt, int64_t ncol,
-                                          char* lds, RowTile* out) {
-  int64_t* wsum = (int64_t*)lds;             // NT / 64
-  RowTile& found = *(RowTile*)(lds + 256);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t b = 0, e = 0, first = 0, cnt = 0;
-  // Tiles of experts x0 + thread, and the sum over all of this turn's.
-  auto turn = [&](int64_t x0) {
-    const int64_t x = x0 + threadIdx.x;
-    b = e = 0;
-    if (x < G) group_range(off, x, rows, &b, &e);
-    cnt = (e - b + bt - 1) / bt;
-    int64_t incl = cnt;
+// expert's weights or a row tile's activations share an L2.  Each wave sums the
+// tile counts of all experts by itself, 4 experts per lane and turn: no
+// barrier, and about 1 us less than sums across the workgroup took, which a
+// one-token product spends several times over.  Offsets are clamped into
+// [0, rows], so that none lead out of the buffers.
+template <int BT>
+__device__ __forceinline__ bool find_tile(const int64_t* __restrict__ off, int64_t G, int64_t rows, uint32_t ncol,
+                                          RowTile* out) {
+  constexpr int EPL = 4;
+  const int lane = threadIdx.x & 63;
+  int b[EPL], e[EPL], mine = 0, incl = 0;
+  auto turn = [&](int64_t x0) {   // tiles of experts x0 + EPL lane ..; returns the sum over the wave
+    int64_t v[EPL + 1];
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t y = __shfl_up(incl, o);
-      if (lane >= o) incl += y;
-    }
-    __syncthreads();
-    if (lane == 63) wsum[wave] = incl;
-    __syncthreads();
-    int64_t all = 0;
-    first = incl - cnt;
+    for (int i = 0; i <= EPL; ++i) v[i] = off[min(x0 + EPL * lane + i, G)];
+    mine = 0;
 #pragma unroll
-    for (int w = 0; w < NT / 64; ++w) {
-      first += w < wave ? wsum[w] : 0;
-      all += wsum[w];
+    for (int i = 0; i < EPL; ++i) {
+      b[i] = (int)min(max(v[i], (int64_t)0), rows);
+      e[i] = (int)min(max(v[i + 1], (int64_t)b[i]), rows);
+      mine += (int)(((uint32_t)(e[i] - b[i]) + BT - 1) / BT);
     }
-    return all;
+    incl = wave_inclusive(mine);
+    return (uint32_t)__builtin_amdgcn_readlane(incl, 63);
   };
-  int64_t total = 0;
-  for (int64_t x0 = 0; x0 < G; x0 += NT) total += turn(x0);
-  const int64_t n = total * ncol, per = (n + 7) / 8;
-  const int64_t i = blockIdx.x >> 3, id = (blockIdx.x & 7) * per + i;
-  if (i >= per || id >= n) return false;   // the same in every thread
-  const int64_t tile = id / ncol;
-  int64_t before = 0;
-  for (int64_t x0 = 0; x0 < G; x0 += NT) {
-    const int64_t all = G > NT ? turn(x0) : total;   // (one turn: its values are still there)
-    if (tile >= before + first && tile < before + first + cnt) {
-      found.expert = x0 + threadIdx.x;
-      found.r0 = b + (tile - before - first) * bt;
-      found.r1 = min(e, found.r0 + bt);
+  uint32_t total = 0;
+  for (int64_t x0 = 0; x0 < G; x0 += 64 * EPL) total += turn(x0);
+  const uint64_t n = (uint64_t)total * ncol, per = (n + 7) / 8;
+  const uint32_t i = blockIdx.x >> 3;
+  const uint64_t id = (blockIdx.x & 7) * per + i;
+  if (i >= per || id >= n) return false;
+  const uint32_t tile = (uint32_t)id / ncol;   // (the grid has fewer than 2^31 workgroups)
+  uint32_t before = 0;
+  for (int64_t x0 = 0; x0 < G; x0 += 64 * EPL) {
+    const uint32_t all = G > 64 * EPL ? turn(x0) : total;   // (one turn: its values are still there)
+    if (tile < before + all) {
+      const uint32_t first = before + incl - mine;   // of the lane's experts
+      const int src = __ffsll((unsigned long long)__ballot(tile >= first && tile < first + mine)) - 1;
+      int at = (int)(tile - first), x = 0, r0 = 0, r1 = 0;
+      bool found = false;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        const int cnt = (int)(((uint32_t)(e[j] - b[j]) + BT - 1) / BT);
+        const bool here = !found && at < cnt;
+        x = here ? j : x;
+        r0 = here ? b[j] + at * BT : r0;
+        r1 = here ? min(e[j], b[j] + at * BT + BT) : r1;
+        found |= here;
+        at -= cnt;
+      }
+      out->expert = x0 + EPL * src + __builtin_amdgcn_readlane(x, src);
+      out->r0 = __builtin_amdgcn_readlane(r0, src);
+      out->r1 = __builtin_amdgcn_readlane(r1, src);
+      out->col = (uint32_t)id - tile * ncol;
+      return true;
     }
     before += all;
   }
-  __syncthreads();
-  *out = found;
-  out->col = id - tile * ncol;
-  __syncthreads();   // lds is free again
-  return true;
+  return false;
 }
 
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint16_t u16_any __attribute__((aligned(1)));
 
 __device__ __forceinline__ constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 __device__ __forceinline__ constexpr int waitcnt_vm_lgkm0(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
@@ -151,11 +163,37 @@ __device__ __forceinline__ void copy_lds(char* __restrict__ dst, const void* src
 #endif
 }
 
+// What is copied for activations past the last input channel where X is FAR.
+__device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
+
+// The same for rows of X, offsets in 16-byte pieces.  FAR: X has 2^32 bytes or
+// more, which a buffer cannot span; the copies then go by 64-bit addresses.
+template <int NL, int STRIDE, bool FAR>
+__device__ __forceinline__ void copy_x(char* __restrict__ dst, const uint16_t* src, uint32_t bound, const uint32_t (&off)[NL],
+                                       bool in) {
+#if __HIP_DEVICE_COMPILE__
+  if (FAR) {
+#pragma unroll
+    for (int q = 0; q < NL; ++q) {
+      const void* p = in ? (const void*)((const char*)src + (uint64_t)off[q] * 16) : (const void*)&kZeros;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
+                                       (__attribute__((address_space(3))) void*)(dst + q * STRIDE), 16, 0, 0);
+    }
+  } else {
+    __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)src, (short)0, bound, 0x00020000);
+#pragma unroll
+    for (int q = 0; q < NL; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + q * STRIDE), 16,
+                                               in ? off[q] * 16 : 0xFFFFFFF0u, 0, 0, 0);
+  }
+#endif
+}
+
 // What a wave's steps share.
 template <int NW, int RF, int CF, int CR>
 struct Wave {
-  uint32_t xoff[Tile<NW, RF, CF, CR>::kXLoads];   // its copies' byte offsets from X
-  uint32_t coff[Tile<NW, RF, CF, CR>::kCLoads];   // and from its codes
+  uint32_t xoff[Tile<NW, RF, CF, CR>::kXLoads];   // its copies' offsets from X (16-byte pieces)
+  uint32_t coff[Tile<NW, RF, CF, CR>::kCLoads];   // and from its codes (bytes)
   int xrd[4], crd[2];                         // LDS offsets of product j's row fragment, of step t's codes
   int h;
 };
@@ -164,7 +202,7 @@ struct Wave {
 // into xd and (T = 0) the codes of CR - 1 chunks on into cd; cb and cn are
 // this chunk's codes and the next's.  The buffers are distinct, which the restrict
 // qualifiers state, so that reads need not wait for the copies in flight.
-template <int NW, int RF, int CF, int CR, int T, bool WIDE>
+template <int NW, int RF, int CF, int CR, int T, bool WIDE, bool FAR>
 __device__ __forceinline__ void product_step(const char* __restrict__ xb, const char* __restrict__ xn,
                                              char* __restrict__ xd, const char* __restrict__ cb,
                                              const char* __restrict__ cn, char* __restrict__ cd, const uint16_t* xsrc,
@@ -215,7 +253,7 @@ __device__ __forceinline__ void product_step(const char* __restrict__ xb, const 
       }
       __builtin_amdgcn_sched_barrier(0);
       if (j == 0 && i == 0) {
-        copy_lds<NX, NW * 1024>(xd, xsrc, xbound, w.xoff, in);
+        copy_x<NX, NW * 1024, FAR>(xd, xsrc, xbound, w.xoff, in);
         if (T == 0) copy_lds<NC, 1024>(cd, csrc, cbound, w.coff, true);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -286,7 +324,7 @@ __device__ __forceinline__ void store_tile(char* smem, const f32x16 (&acc)[RF][C
 
 // Rows without a token (their number is outside [0, n)) read token 0's and
 // are stored as zeros.
-template <int NW, int RF, int CF, int CR, int OUT_BF16>
+template <int NW, int RF, int CF, int CR, int OUT_BF16, bool FAR>
 __device__ __forceinline__ void tile_product(char* smem, const RowTile& tl, const uint16_t* __restrict__ X, int64_t n,
                                              int64_t k, int64_t ldx, const int32_t* __restrict__ tok_idx,
                                              const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
@@ -306,9 +344,9 @@ __device__ __forceinline__ void tile_product(char* smem, const RowTile& tl, cons
   for (int q = 0; q < NX; ++q) {
     const int64_t r = tl.r0 + 8 * (NW * q + wave) + (lane >> 3);
     const int64_t t = r < tl.r1 ? (tok_idx ? tok_idx[r] : r) : 0;
-    w.xoff[q] = (uint32_t)((t >= 0 && t < n ? t : 0) * ldx + xk) * 2;
+    w.xoff[q] = (uint32_t)(((t >= 0 && t < n ? t : 0) * ldx + xk) / 8);
   }
-  // Bytes of X from step st on (below 2^32 - 256: checked on the host).
+  // Bytes of X from step st on (not FAR: below 2^32 - 256).
   auto bound = [&](int64_t st) { return (uint32_t)max((int64_t)0, ((n - 1) * ldx + k - st * 64) * 2); };
   auto inside = [&](int64_t st) { return st * 64 + xk < k; };
 
@@ -347,10 +385,10 @@ __device__ __forceinline__ void tile_product(char* smem, const RowTile& tl, cons
   if (whole) load_scales<CF, false>(scales, srow, 8, sc);
   else load_scales<CF, true>(scales, srow, kb, sc);
   copy_lds<NC, 1024>(c0, codes, cbound(0), w.coff, true);
-  copy_lds<NX, NW * 1024>(x0 + xw, X, bound(0), w.xoff, inside(0));
+  copy_x<NX, NW * 1024, FAR>(x0 + xw, X, bound(0), w.xoff, inside(0));
   __builtin_amdgcn_sched_barrier(0);
   if (CR == 3) copy_lds<NC, 1024>(c1, codes + 64, cbound(1), w.coff, true);
-  copy_lds<NX, NW * 1024>(x1 + xw, X + 64, bound(1), w.xoff, inside(1));
+  copy_x<NX, NW * 1024, FAR>(x1 + xw, X + 64, bound(1), w.xoff, inside(1));
   __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(CR == 3 ? NX + NC : NX));   // step 0's and chunk 0's have landed
   asm volatile("s_barrier" ::: "memory");
@@ -370,9 +408,9 @@ __device__ __forceinline__ void tile_product(char* smem, const RowTile& tl, cons
     const int64_t st = 2 * ch;
     load_scales<CF, !WIDE>(scales + (ch + 1) * 8, srow, kb - 8 * (ch + 1), sn);
     __builtin_amdgcn_sched_barrier(0);
-    product_step<NW, RF, CF, CR, 0, WIDE>(x0, x1, x2 + xw, c0, c1, c2, X + (st + 2) * 64, bound(st + 2), WIDE || inside(st + 2),
+    product_step<NW, RF, CF, CR, 0, WIDE, FAR>(x0, x1, x2 + xw, c0, c1, c2, X + (st + 2) * 64, bound(st + 2), WIDE || inside(st + 2),
                                       codes + (ch + CR - 1) * 64, cbound(ch + CR - 1), w, sc, sn, cw, xa, qa, acc);
-    product_step<NW, RF, CF, CR, 1, WIDE>(x1, x2, x0 + xw, c0, c1, c2, X + (st + 3) * 64, bound(st + 3), WIDE || inside(st + 3),
+    product_step<NW, RF, CF, CR, 1, WIDE, FAR>(x1, x2, x0 + xw, c0, c1, c2, X + (st + 3) * 64, bound(st + 3), WIDE || inside(st + 3),
                                       codes, 0, w, sc, sn, cw, xa, qa, acc);
 #pragma unroll
     for (int f = 0; f < CF; ++f) sc[f] = sn[f];
@@ -405,7 +443,7 @@ __device__ __forceinline__ void for_row_blocks(const RowTile& tl, F f) {
   f.template operator()<RF>();
 }
 
-template <int NW, int RF, int CF, int CR, int OUT_BF16>
+template <int NW, int RF, int CF, int CR, int OUT_BF16, bool FAR>
 __global__ __launch_bounds__(64 * NW, 2) void grouped_gemm_kernel(const uint16_t* __restrict__ X, int64_t n, int64_t k,
                                                                   int64_t ldx, const int32_t* __restrict__ tok_idx,
                                                                   int64_t rows, const int64_t* __restrict__ off,
@@ -416,11 +454,165 @@ __global__ __launch_bounds__(64 * NW, 2) void grouped_gemm_kernel(const uint16_t
   using TL = Tile<NW, RF, CF, CR>;
   __shared__ __attribute__((aligned(1024))) char smem[TL::kLds];
   RowTile tl;
-  if (!find_tile<64 * NW>(off, G, rows, TL::kRows, (m + TL::kCols - 1) / TL::kCols, smem, &tl)) return;
+  if (!find_tile<TL::kRows>(off, G, rows, (uint32_t)((m + TL::kCols - 1) / TL::kCols), &tl)) return;
   for_row_blocks<RF>(tl, [&]<int R>() {
-    tile_product<NW, R, CF, CR, OUT_BF16>(smem, tl, X, n, k, ldx, tok_idx, codes + tl.expert * m * (k / 2),
+    tile_product<NW, R, CF, CR, OUT_BF16, FAR>(smem, tl, X, n, k, ldx, tok_idx, codes + tl.expert * m * (k / 2),
                                           scales + tl.expert * m * (k / 16), gs[tl.expert], m, Y, ldy, vec_out != 0);
   });
+}
+
+// ---- few rows ---------------------------------------------------------------------
+// A token's experts are so few tiles of the kernel above that most of the
+// device would idle.  Here a workgroup of 8 waves takes 16 rows and 32 output
+// channels, the waves share k in turn, in pairs of 128 k (whole 128-byte lines
+// of codes), and nothing is staged: all of a pair's loads are issued ahead, the
+// next pairs' while it is multiplied.
+//   v_mfma_f32_16x16x32_bf16, A = 16 channels, B = 16 rows: lane (c = l % 16,
+//   q = l / 16) takes the 32 consecutive k from 32 q of each 128, 8 per product
+//   (16 bytes of codes and 2 scales per channel), of channel c and row c.
+// Lanes without a row read the tile's last row's activations and are not
+// stored.  The waves' partial sums are added in wave order through LDS.
+constexpr int FW = 8, FROWS = 16, FCG = 2, FCOLS = 16 * FCG, FD = 2;
+typedef float f32x4c __attribute__((ext_vector_type(4)));
+
+struct FewPair {
+  u32x4 w[2][FCG];
+  uint32_t s[2][FCG];
+};
+struct FewX {
+  u32x4 v[4];
+};
+
+template <int OUT_BF16>
+__global__ __launch_bounds__(64 * FW, 4) void grouped_few_kernel(const uint16_t* __restrict__ X, int64_t n, int64_t k,
+                                                                 int64_t ldx, const int32_t* __restrict__ tok_idx,
+                                                                 int64_t rows, const int64_t* __restrict__ off,
+                                                                 int64_t G, const uint8_t* __restrict__ codes,
+                                                                 const uint8_t* __restrict__ scales,
+                                                                 const float* __restrict__ gs, int64_t m,
+                                                                 void* __restrict__ Y, int64_t ldy) {
+  __shared__ __attribute__((aligned(16))) float part[FW][FROWS][FCOLS + 4];
+  RowTile tl;
+  if (!find_tile<FROWS>(off, G, rows, (uint32_t)((m + FCOLS - 1) / FCOLS), &tl)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, q = lane >> 4;
+  const int64_t kb = k / 16, o0 = tl.col * FCOLS;
+  codes += (tl.expert * m + o0) * (k / 2);
+  scales += (tl.expert * m + o0) * kb;
+  uint32_t crow[FCG], srow[FCG];   // the lane's channels from the tile's first (past m: the last one)
+#pragma unroll
+  for (int f = 0; f < FCG; ++f) {
+    const int64_t o = min((int64_t)(16 * f + c), m - 1 - o0);
+    crow[f] = (uint32_t)(o * (k / 2)) + 16 * q;
+    srow[f] = (uint32_t)(o * kb) + 2 * q;
+  }
+  const int whole = (int)(k / 256);   // pairs of 128 k that k has
+  auto load_pair = [&](int p, FewPair& x) {
+    const uint8_t *cp = codes + (int64_t)p * 128, *sp = scales + (int64_t)p * 16;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int f = 0; f < FCG; ++f) {
+        x.w[u][f] = *(const u32x4_any*)(cp + 64 * u + crow[f]);
+        x.s[u][f] = *(const u16_any*)(sp + 8 * u + srow[f]);
+      }
+  };
+  const int mine = whole > wave ? (whole - wave + FW - 1) / FW : 0;   // the wave's i-th is wave + FW i
+  FewPair buf[FD];
+#pragma unroll
+  for (int d = 0; d < FD; ++d)
+    if (d < mine) load_pair(wave + FW * d, buf[d]);
+  const int64_t row = min(tl.r0 + c, tl.r1 - 1);
+  const int64_t t = tok_idx ? tok_idx[row] : row;
+  const bool token = t >= 0 && t < n;
+  const uint16_t* xrow = X + (token ? t : 0) * ldx + 32 * q;
+  auto load_x = [&](int64_t k0, FewX& x) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x.v[j] = *(const u32x4*)(xrow + k0 + 8 * j);
+  };
+  f32x4c acc[FCG];
+#pragma unroll
+  for (int f = 0; f < FCG; ++f) acc[f] = f32x4c{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const u32x4 (&w)[FCG], const uint32_t (&s2)[FCG], const FewX& x) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int f = 0; f < FCG; ++f) {
+        const float s = j < 2 ? e4m3_byte<0>(s2[f]) : e4m3_byte<1>(s2[f]);
+        const u32x4 qv{dq_byte<0>(w[f][j], s), dq_byte<1>(w[f][j], s), dq_byte<2>(w[f][j], s), dq_byte<3>(w[f][j], s)};
+        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, qv), __builtin_bit_cast(bf16x8, x.v[j]),
+                                                         acc[f], 0, 0, 0);
+      }
+  };
+  FewX xa, xb;
+  auto k_of = [&](int i) { return 256 * (int64_t)(wave + FW * i); };
+  // Multiplies pair i (its first half's activations are in xa), then loads pair i + FD in its place.
+  auto stage = [&](int i, FewPair& p, bool more, bool ahead) {
+    load_x(k_of(i) + 128, xb);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(p.w[0], p.s[0], xa);
+    if (more) load_x(k_of(i + 1), xa);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(p.w[1], p.s[1], xb);
+    if (ahead) load_pair(wave + FW * (i + FD), p);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (mine > 0) {
+    load_x(k_of(0), xa);
+    int i = 0;
+    for (; i + 2 * FD <= mine; i += FD)
+#pragma unroll
+      for (int d = 0; d < FD; ++d) stage(i + d, buf[d], true, true);
+    // fewer than 2 FD pairs left
+#pragma unroll
+    for (int d = 0; d < 2 * FD - 1; ++d)
+      if (i + d < mine) stage(i + d, buf[d % FD], i + d + 1 < mine, i + d + FD < mine);
+  }
+  // The rest of k, less than a pair: blocks past k as zero codes under zero scales.
+  FewPair cur;
+  if (wave == whole % FW && (int64_t)whole * 256 < k) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t k0 = (int64_t)whole * 256 + 128 * u, b0 = k0 / 16 + 2 * q;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        xa.v[j] = k0 + 32 * q + 8 * j < k ? *(const u32x4*)(xrow + k0 + 8 * j) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int f = 0; f < FCG; ++f) {
+        u32x2 lo{0u, 0u}, hi{0u, 0u};
+        uint32_t s = 0;
+        if (b0 < kb) {
+          lo = *(const u32x2_any*)(codes + k0 / 2 + crow[f]);
+          s = scales[k0 / 16 + srow[f]];
+        }
+        if (b0 + 1 < kb) {
+          hi = *(const u32x2_any*)(codes + k0 / 2 + 8 + crow[f]);
+          s |= (uint32_t)scales[k0 / 16 + 1 + srow[f]] << 8;
+        }
+        cur.w[u][f] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        cur.s[u][f] = s;
+      }
+      multiply(cur.w[u], cur.s[u], xa);
+    }
+  }
+  // Accumulator register r of lane l: channel 4 q + r, row c.
+#pragma unroll
+  for (int f = 0; f < FCG; ++f) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[f][r] = token ? acc[f][r] : 0.0f;
+    *(f32x4c*)&part[wave][c][16 * f + 4 * q] = acc[f];
+  }
+  __syncthreads();
+  const int r = tid / FCOLS, o = tid % FCOLS;
+  static_assert(FROWS * FCOLS == 64 * FW, "one output per thread");
+  if (tl.r0 + r >= tl.r1 || o0 + o >= m) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int w = 0; w < FW; ++w) v += part[w][r][o];
+  v *= gs[tl.expert];
+  const int64_t at = (tl.r0 + r) * ldy + o0 + o;
+  if (OUT_BF16) ((__bf16*)Y)[at] = (__bf16)v;
+  else ((float*)Y)[at] = v;
 }
 
 // ---- the gradient of the rows ---------------------------------------------------
@@ -694,7 +886,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grouped_dx_kernel(const uint16_t* 
   using TL = GradTile<NW, RF, CF>;
   __shared__ __attribute__((aligned(1024))) char smem[TL::kLds];
   RowTile tl;
-  if (!find_tile<64 * NW>(off, G, rows, TL::kRows, (k + TL::kCols - 1) / TL::kCols, smem, &tl)) return;
+  if (!find_tile<TL::kRows>(off, G, rows, (uint32_t)((k + TL::kCols - 1) / TL::kCols), &tl)) return;
   for_row_blocks<RF>(tl, [&]<int R>() {
     tile_gradient<NW, R, CF, DMA, OUT_BF16>(smem, tl, dY, m, lddy, codes + tl.expert * m * (k / 2),
                                             scales + tl.expert * m * (k / 16), gs[tl.expert], k, dX, lddx, vec_out != 0);
@@ -715,24 +907,39 @@ hipError_t nvfp4_gemm_grouped_launch(const uint16_t* X, int64_t n, int64_t k, in
                                      const uint8_t* scales, const float* g, int64_t m, void* Y, int out_bf16,
                                      int64_t ldy, hipStream_t s) {
   const int vec = ldy % (out_bf16 ? 8 : 4) == 0 && (uintptr_t)Y % 16 == 0;
-#define NVQ_GROUPED(NW, RF, CF, CR)                                                                                      \
+#define NVQ_LAUNCH(KERNEL, ROWS, COLS, THREADS, ...)                                                                 \
   do {                                                                                                               \
-    using TL = Tile<NW, RF, CF, CR>;                                                                                     \
-    const int64_t blocks = most_tiles(rows, G, TL::kRows, (m + TL::kCols - 1) / TL::kCols);                          \
+    const int64_t blocks = most_tiles(rows, G, ROWS, (m + (COLS)-1) / (COLS));                                       \
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;                                                            \
-    if (out_bf16)                                                                                                    \
-      hipLaunchKernelGGL((grouped_gemm_kernel<NW, RF, CF, CR, 1>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, X, n, k, \
-                         ldx, tok_idx, rows, grp_off, G, codes, scales, g, m, Y, ldy, vec);                          \
-    else                                                                                                             \
-      hipLaunchKernelGGL((grouped_gemm_kernel<NW, RF, CF, CR, 0>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, X, n, k, \
-                         ldx, tok_idx, rows, grp_off, G, codes, scales, g, m, Y, ldy, vec);                          \
+    hipLaunchKernelGGL((KERNEL), dim3((unsigned)blocks), dim3(THREADS), 0, s, X, n, k, ldx, tok_idx, rows, grp_off, G, \
+                       codes, scales, g, m, Y, ldy __VA_OPT__(, ) __VA_ARGS__);                                      \
+    return hipGetLastError();                                                                                        \
   } while (0)
-  const int64_t avg = rows / std::min(rows, G);
-  const int f = avg >= 4 ? 4 : 1;
-  if (f == 4) NVQ_GROUPED(4, 4, 2, 2);
-  else NVQ_GROUPED(4, 1, 1, 3);
-#undef NVQ_GROUPED
-  return hipGetLastError();
+#define NVQ_TILE(RF, CF, CR, FAR)                                                                               \
+  do {                                                                                                          \
+    using TL = Tile<4, RF, CF, CR>;                                                                             \
+    if (out_bf16) NVQ_LAUNCH((grouped_gemm_kernel<4, RF, CF, CR, 1, FAR>), TL::kRows, TL::kCols, 256, vec);     \
+    NVQ_LAUNCH((grouped_gemm_kernel<4, RF, CF, CR, 0, FAR>), TL::kRows, TL::kCols, 256, vec);                   \
+  } while (0)
+  const int64_t used = std::min(rows, G);   // the most experts that can have rows
+  if (((n - 1) * ldx + k) * 2 >= 0xFFFFFF00) NVQ_TILE(4, 2, 2, true);
+  // Times in us, few rows / 64 x 128 tiles / 128 x 256 tiles, measured for
+  // layers of 8 to 256 experts, 1000 to 4096 outputs and 1024 to 4096 inputs.
+  // Few rows: up to about one round of its workgroups on the device (512); 8 rows
+  // on 256 experts 2048 x 4096 15 / 24 / 34, 16 rows 27 / 24 / 35; 12 rows on
+  // 64 experts 2048 x 2048 13 / 14 / 20, 18 rows 16 / 15 / 20.
+  if (most_tiles(rows, G, FROWS, (m + FCOLS - 1) / FCOLS) <= 768) {
+    if (out_bf16) NVQ_LAUNCH(grouped_few_kernel<1>, FROWS, FCOLS, 64 * FW);
+    NVQ_LAUNCH(grouped_few_kernel<0>, FROWS, FCOLS, 64 * FW);
+  }
+  // Large tiles: enough of them for the device, and experts that fill them; 64
+  // experts 2048 x 2048 with 1536 rows - / 54 / 68, 4200 rows - / 82 / 78,
+  // 24594 rows - / 280 / 214; 16 experts 4096 x 1024 with 1024 rows - / 22 / 29,
+  // 2800 rows - / 42 / 34; 8 experts 1024 x 2048 with 3074 rows - / 25 / 32.
+  if (rows >= 32 * used && most_tiles(rows, G, 128, (m + 255) / 256) >= 448) NVQ_TILE(4, 2, 2, false);
+  NVQ_TILE(2, 1, 3, false);
+#undef NVQ_TILE
+#undef NVQ_LAUNCH
 }
 
 hipError_t nvfp4_gemm_grouped_dx_launch(const uint16_t* dY, int64_t rows, int64_t m, int64_t lddy,

@@ -208,7 +208,8 @@ def _check_product(Y, ref, mag, depth, dtype):
 SHAPES = [  # n tokens, rows, G, m, k
     (1, 1, 1, 1, 16), (1, 8, 256, 64, 128), (3, 5, 7, 33, 48), (1, 8, 16, 100, 4096), (20, 64, 5, 130, 272),
     (64, 512, 40, 96, 512), (100, 300, 24, 203, 1040), (300, 900, 3, 256, 384), (257, 257, 1, 512, 2064),
-    (700, 2100, 10, 129, 160), (900, 3600, 6, 320, 544), (1500, 9000, 4, 272, 336), (2048, 8192, 3, 513, 128)]
+    (700, 2100, 10, 129, 160), (900, 3600, 6, 320, 544), (1500, 9000, 4, 272, 336), (2048, 8192, 3, 513, 128),
+    (50, 70, 1000, 40, 64), (40, 1500, 600, 24, 32), (3000, 9001, 70, 1800, 48), (10, 10, 2, 5, 2320)]
 
 
 @pytest.mark.parametrize("n,rows,G,m,k", SHAPES)
@@ -350,6 +351,24 @@ def test_product_wide_weights_and_offsets_out_of_range(nvq):
     off[G], off[3] = 1 << 40, -5
     nvq.nvfp4_gemm_grouped(X, codes, scales, g, off, Y=guard[1:10])
     assert (guard[0] == 7).all() and (guard[10] == 7).all()
+
+
+@pytest.mark.parametrize("rows,m", [(5, 40), (300, 70), (700, 300)])
+def test_product_activations_past_4_gib(nvq, rows, m):
+    # rows of X that lie 2^32 bytes and more behind its start (a wide row stride)
+    rng = np.random.default_rng(rows)
+    G, n, k, ldx = 3, 270, 272, 1 << 23
+    packed, scales, g = _experts(rng, G, m, k)
+    W = moe.experts_matrices(packed, scales, g)
+    X = torch.empty(n, ldx, dtype=torch.bfloat16, device=DEV)[:, :k]
+    X.copy_(torch.from_numpy(rng.standard_normal((n, k)).astype(np.float32)))
+    assert (n - 1) * ldx * 2 > 2 ** 32
+    off = np.array([0, rows // 3, rows - 1, rows], dtype=np.int64)
+    tok = rng.integers(0, n, rows).astype(np.int32)
+    tok[-1], tok[0] = n - 1, 257
+    Y = nvq.nvfp4_gemm_grouped(X, _dev(packed), _dev(scales), _dev(g), _dev(off), tok_idx=_dev(tok))
+    _check_product(Y, moe.grouped_matmul(_np(X), W, off, tok), moe.grouped_matmul(np.abs(_np(X)), np.abs(W), off, tok), k,
+                   torch.float32)
 
 
 # ---- weighted sum -----------------------------------------------------------------
