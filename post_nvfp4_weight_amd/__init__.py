@@ -426,18 +426,40 @@ def _dense(t, name, dtype, shape, dev):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _matrix(t, name, dtypes, shape, dev):
-    """t must be a 2-D tensor of unit column stride (_want's checks); returns its row stride."""
-    _want(t, name, dtypes, shape, dev)
-    rows, cols = t.shape
-    s0, s1 = t.stride()
-    if cols > 1 and s1 != 1:
+def _matrix(t, name, dtypes, dev=None):
+    """(rows, columns, row stride) of a 2-D tensor of unit column stride, of one of dtypes, on device number dev (None: any)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == 2
+            and (dev is None or t.get_device() == dev)):
+        _want(t, name, dtypes, (None, None), dev)
+    (rows, cols), (s0, s1) = t.shape, t.stride()
+    if s1 != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
     if rows <= 1:
-        return cols
+        return rows, cols, cols
     if s0 < cols:
         raise ValueError(f"{name} must not have overlapping rows")
-    return s0
+    return rows, cols, s0
+
+
+def _table(t, name, rows, dev):
+    """Columns of a contiguous int32 tensor [rows, *] (rows None: any) on device number dev."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is _I32 and t.dim() == 2
+            and (rows is None or t.shape[0] == rows) and t.is_contiguous()):
+        _want(t, name, (_I32,), (rows, None), dev)
+        raise ValueError(f"{name} must be contiguous")
+    return t.shape[1]
+
+
+def _output(t, name, like, rows, cols, dtype, dev):
+    """(t, row stride): the caller's output, checked, or a new one beside `like`."""
+    if t is None:
+        if dtype not in _FLOATS:
+            raise TypeError(f"unsupported dtype {dtype}")
+        return like.new_empty((rows, cols), dtype=dtype), cols
+    r, c, ld = _matrix(t, name, _FLOATS, dev)
+    if r != rows or c != cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {(rows, cols)}")
+    return t, ld
 
 
 def _addr(t):
@@ -445,11 +467,12 @@ def _addr(t):
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _call(f, name, dev, *args):
     """The library call on the current stream of device number dev, with that device current."""
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = f(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -462,8 +485,7 @@ def moe_topk(logits, top_k, renorm=True):
     """The router: (ids int32 [T, top_k], weights fp32 [T, top_k]) of logits [T, E] (bf16 or fp32), each token's largest
     logits in falling order (ties: the lower expert) and their softmax weights, over the chosen experts (renorm) or all.
     -inf masks an expert; a slot with no expert left has id -1 and weight 0, a row with a NaN or +inf ids -1 and NaN."""
-    ld = _matrix(logits, "logits", _FLOATS, (None, None), None)
-    T, E = logits.shape
+    T, E, ld = _matrix(logits, "logits", _FLOATS)
     top_k = int(top_k)
     ids = logits.new_empty((T, max(0, top_k)), dtype=_I32)
     weights = logits.new_empty((T, max(0, top_k)), dtype=_F32)
@@ -474,12 +496,9 @@ def moe_topk(logits, top_k, renorm=True):
 
 def moe_topk_backward(logits, ids, weights, dweights, renorm=True):
     """Gradient of moe_topk's weights with respect to the logits: [T, E] in the logits' dtype."""
-    ld = _matrix(logits, "logits", _FLOATS, (None, None), None)
-    T, E = logits.shape
+    T, E, ld = _matrix(logits, "logits", _FLOATS)
     dev = logits.get_device()
-    _want(ids, "ids", (_I32,), (T, None), dev)
-    K = ids.shape[1]
-    _dense(ids, "ids", _I32, (T, K), dev)
+    K = _table(ids, "ids", T, dev)
     _dense(weights, "weights", _F32, (T, K), dev)
     _dense(dweights, "dweights", _F32, (T, K), dev)
     out = logits.new_empty((T, E))
@@ -493,16 +512,17 @@ def moe_sort(ids, n_experts):
     expert e (grp_off[e] <= r < grp_off[e+1]) is token tok_idx[r]; slot (t, s) is row pos[t, s].  Slots whose id is
     outside [0, n_experts) have pos -1, and tok_idx past the last row is -1.  (hessian_accumulate_grouped takes tok_idx
     and grp_off.tolist().)"""
-    _want(ids, "ids", (_I32,), (None, None), None)
-    T, K = ids.shape
-    E = int(n_experts)
+    if not isinstance(ids, torch.Tensor) or not ids.is_cuda:
+        raise ValueError("ids must be a tensor on a HIP device")
     dev = ids.get_device()
-    _dense(ids, "ids", _I32, (T, K), dev)
+    K = _table(ids, "ids", None, dev)
+    T = ids.shape[0]
+    E = int(n_experts)
     tok_idx = ids.new_empty(T * K)
     grp_off = ids.new_empty(max(0, E) + 1, dtype=_I64)
     pos = ids.new_empty((T, K))
     need = lib.moe_sort_workspace_size(T, K, E)
-    ws = _workspace(need, ids.device)
+    ws = _workspace(need, ids.device) if need else None
     _call(lib.moe_sort, "moe_sort", dev, ids.data_ptr(), T, K, E, tok_idx.data_ptr(), grp_off.data_ptr(), pos.data_ptr(), _addr(ws),
           need)
     return tok_idx, grp_off, pos
@@ -524,20 +544,18 @@ def nvfp4_gemm_grouped(X, codes, scales, g, grp_off, tok_idx=None, out_dtype=tor
 
     X: [n, k] bf16; codes [G, m, k/2], scales [G, m, k/16], g [G] as gptq_nvfp4_quantize_batched gives them; grp_off and
     tok_idx from moe_sort (without tok_idx row r of X is row r).  Rows of Y from grp_off[G] on are not written."""
-    ldx = _matrix(X, "X", (_BF16,), (None, None), None)
+    n, kx, ldx = _matrix(X, "X", (_BF16,))
     dev = X.get_device()
     G, m, k = _experts(codes, scales, g, grp_off, dev)
-    n = X.shape[0]
-    if X.shape[1] != k:
-        raise ValueError(f"X has {X.shape[1]} columns, the experts {k} inputs")
+    if kx != k:
+        raise ValueError(f"X has {kx} columns, the experts {k} inputs")
     rows = n
     if tok_idx is not None:
-        _want(tok_idx, "tok_idx", (_I32,), (None,), dev)
+        if not isinstance(tok_idx, torch.Tensor) or tok_idx.dim() != 1:
+            raise ValueError("tok_idx must be a 1-D tensor")
         rows = tok_idx.shape[0]
         _dense(tok_idx, "tok_idx", _I32, (rows,), dev)
-    if Y is None:
-        Y = X.new_empty((rows, m), dtype=out_dtype)
-    ldy = _matrix(Y, "Y", _FLOATS, (rows, m), dev)
+    Y, ldy = _output(Y, "Y", X, rows, m, out_dtype, dev)
     _call(lib.nvfp4_gemm_grouped, "nvfp4_gemm_grouped", dev, X.data_ptr(), NVQ_DTYPE_BF16, n, k, ldx, _addr(tok_idx), rows, grp_off.data_ptr(), G,
           codes.data_ptr(), scales.data_ptr(), g.data_ptr(), m, Y.data_ptr(), _CODES[Y.dtype], ldy)
     return Y
@@ -546,15 +564,12 @@ def nvfp4_gemm_grouped(X, codes, scales, g, grp_off, tok_idx=None, out_dtype=tor
 def nvfp4_gemm_grouped_dx(dY, codes, scales, g, grp_off, out_dtype=torch.float32, dX=None):
     """Gradient of nvfp4_gemm_grouped with respect to its rows: dX[r] = dY[r] dequant(W_e), dY [rows, m] bf16.  The tokens'
     gradient is moe_combine(dX, pos).  Rows from grp_off[G] on are not written."""
-    lddy = _matrix(dY, "dY", (_BF16,), (None, None), None)
+    rows, my, lddy = _matrix(dY, "dY", (_BF16,))
     dev = dY.get_device()
     G, m, k = _experts(codes, scales, g, grp_off, dev)
-    rows = dY.shape[0]
-    if dY.shape[1] != m:
-        raise ValueError(f"dY has {dY.shape[1]} columns, the experts {m} outputs")
-    if dX is None:
-        dX = dY.new_empty((rows, k), dtype=out_dtype)
-    lddx = _matrix(dX, "dX", _FLOATS, (rows, k), dev)
+    if my != m:
+        raise ValueError(f"dY has {my} columns, the experts {m} outputs")
+    dX, lddx = _output(dX, "dX", dY, rows, k, out_dtype, dev)
     _call(lib.nvfp4_gemm_grouped_dx, "nvfp4_gemm_grouped_dx", dev, dY.data_ptr(), NVQ_DTYPE_BF16, rows, m, lddy, grp_off.data_ptr(), G,
           codes.data_ptr(), scales.data_ptr(), g.data_ptr(), k, dX.data_ptr(), _CODES[dX.dtype], lddx)
     return dX
@@ -563,17 +578,13 @@ def nvfp4_gemm_grouped_dx(dY, codes, scales, g, grp_off, out_dtype=torch.float32
 def moe_combine(Y, pos, weights=None, out_dtype=None, out=None):
     """out[t] = sum_s weights[t, s] * Y[pos[t, s]] (weights None: all 1), Y [rows, d] bf16 or fp32, pos int32 and weights
     fp32 [T, K].  A pos outside the rows counts as zeros.  out_dtype None: Y's."""
-    ldy = _matrix(Y, "Y", _FLOATS, (None, None), None)
+    rows, d, ldy = _matrix(Y, "Y", _FLOATS)
     dev = Y.get_device()
-    _want(pos, "pos", (_I32,), (None, None), dev)
-    T, K = pos.shape
-    _dense(pos, "pos", _I32, (T, K), dev)
+    K = _table(pos, "pos", None, dev)
+    T = pos.shape[0]
     if weights is not None:
         _dense(weights, "weights", _F32, (T, K), dev)
-    rows, d = Y.shape
-    if out is None:
-        out = Y.new_empty((T, d), dtype=out_dtype or Y.dtype)
-    ldo = _matrix(out, "out", _FLOATS, (T, d), dev)
+    out, ldo = _output(out, "out", Y, T, d, out_dtype or Y.dtype, dev)
     _call(lib.moe_combine, "moe_combine", dev, Y.data_ptr(), _CODES[Y.dtype], rows, d, ldy, pos.data_ptr(), _addr(weights), T, K,
           out.data_ptr(), _CODES[out.dtype], ldo)
     return out
@@ -582,19 +593,17 @@ def moe_combine(Y, pos, weights=None, out_dtype=None, out=None):
 def moe_combine_backward(dout, Y, pos, weights=None, dY=None):
     """Gradients of moe_combine: (dY [rows, d] in Y's dtype, dweights fp32 [T, K]).  Rows of dY that no slot of pos names
     (past moe_sort's last row) are not written; no row may be named twice."""
-    ldd = _matrix(dout, "dout", _FLOATS, (None, None), None)
+    T, d, ldd = _matrix(dout, "dout", _FLOATS)
     dev = dout.get_device()
-    T, d = dout.shape
-    ldy = _matrix(Y, "Y", _FLOATS, (None, d), dev)
-    _want(pos, "pos", (_I32,), (T, None), dev)
-    K = pos.shape[1]
-    _dense(pos, "pos", _I32, (T, K), dev)
+    rows, dy, ldy = _matrix(Y, "Y", _FLOATS, dev)
+    if dy != d:
+        raise ValueError(f"dout has {d} columns, Y {dy}")
+    K = _table(pos, "pos", T, dev)
     if weights is not None:
         _dense(weights, "weights", _F32, (T, K), dev)
-    rows = Y.shape[0]
-    if dY is None:
-        dY = Y.new_empty((rows, d))
-    lddy = _matrix(dY, "dY", (Y.dtype,), (rows, d), dev)
+    if dY is not None and (not isinstance(dY, torch.Tensor) or dY.dtype is not Y.dtype):
+        raise TypeError("dY must be a tensor of Y's dtype")
+    dY, lddy = _output(dY, "dY", Y, rows, d, Y.dtype, dev)
     dw = dout.new_empty((T, K), dtype=_F32)
     _call(lib.moe_combine_backward, "moe_combine_backward", dev, dout.data_ptr(), _CODES[dout.dtype], T, d, ldd, Y.data_ptr(), _CODES[Y.dtype], rows,
           ldy, pos.data_ptr(), _addr(weights), K, dY.data_ptr(), lddy, dw.data_ptr())

@@ -149,17 +149,18 @@ __device__ __forceinline__ void load_scales(const uint8_t* scales, const uint32_
   }
 }
 
-// NL copies of 1024 bytes to LDS (16 per lane), from `src` + off[q]; offsets at
-// or past the bound bring zeros.
+// Copies q0 .. q1 - 1 of NL, each 1024 bytes to LDS (16 per lane), from `src` +
+// off[q]; offsets at or past the bound bring zeros.
 template <int NL, int STRIDE>
 __device__ __forceinline__ void copy_lds(char* __restrict__ dst, const void* src, uint32_t bound, const uint32_t (&off)[NL],
-                                         bool in) {
+                                         bool in, int q0 = 0, int q1 = NL) {
 #if __HIP_DEVICE_COMPILE__
   __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)src, (short)0, bound, 0x00020000);
 #pragma unroll
   for (int q = 0; q < NL; ++q)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + q * STRIDE), 16,
-                                             in ? off[q] : 0xFFFFFFF0u, 0, 0, 0);
+    if (q >= q0 && q < q1)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + q * STRIDE), 16,
+                                               in ? off[q] : 0xFFFFFFF0u, 0, 0, 0);
 #endif
 }
 
@@ -170,11 +171,12 @@ __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
 // more, which a buffer cannot span; the copies then go by 64-bit addresses.
 template <int NL, int STRIDE, bool FAR>
 __device__ __forceinline__ void copy_x(char* __restrict__ dst, const uint16_t* src, uint32_t bound, const uint32_t (&off)[NL],
-                                       bool in) {
+                                       bool in, int q0 = 0, int q1 = NL) {
 #if __HIP_DEVICE_COMPILE__
   if (FAR) {
 #pragma unroll
     for (int q = 0; q < NL; ++q) {
+      if (q < q0 || q >= q1) continue;
       const void* p = in ? (const void*)((const char*)src + (uint64_t)off[q] * 16) : (const void*)&kZeros;
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
                                        (__attribute__((address_space(3))) void*)(dst + q * STRIDE), 16, 0, 0);
@@ -183,8 +185,9 @@ __device__ __forceinline__ void copy_x(char* __restrict__ dst, const uint16_t* s
     __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)src, (short)0, bound, 0x00020000);
 #pragma unroll
     for (int q = 0; q < NL; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + q * STRIDE), 16,
-                                               in ? off[q] * 16 : 0xFFFFFFF0u, 0, 0, 0);
+      if (q >= q0 && q < q1)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + q * STRIDE), 16,
+                                                 in ? off[q] * 16 : 0xFFFFFFF0u, 0, 0, 0);
   }
 #endif
 }
@@ -251,12 +254,12 @@ __device__ __forceinline__ void product_step(const char* __restrict__ xb, const 
         const float s = j == 0 || j == 3 ? e4m3_byte<0>(s2) : e4m3_byte<1>(s2);
         qa[p ^ 1][f][piece] = dq_byte(word, s, piece);
       }
+      // The copies one by one between the products: issued together, they held
+      // the wave at the full address queue (the gradient at 4099 tokens 250 us
+      // instead of COPY_B).
+      if (j == 0) copy_x<NX, NW * 1024, FAR>(xd, xsrc, xbound, w.xoff, in, i * NX / RF, (i + 1) * NX / RF);
+      if (j == 1 && T == 0) copy_lds<NC, 1024>(cd, csrc, cbound, w.coff, true, i * NC / RF, (i + 1) * NC / RF);
       __builtin_amdgcn_sched_barrier(0);
-      if (j == 0 && i == 0) {
-        copy_x<NX, NW * 1024, FAR>(xd, xsrc, xbound, w.xoff, in);
-        if (T == 0) copy_lds<NC, 1024>(cd, csrc, cbound, w.coff, true);
-        __builtin_amdgcn_sched_barrier(0);
-      }
     }
   }
 #pragma unroll
@@ -698,7 +701,7 @@ __device__ __forceinline__ void gradient_step(const char* __restrict__ yb, const
   for (int j = 0; j < 4; ++j) {
     const int p = j & 1;
     if (j == 0) {
-      // What registers hold of the next step to LDS, then the loads and copies of the step behind it.
+      // What registers hold of the next step to LDS, then the loads of the step behind it.
 #pragma unroll
       for (int b = 0; b < 4; ++b) sw[b * 64] = (char)(sreg >> (8 * b));
       if (!DMA)
@@ -707,9 +710,6 @@ __device__ __forceinline__ void gradient_step(const char* __restrict__ yb, const
       read_grad_codes<CF>(cb, sb, 1, crd, srd, q1);
       __builtin_amdgcn_sched_barrier(0);
       load_next();
-      __builtin_amdgcn_sched_barrier(0);
-      if (DMA) copy_lds<TL::kYLoads, NW * 1024>(yd, ysrc, ybound, yoff, in);
-      copy_lds<NC, NW * 1024>(cd, csrc, cbound, coff, true);
       __builtin_amdgcn_sched_barrier(0);
     }
     if (j == 3) {
@@ -732,6 +732,8 @@ __device__ __forceinline__ void gradient_step(const char* __restrict__ yb, const
         const GradCodes<CF>& c = j == 1 || j == 2 ? q1 : q;
         qa[p ^ 1][f][piece] = dq_pair(c.w[f][v], c.s[f][2 * v + (piece >> 1)], piece);
       }
+      if (DMA && j == 0) copy_lds<TL::kYLoads, NW * 1024>(yd, ysrc, ybound, yoff, in, i * NY / RF, (i + 1) * NY / RF);
+      if (j == 1) copy_lds<NC, NW * 1024>(cd, csrc, cbound, coff, true, i * NC / RF, (i + 1) * NC / RF);
       __builtin_amdgcn_sched_barrier(0);
     }
   }

@@ -70,24 +70,26 @@ struct RowLayout {
   static constexpr int VW = EPL < kMost ? EPL : kMost;
   static __device__ __forceinline__ int index(int lane, int i) { return (i / VW) * (LPT * VW) + lane * VW + i % VW; }
 };
-// The lane's elements as fp32, -inf past E.  VEC: whole vectors (E and the row
-// stride multiples of VW, rows aligned to them).
-template <typename L, int LPT, int EPL, bool VEC>
+// The lane's elements as fp32, -inf past E: whole vectors at any element's
+// address, the row's last elements one by one.
+template <typename L, int LPT, int EPL>
 __device__ __forceinline__ void load_row(const L* row, int E, int lane, float (&v)[EPL]) {
   using R = RowLayout<L, LPT, EPL>;
+  typedef L Vec __attribute__((ext_vector_type(R::VW), aligned(sizeof(L))));
 #pragma unroll
   for (int c = 0; c < EPL / R::VW; ++c) {
     const int e0 = R::index(lane, c * R::VW);
-    if (VEC) {
-      struct alignas(sizeof(L) * R::VW) Vec { L x[R::VW]; };
-      Vec x = {};
-      if (e0 < E) x = *(const Vec*)(row + e0);
+    L x[R::VW];
+    if (e0 + R::VW <= E) {
+      const Vec y = *(const Vec*)(row + e0);
 #pragma unroll
-      for (int i = 0; i < R::VW; ++i) v[c * R::VW + i] = e0 < E ? load_f(&x.x[i]) : -__builtin_inff();
+      for (int i = 0; i < R::VW; ++i) x[i] = y[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < R::VW; ++i) v[c * R::VW + i] = e0 + i < E ? load_f(row + e0 + i) : -__builtin_inff();
+      for (int i = 0; i < R::VW; ++i) x[i] = e0 + i < E ? row[e0 + i] : (L)0;
     }
+#pragma unroll
+    for (int i = 0; i < R::VW; ++i) v[c * R::VW + i] = e0 + i < E ? load_f(&x[i]) : -__builtin_inff();
   }
 }
 
@@ -117,7 +119,7 @@ __device__ __forceinline__ float logit_of(uint32_t k) {
   return PACKED ? __uint_as_float(__float_as_uint(key_value(k)) & 0xFFFF0000u) : key_value(k);
 }
 
-template <typename L, int LPT, int EPL, bool VEC>
+template <typename L, int LPT, int EPL>
 __global__ __launch_bounds__(256) void topk_kernel(const L* __restrict__ logits, int64_t T, int E, int64_t ld, int K,
                                                    int renorm, int32_t* __restrict__ ids,
                                                    float* __restrict__ weights) {
@@ -132,7 +134,7 @@ __global__ __launch_bounds__(256) void topk_kernel(const L* __restrict__ logits,
   bool bad = false;
   {
     float v[EPL];
-    load_row<L, LPT, EPL, VEC>(logits + row * ld, E, lane, v);
+    load_row<L, LPT, EPL>(logits + row * ld, E, lane, v);
     uint32_t own = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -197,7 +199,7 @@ __global__ __launch_bounds__(256) void topk_kernel(const L* __restrict__ logits,
 // all experts, or with renorm the same over the chosen experts only (w_s in
 // the place of p_j).  LPT lanes per token as in topk_kernel; the slots' terms
 // reach their experts' lanes through a row of LDS.
-template <typename L, int LPT, int EPL, bool VEC>
+template <typename L, int LPT, int EPL>
 __global__ __launch_bounds__(256) void topk_backward_kernel(const L* __restrict__ logits, int64_t T, int E, int64_t ld,
                                                             const int32_t* __restrict__ ids,
                                                             const float* __restrict__ weights,
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(256) void topk_backward_kernel(const L* __restrict_
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   float p[EPL], total = 0.0f, top = 0.0f;
   if (!renorm) {
-    load_row<L, LPT, EPL, VEC>(logits + t * ld, E, lane, p);
+    load_row<L, LPT, EPL>(logits + t * ld, E, lane, p);
     uint32_t own = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) own = max(own, order_key(p[i]));   // (a NaN comes out as NaN, or meets one in c)
@@ -243,11 +245,16 @@ __global__ __launch_bounds__(256) void topk_backward_kernel(const L* __restrict_
       const float d = mine[e0 + i];
       r[i] = renorm ? (c != c ? c : d) : p[v * R::VW + i] / total * (d - c);
     }
-    if (VEC) {
-      struct alignas(sizeof(L) * R::VW) Vec { L x[R::VW]; } x;
+    if (e0 + R::VW <= E) {
+      typedef L Vec __attribute__((ext_vector_type(R::VW), aligned(sizeof(L))));
+      Vec x;
 #pragma unroll
-      for (int i = 0; i < R::VW; ++i) store_f(&x.x[i], r[i]);
-      if (e0 < E) *(Vec*)(out + e0) = x;
+      for (int i = 0; i < R::VW; ++i) {
+        L y;
+        store_f(&y, r[i]);
+        x[i] = y;
+      }
+      *(Vec*)(out + e0) = x;
     } else {
 #pragma unroll
       for (int i = 0; i < R::VW; ++i)
@@ -259,44 +266,14 @@ __global__ __launch_bounds__(256) void topk_backward_kernel(const L* __restrict_
 // ---- tokens sorted by expert -----------------------------------------------------
 // A stable counting sort.  Assignment i (token i / K, slot i % K) goes to row
 // base(expert) + the number of earlier assignments of that expert.  Blocks
-// take consecutive chunks of SORT_CHUNK assignments, the waves of a block
-// consecutive parts of its chunk; ranks inside 64 assignments come from ballots
-// over the bits of the expert number, so nothing depends on timing.
-constexpr int SORT_T = 1024, SORT_W = SORT_T / 64, SORT_CHUNK = 8192;
-
-// LDS counts cnt[w][e] of wave w's part [b, e) of the assignments.
-__device__ __forceinline__ void sort_count(const int32_t* ids, int64_t beg, int64_t end, int E, int* cnt) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int i = threadIdx.x; i < SORT_W * E; i += SORT_T) cnt[i] = 0;
-  __syncthreads();
-  for (int64_t i = beg + lane; i < end; i += 64) {
-    const int id = ids[i];
-    if ((unsigned)id < (unsigned)E) atomicAdd(cnt + wave * E + id, 1);   // integer counts: no order
-  }
-  __syncthreads();
-}
-
-// Exclusive sum of v over the SORT_T threads of the block; *total the whole sum.
-__device__ __forceinline__ int block_exclusive(int v, int* part, int* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 63) part[wave] = x;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < SORT_W; ++w) {
-    before += w < wave ? part[w] : 0;
-    all += part[w];
-  }
-  *total = all;
-  return before + x - v;
-}
+// take consecutive chunks of assignments, the waves of a block consecutive
+// parts of its chunk, 64 at a time; ranks inside 64 come from ballots over the
+// bits of the expert number, so nothing depends on timing.
+// Few assignments: one workgroup and launch.  Many: counts per chunk, their
+// sums, and the rows, three launches.  A chunk's rows are first sorted in LDS
+// and leave in runs per expert: written one by one, 4 bytes each, they took
+// the last launch SORT_A us instead of SORT_B (2^21 assignments, 256 experts).
+constexpr int SORT_T = 1024, SORT_W = SORT_T / 64;
 
 // i / K for 0 <= i < 2^31 as a multiplication: with s = ceil(log2 K) and
 // mul = ceil(2^(31 + s) / K), i mul / 2^(31 + s) exceeds i / K by less than
@@ -305,92 +282,162 @@ struct DivK {
   uint32_t mul, shift;
 };
 DivK div_by(uint32_t k) {
-  DivK d{0, 31};
-  while (((uint64_t)1 << (d.shift - 31)) < k) ++d.shift;
-  d.mul = (uint32_t)((((uint64_t)1 << d.shift) + k - 1) / k);
+  DivK d{0, 0};
+  while (((uint64_t)1 << d.shift) < k) ++d.shift;
+  d.mul = (uint32_t)((((uint64_t)1 << (31 + d.shift)) + k - 1) / k);
   return d;
 }
-__device__ __forceinline__ int32_t div_k(int64_t i, DivK d) { return (int32_t)(((uint64_t)i * d.mul) >> d.shift); }
+__device__ __forceinline__ int32_t div_k(int64_t i, DivK d) { return (int32_t)(__umulhi(2 * (uint32_t)i, d.mul) >> d.shift); }
 
-// cnt[w][e] holds the row of wave w's next assignment of expert e.
-__device__ __forceinline__ void sort_place(const int32_t* ids, int64_t beg, int64_t end, DivK K, int E, int* cnt,
-                                           int32_t* tok_idx, int32_t* pos) {
+// Inclusive sum over the wave's lanes (row shifts, then the rows' last lanes to the rows behind).
+__device__ __forceinline__ int wave_inclusive(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
+// Exclusive sums of N values per expert over the threads x < E (thread = expert),
+// in place, and the whole sums in total; the waves past E only join the barrier.
+template <int N>
+__device__ __forceinline__ void expert_sums(int E, int (&v)[N], int (&total)[N], int (*part)[SORT_W]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = (E + 63) / 64;
+  int incl[N];
+  if (wave < nw) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      incl[i] = wave_inclusive(v[i]);
+      if (lane == 63) part[i][wave] = incl[i];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) total[i] = 0;
+  int before[N] = {};
+  for (int w = 0; w < nw; ++w)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = part[i][w];
+      before[i] += w < wave ? p : 0;
+      total[i] += p;
+    }
+  if (wave < nw) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = before[i] + incl[i] - v[i];
+  }
+}
+
+// Loads the wave's part of a chunk that starts at beg and ends before end (n of
+// the call at most): assignment 64 u + lane of the part in id[u], -1 for none;
+// and counts it per expert into cnt[wave][e] (LDS).
+template <int PER>
+__device__ __forceinline__ void sort_count(const int32_t* __restrict__ ids, int64_t beg, int64_t end, int E, int* cnt,
+                                           int (&id)[PER]) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const int64_t i = beg + (wave * PER + u) * 64 + lane;
+    const int x = i < end ? ids[i] : -1;
+    id[u] = (unsigned)x < (unsigned)E ? x : -1;
+  }
+  for (int i = threadIdx.x; i < SORT_W * E; i += SORT_T) cnt[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < PER; ++u)
+    if (id[u] >= 0) atomicAdd(cnt + wave * E + id[u], 1);   // integer counts: no order
+  __syncthreads();
+}
+
+// Of the thread's expert: the counts of the waves, their sum in the return value ...
+__device__ __forceinline__ int wave_counts(int E, const int* cnt, int (&c)[SORT_W]) {
+  int sum = 0;
+  if ((int)threadIdx.x < E)
+#pragma unroll
+    for (int w = 0; w < SORT_W; ++w) sum += c[w] = cnt[w * E + threadIdx.x];
+  return sum;
+}
+// ... and the waves' first places, from the expert's first one on.
+__device__ __forceinline__ void wave_bases(int E, int* cnt, const int (&c)[SORT_W], int first) {
+  if ((int)threadIdx.x < E)
+#pragma unroll
+    for (int w = 0; w < SORT_W; ++w) {
+      cnt[w * E + threadIdx.x] = first;
+      first += c[w];
+    }
+}
+
+// place(u, at): the place among the counted ones of each assignment (id[u] >= 0), by wave, in order.
+template <int PER, typename F>
+__device__ __forceinline__ void sort_rank(const int (&id)[PER], int E, int* cnt, F place) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   int bits = 1;
   while ((1 << bits) < E) ++bits;
   int* base = cnt + wave * E;
-  for (int64_t i0 = beg; i0 < end; i0 += 64) {
-    const int64_t i = i0 + lane;
-    int id = i < end ? ids[i] : -1;
-    const bool ok = (unsigned)id < (unsigned)E;
-    if (!ok) id = 0;
-    unsigned long long same = __ballot(ok);
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const bool ok = id[u] >= 0;
+    const int x = ok ? id[u] : 0;
+    const uint64_t some = __ballot(ok);
+    uint32_t lo = (uint32_t)some, hi = (uint32_t)(some >> 32);   // the lanes with the lane's expert
     for (int b = 0; b < bits; ++b) {
-      const unsigned long long m = __ballot((id >> b) & 1);
-      same &= ((id >> b) & 1) ? m : ~m;
+      const int t = (int)((uint32_t)x << (31 - b)) >> 31;        // all ones where the bit is set
+      const uint64_t m = __ballot(t != 0);
+      lo &= ~((uint32_t)m ^ (uint32_t)t);
+      hi &= ~((uint32_t)(m >> 32) ^ (uint32_t)t);
     }
-    const int rank = __popcll(same & ((1ull << lane) - 1));
-    int row = -1;
-    if (ok) row = base[id] + rank;
+    const int rank = __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0));   // of them, below the lane
+    const int at = ok ? base[x] + rank : -1;
     // Every lane has read its base before one lane per expert moves it on, and
     // reads it anew in the next turn (LDS operations of a wave run in order).
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (ok && rank == 0) base[id] += __popcll(same);
+    if (ok && rank == 0) base[x] = at + __popc(lo) + __popc(hi);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (i < end) {
-      pos[i] = row;
-      if (ok) tok_idx[row] = div_k(i, K);
-    }
+    place(u, at);
   }
 }
 
-__device__ __forceinline__ void wave_part(int64_t beg, int64_t end, int64_t* b, int64_t* e) {
-  const int64_t n = end - beg;
-  const int64_t per = ((n + SORT_W - 1) / SORT_W + 63) / 64 * 64;
-  const int wave = threadIdx.x >> 6;
-  *b = std::min<int64_t>(end, beg + wave * per);
-  *e = std::min<int64_t>(end, *b + per);
-}
-
 // Few assignments: one workgroup does it all.
+template <int PER>
 __global__ __launch_bounds__(SORT_T) void sort_small_kernel(const int32_t* __restrict__ ids, int64_t n, DivK K, int E,
                                                             int32_t* __restrict__ tok_idx, int64_t* __restrict__ grp_off,
                                                             int32_t* __restrict__ pos) {
   extern __shared__ int cnt[];   // SORT_W * E
-  __shared__ int part[SORT_W];
-  int64_t b, e;
-  wave_part(0, n, &b, &e);
-  sort_count(ids, b, e, E, cnt);
-  const int x = threadIdx.x;
-  int mine = 0, total;
-  if (x < E)
-    for (int w = 0; w < SORT_W; ++w) mine += cnt[w * E + x];
-  int run = block_exclusive(mine, part, &total);
-  if (x < E) {
-    grp_off[x] = run;
-    for (int w = 0; w < SORT_W; ++w) {
-      const int c = cnt[w * E + x];
-      cnt[w * E + x] = run;
-      run += c;
-    }
-  }
-  if (x == 0) grp_off[E] = total;
+  __shared__ int part[1][SORT_W];
+  int id[PER], c[SORT_W], sum[1], all[1];
+  sort_count<PER>(ids, 0, n, E, cnt, id);
+  sum[0] = wave_counts(E, cnt, c);
+  expert_sums<1>(E, sum, all, part);
+  wave_bases(E, cnt, c, sum[0]);
+  const int total = all[0];
+  if ((int)threadIdx.x < E) grp_off[threadIdx.x] = sum[0];
+  if (threadIdx.x == 0) grp_off[E] = total;
   __syncthreads();
-  sort_place(ids, b, e, K, E, cnt, tok_idx, pos);
-  for (int64_t i = total + x; i < n; i += SORT_T) tok_idx[i] = -1;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  sort_rank<PER>(id, E, cnt, [&](int u, int at) {
+    const int64_t i = (wave * PER + u) * 64 + lane;
+    if (i < n) pos[i] = at;
+    if (at >= 0) tok_idx[at] = div_k(i, K);
+  });
+  for (int64_t i = total + (int)threadIdx.x; i < n; i += SORT_T) tok_idx[i] = -1;
 }
 
 // Many: counts of each chunk [nb][E] ...
+template <int PER>
 __global__ __launch_bounds__(SORT_T) void sort_hist_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
                                                            int32_t* __restrict__ hist) {
   extern __shared__ int cnt[];   // E
+  const int64_t beg = (int64_t)blockIdx.x * (SORT_T * PER) + threadIdx.x;
+  int id[PER];
+#pragma unroll
+  for (int u = 0; u < PER; ++u) id[u] = beg + u * SORT_T < n ? ids[beg + u * SORT_T] : -1;
   for (int i = threadIdx.x; i < E; i += SORT_T) cnt[i] = 0;
   __syncthreads();
-  const int64_t beg = (int64_t)blockIdx.x * SORT_CHUNK, end = std::min<int64_t>(n, beg + SORT_CHUNK);
-  for (int64_t i = beg + threadIdx.x; i < end; i += SORT_T) {
-    const int id = ids[i];
-    if ((unsigned)id < (unsigned)E) atomicAdd(cnt + id, 1);
-  }
+#pragma unroll
+  for (int u = 0; u < PER; ++u)
+    if ((unsigned)id[u] < (unsigned)E) atomicAdd(cnt + id[u], 1);
   __syncthreads();
   for (int i = threadIdx.x; i < E; i += SORT_T) hist[(int64_t)blockIdx.x * E + i] = cnt[i];
 }
@@ -436,54 +483,73 @@ __global__ __launch_bounds__(SORT_T) void sort_scan_kernel(int32_t* __restrict__
   if (wave == 0) total[e] = all;
 }
 
-// ... and the rows.
+// ... and the rows: the chunk's places in LDS first, then each place's row is
+// its expert's shift (row of the chunk's first one of the expert - its place) away.
+template <int PER>
 __global__ __launch_bounds__(SORT_T) void sort_place_kernel(const int32_t* __restrict__ ids, int64_t n, DivK K, int E,
                                                             const int32_t* __restrict__ hist,
                                                             const int32_t* __restrict__ total,
                                                             int32_t* __restrict__ tok_idx,
                                                             int64_t* __restrict__ grp_off, int32_t* __restrict__ pos) {
-  extern __shared__ int cnt[];   // SORT_W * E
-  __shared__ int part[SORT_W];
-  const int64_t beg = (int64_t)blockIdx.x * SORT_CHUNK, end = std::min<int64_t>(n, beg + SORT_CHUNK);
-  int64_t b, e;
-  wave_part(beg, end, &b, &e);
-  sort_count(ids, b, e, E, cnt);
-  const int x = threadIdx.x;
-  int all;
-  const int off = block_exclusive(x < E ? total[x] : 0, part, &all);
+  extern __shared__ int cnt[];   // SORT_W * E, then E shifts
+  __shared__ int part[2][SORT_W];
+  __shared__ int32_t tok[SORT_T * PER];
+  __shared__ uint16_t expert[SORT_T * PER];
+  int* shift = cnt + SORT_W * E;
+  const int64_t beg = (int64_t)blockIdx.x * (SORT_T * PER), end = std::min<int64_t>(n, beg + SORT_T * PER);
+  const int x = threadIdx.x, wave = x >> 6, lane = x & 63;
+  int id[PER], c[SORT_W], sum[2], all[2];
+  sum[0] = x < E ? total[x] : 0;
+  const int before = x < E ? hist[(int64_t)blockIdx.x * E + x] : 0;
+  sort_count<PER>(ids, beg, end, E, cnt, id);
+  sum[1] = wave_counts(E, cnt, c);
+  expert_sums<2>(E, sum, all, part);   // the experts' first rows, and their first places in the chunk
+  wave_bases(E, cnt, c, sum[1]);
   if (x < E) {
-    int run = off + hist[(int64_t)blockIdx.x * E + x];
-    for (int w = 0; w < SORT_W; ++w) {
-      const int c = cnt[w * E + x];
-      cnt[w * E + x] = run;
-      run += c;
-    }
-    if (blockIdx.x == 0) grp_off[x] = off;
+    shift[x] = sum[0] + before - sum[1];
+    if (blockIdx.x == 0) grp_off[x] = sum[0];
   }
-  if (blockIdx.x == 0 && x == 0) grp_off[E] = all;
+  if (blockIdx.x == 0 && x == 0) grp_off[E] = all[0];
   __syncthreads();
-  sort_place(ids, b, e, K, E, cnt, tok_idx, pos);
+  sort_rank<PER>(id, E, cnt, [&](int u, int at) {
+    const int64_t i = beg + (wave * PER + u) * 64 + lane;
+    if (i < end) pos[i] = at >= 0 ? at + shift[id[u]] : -1;
+    if (at >= 0) {
+      tok[at] = div_k(i, K);
+      expert[at] = (uint16_t)id[u];
+    }
+  });
+  __syncthreads();
+  for (int i = x; i < all[1]; i += SORT_T) tok_idx[i + shift[expert[i]]] = tok[i];
   for (int64_t i = beg + x; i < end; i += SORT_T)
-    if (i >= all) tok_idx[i] = -1;
+    if (i >= all[0]) tok_idx[i] = -1;
 }
 
 // ---- a token's experts summed ------------------------------------------------------
-// Elements move in vectors of VW (16 bytes of the wider type when rows and
-// strides allow it, else one).
-template <typename E, int VW>
-struct alignas(sizeof(E) * VW) VecOf { E x[VW]; };
+// Elements move in vectors of VW (16 bytes of the wider type), at any element's
+// address (the device loads and stores them whole); the columns behind the last
+// whole vector one by one.
 template <typename E, int VW>
 __device__ __forceinline__ void load_vec(const E* p, float (&v)[VW]) {
-  const VecOf<E, VW> x = *(const VecOf<E, VW>*)p;
+  typedef E Vec __attribute__((ext_vector_type(VW), aligned(sizeof(E))));
+  const Vec x = *(const Vec*)p;
 #pragma unroll
-  for (int i = 0; i < VW; ++i) v[i] = load_f(&x.x[i]);
+  for (int i = 0; i < VW; ++i) {
+    const E e = x[i];
+    v[i] = load_f(&e);
+  }
 }
 template <typename E, int VW>
 __device__ __forceinline__ void store_vec(E* p, const float (&v)[VW]) {
-  VecOf<E, VW> x;
+  typedef E Vec __attribute__((ext_vector_type(VW), aligned(sizeof(E))));
+  Vec x;
 #pragma unroll
-  for (int i = 0; i < VW; ++i) store_f(&x.x[i], v[i]);
-  *(VecOf<E, VW>*)p = x;
+  for (int i = 0; i < VW; ++i) {
+    E e;
+    store_f(&e, v[i]);
+    x[i] = e;
+  }
+  *(Vec*)p = x;
 }
 
 // One thread per vector of a token's columns: blockDim = (columns, tokens).
@@ -491,42 +557,46 @@ __device__ __forceinline__ void store_vec(E* p, const float (&v)[VW]) {
 // reading the rows once: COMBINE_NOTE
 constexpr int KC = 8;
 template <typename Y, typename O, int VW>
-__global__ __launch_bounds__(256) void combine_kernel(const Y* __restrict__ y, int64_t rows, int64_t nv, int64_t ldy,
+__global__ __launch_bounds__(256) void combine_kernel(const Y* __restrict__ y, int64_t rows, int64_t d, int64_t ldy,
                                                       const int32_t* __restrict__ pos, const float* __restrict__ w,
                                                       int64_t T, int K, O* __restrict__ out, int64_t ldo,
                                                       int col_blocks) {
   const int64_t v = (int64_t)(blockIdx.x % col_blocks) * blockDim.x + threadIdx.x;
   const int64_t t = (int64_t)(blockIdx.x / col_blocks) * blockDim.y +
                     __builtin_amdgcn_readfirstlane(threadIdx.y);   // the same in a whole wave: blockDim.x is 64 or more
-  if (v >= nv || t >= T) return;
-  const int64_t c = v * VW;
-  float sum[VW];
+  if (v * VW >= d || t >= T) return;
+  auto columns = [&]<int W>(int64_t c) {
+    float sum[W];
 #pragma unroll
-  for (int i = 0; i < VW; ++i) sum[i] = 0.0f;
-  for (int s0 = 0; s0 < K; s0 += KC) {
-    float wt[KC], x[KC][VW];
+    for (int i = 0; i < W; ++i) sum[i] = 0.0f;
+    for (int s0 = 0; s0 < K; s0 += KC) {
+      float wt[KC], x[KC][W];
 #pragma unroll
-    for (int j = 0; j < KC; ++j) {
-      const int64_t i = t * K + s0 + j;
-      const int64_t r = s0 + j < K ? pos[i] : -1;
-      wt[j] = s0 + j < K ? (w ? w[i] : 1.0f) : 0.0f;
+      for (int j = 0; j < KC; ++j) {
+        const int64_t i = t * K + s0 + j;
+        const int64_t r = s0 + j < K ? pos[i] : -1;
+        wt[j] = s0 + j < K ? (w ? w[i] : 1.0f) : 0.0f;
 #pragma unroll
-      for (int q = 0; q < VW; ++q) x[j][q] = 0.0f;
-      if ((uint64_t)r < (uint64_t)rows) load_vec<Y, VW>(y + r * ldy + c, x[j]);
+        for (int q = 0; q < W; ++q) x[j][q] = 0.0f;
+        if ((uint64_t)r < (uint64_t)rows) load_vec<Y, W>(y + r * ldy + c, x[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < KC; ++j)
+#pragma unroll
+        for (int q = 0; q < W; ++q) sum[q] = fmaf(wt[j], x[j][q], sum[q]);
     }
-#pragma unroll
-    for (int j = 0; j < KC; ++j)
-#pragma unroll
-      for (int q = 0; q < VW; ++q) sum[q] = fmaf(wt[j], x[j][q], sum[q]);
-  }
-  store_vec<O, VW>(out + t * ldo + c, sum);
+    store_vec<O, W>(out + t * ldo + c, sum);
+  };
+  if (v * VW + VW <= d) columns.template operator()<VW>(v * VW);
+  else
+    for (int64_t c = v * VW; c < d; ++c) columns.template operator()<1>(c);
 }
 
 // Its gradients: a workgroup of NW waves per token, dout's row read once for
 // KC slots at a time; each lane sums its columns' products, then lanes and
 // waves are added in a fixed order.
 template <typename G, typename Y, int VW, int NW>
-__global__ __launch_bounds__(64 * NW) void combine_backward_kernel(const G* __restrict__ dout, int64_t T, int64_t nv,
+__global__ __launch_bounds__(64 * NW) void combine_backward_kernel(const G* __restrict__ dout, int64_t T, int64_t d,
                                                                    int64_t ldd, const Y* __restrict__ y, int64_t rows,
                                                                    int64_t ldy, const int32_t* __restrict__ pos,
                                                                    const float* __restrict__ w, int K,
@@ -536,75 +606,75 @@ __global__ __launch_bounds__(64 * NW) void combine_backward_kernel(const G* __re
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = blockIdx.x;
   for (int s0 = 0; s0 < K; s0 += KC) {
-    int64_t r[KC];
+    int r[KC];
     float wt[KC], dot[KC];
 #pragma unroll
     for (int j = 0; j < KC; ++j) {
       const int64_t i = t * K + s0 + j;
       r[j] = s0 + j < K ? pos[i] : -1;
-      if ((uint64_t)r[j] >= (uint64_t)rows) r[j] = -1;
+      if (r[j] >= rows) r[j] = -1;
       wt[j] = s0 + j < K ? (w ? w[i] : 1.0f) : 0.0f;
       dot[j] = 0.0f;
     }
-    for (int64_t v = threadIdx.x; v < nv; v += 64 * NW) {
-      const int64_t c = v * VW;
-      float g[VW], x[KC][VW];
-      load_vec<G, VW>(dout + t * ldd + c, g);
+    auto columns = [&]<int W>(int64_t c) {
+      float g[W], x[KC][W];
+      load_vec<G, W>(dout + t * ldd + c, g);
       if (dw) {
 #pragma unroll
         for (int j = 0; j < KC; ++j) {
 #pragma unroll
-          for (int q = 0; q < VW; ++q) x[j][q] = 0.0f;
-          if (r[j] >= 0) load_vec<Y, VW>(y + r[j] * ldy + c, x[j]);
+          for (int q = 0; q < W; ++q) x[j][q] = 0.0f;
+          if (r[j] >= 0) load_vec<Y, W>(y + (int64_t)r[j] * ldy + c, x[j]);
         }
 #pragma unroll
         for (int j = 0; j < KC; ++j)
           if (r[j] >= 0) {
 #pragma unroll
-            for (int q = 0; q < VW; ++q) dot[j] = fmaf(g[q], x[j][q], dot[j]);
+            for (int q = 0; q < W; ++q) dot[j] = fmaf(g[q], x[j][q], dot[j]);
           }
       }
       if (dy)
 #pragma unroll
         for (int j = 0; j < KC; ++j)
           if (r[j] >= 0) {
-            float o[VW];
+            float o[W];
 #pragma unroll
-            for (int q = 0; q < VW; ++q) o[q] = wt[j] * g[q];
-            store_vec<Y, VW>(dy + r[j] * lddy + c, o);
+            for (int q = 0; q < W; ++q) o[q] = wt[j] * g[q];
+            store_vec<Y, W>(dy + (int64_t)r[j] * lddy + c, o);
           }
+    };
+    for (int64_t c = (int64_t)threadIdx.x * VW; c < d; c += 64 * NW * VW) {
+      if (c + VW <= d) columns.template operator()<VW>(c);
+      else
+        for (int64_t e = c; e < d; ++e) columns.template operator()<1>(e);
     }
     if (!dw) continue;
 #pragma unroll
     for (int j = 0; j < KC; ++j) {
-      const float d = group_sum<64>(dot[j]);
-      if (lane == 0) part[wave][j] = d;
+      const float sum = group_sum<64>(dot[j]);
+      if (lane == 0) part[wave][j] = sum;
     }
     __syncthreads();
     if (threadIdx.x < KC && s0 + (int)threadIdx.x < K) {
-      float d = 0.0f;
+      float sum = 0.0f;
 #pragma unroll
-      for (int x = 0; x < NW; ++x) d += part[x][threadIdx.x];
-      dw[t * K + s0 + threadIdx.x] = d;
+      for (int x = 0; x < NW; ++x) sum += part[x][threadIdx.x];
+      dw[t * K + s0 + threadIdx.x] = sum;
     }
     __syncthreads();
   }
 }
 
-// Calls f(LPT, EPL, VEC) with the constants for E experts in rows whose start
-// and stride are multiples of `unit` elements: 16 lanes per token when there
-// are tokens enough to fill the device that way, at most 256 experts and 16 slots.
+// Calls f(LPT, EPL) with the constants for E experts: 16 lanes per token when
+// there are tokens enough to fill the device that way, at most 256 experts and 16 slots.
 constexpr int64_t kTopkWaves = 8192;   // tokens from which 16 lanes per token are taken
-template <typename L, typename F>
-hipError_t topk_dispatch(int64_t T, int E, int K, uintptr_t addr, int64_t ld, F f) {
-  const bool row16 = T >= kTopkWaves && E <= 256 && K <= 16;
-  const int lanes = row16 ? 16 : 64;
+template <typename F>
+hipError_t topk_dispatch(int64_t T, int E, int K, F f) {
+  const int lanes = T >= kTopkWaves && E <= 256 && K <= 16 ? 16 : 64;
   int epl = 1;
   while (epl * lanes < E) epl *= 2;
-  const int vw = std::min<int>(epl, 16 / (int)sizeof(L));
-  const bool vec = E % vw == 0 && ld % vw == 0 && addr % (vw * sizeof(L)) == 0;
 #define NVQ_TOPK_CASE(LPT, EPL) \
-  if (lanes == LPT && epl == EPL) return vec ? f.template operator()<LPT, EPL, true>() : f.template operator()<LPT, EPL, false>()
+  if (lanes == LPT && epl == EPL) return f.template operator()<LPT, EPL>()
   NVQ_TOPK_CASE(16, 1);
   NVQ_TOPK_CASE(16, 2);
   NVQ_TOPK_CASE(16, 4);
@@ -622,10 +692,10 @@ hipError_t topk_dispatch(int64_t T, int E, int K, uintptr_t addr, int64_t ld, F 
 template <typename L>
 hipError_t topk_run(const L* logits, int64_t T, int E, int64_t ld, int K, int renorm, int32_t* ids, float* weights,
                     hipStream_t s) {
-  return topk_dispatch<L>(T, E, K, (uintptr_t)logits, ld, [&]<int LPT, int EPL, bool VEC>() {
+  return topk_dispatch(T, E, K, [&]<int LPT, int EPL>() {
     const int64_t per = 256 / LPT;
-    hipLaunchKernelGGL((topk_kernel<L, LPT, EPL, VEC>), dim3((unsigned)((T + per - 1) / per)), dim3(256), 0, s, logits,
-                       T, E, ld, K, renorm, ids, weights);
+    hipLaunchKernelGGL((topk_kernel<L, LPT, EPL>), dim3((unsigned)((T + per - 1) / per)), dim3(256), 0, s, logits, T, E, ld,
+                       K, renorm, ids, weights);
     return hipGetLastError();
   });
 }
@@ -633,16 +703,19 @@ hipError_t topk_run(const L* logits, int64_t T, int E, int64_t ld, int K, int re
 template <typename L>
 hipError_t topk_backward_run(const L* logits, int64_t T, int E, int64_t ld, const int32_t* ids, const float* w,
                              const float* dw, int K, int renorm, L* dl, int64_t ldd, hipStream_t s) {
-  return topk_dispatch<L>(T, E, K, (uintptr_t)logits | (uintptr_t)dl, ld | ldd, [&]<int LPT, int EPL, bool VEC>() {
+  return topk_dispatch(T, E, K, [&]<int LPT, int EPL>() {
     const int64_t per = 256 / LPT;
-    hipLaunchKernelGGL((topk_backward_kernel<L, LPT, EPL, VEC>), dim3((unsigned)((T + per - 1) / per)), dim3(256), 0, s,
-                       logits, T, E, ld, ids, w, dw, K, renorm, dl, ldd);
+    hipLaunchKernelGGL((topk_backward_kernel<L, LPT, EPL>), dim3((unsigned)((T + per - 1) / per)), dim3(256), 0, s, logits,
+                       T, E, ld, ids, w, dw, K, renorm, dl, ldd);
     return hipGetLastError();
   });
 }
 
-int64_t sort_blocks(int64_t n) { return (n + SORT_CHUNK - 1) / SORT_CHUNK; }
-constexpr int64_t kSortSmall = 16384;   // assignments up to which one workgroup sorts
+// Assignments up to which one workgroup sorts (8192 of them, 256 experts: one
+// workgroup 10.9 us, three launches 12.3), and from which chunks are 8192 long (below: 4096).
+constexpr int64_t kSortSmall = 8 * SORT_T, kSortLarge = (int64_t)1 << 20;
+int sort_per(int64_t n) { return n >= kSortLarge ? 8 : 4; }
+int64_t sort_blocks(int64_t n) { return (n + SORT_T * sort_per(n) - 1) / (SORT_T * sort_per(n)); }
 
 }  // namespace
 
@@ -668,68 +741,65 @@ size_t moe_sort_workspace(int64_t n, int64_t E) {
 hipError_t moe_sort_launch(const int32_t* ids, int64_t n, int K, int64_t E, int32_t* tok_idx, int64_t* grp_off,
                            int32_t* pos, void* ws, hipStream_t s) {
   const size_t lds = (size_t)SORT_W * E * sizeof(int);
+  const DivK div = div_by((uint32_t)K);
+#define NVQ_SORT(PER)                                                                                                   \
+  hipLaunchKernelGGL(sort_small_kernel<PER>, dim3(1), dim3(SORT_T), lds, s, ids, n, div, (int)E, tok_idx, grp_off, pos)
   if (n <= kSortSmall) {
-    hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(SORT_T), lds, s, ids, n, div_by(K), (int)E, tok_idx, grp_off, pos);
+    if (n <= SORT_T) NVQ_SORT(1);
+    else if (n <= 4 * SORT_T) NVQ_SORT(4);
+    else NVQ_SORT(8);
     return hipGetLastError();
   }
+#undef NVQ_SORT
   const int nb = (int)sort_blocks(n);
   int32_t* hist = (int32_t*)ws;
   int32_t* total = hist + (int64_t)nb * E;
-  hipLaunchKernelGGL(sort_hist_kernel, dim3(nb), dim3(SORT_T), E * sizeof(int), s, ids, n, (int)E, hist);
-  hipLaunchKernelGGL(sort_scan_kernel, dim3((unsigned)((E + 63) / 64)), dim3(SORT_T), 0, s, hist, nb, (int)E, total);
-  hipLaunchKernelGGL(sort_place_kernel, dim3(nb), dim3(SORT_T), lds, s, ids, n, div_by(K), (int)E, hist, total, tok_idx,
-                     grp_off, pos);
+#define NVQ_SORT(PER)                                                                                                  \
+  do {                                                                                                                 \
+    hipLaunchKernelGGL(sort_hist_kernel<PER>, dim3(nb), dim3(SORT_T), E * sizeof(int), s, ids, n, (int)E, hist);        \
+    hipLaunchKernelGGL(sort_scan_kernel, dim3((unsigned)((E + 63) / 64)), dim3(SORT_T), 0, s, hist, nb, (int)E, total); \
+    hipLaunchKernelGGL(sort_place_kernel<PER>, dim3(nb), dim3(SORT_T), lds + E * sizeof(int), s, ids, n, div, (int)E,    \
+                       hist, total, tok_idx, grp_off, pos);                                                            \
+  } while (0)
+  if (sort_per(n) == 8) NVQ_SORT(8);
+  else NVQ_SORT(4);
+#undef NVQ_SORT
   return hipGetLastError();
-}
-
-// Elements per vector: 16 bytes of the wider type if every row starts on a
-// multiple of it and the columns are whole vectors, else 1.
-static int vec_width(bool bf16_only, int64_t d, int64_t strides, uintptr_t bf16_addr, uintptr_t f32_addr) {
-  const int vw = bf16_only ? 8 : 4;
-  return d % vw == 0 && strides % vw == 0 && bf16_addr % (2 * vw) == 0 && f32_addr % (4 * vw) == 0 ? vw : 1;
 }
 
 hipError_t moe_combine_launch(const void* Y, int y_bf16, int64_t rows, int64_t d, int64_t ldy, const int32_t* pos,
                               const float* weights, int64_t T, int K, void* out, int out_bf16, int64_t ldo,
                               hipStream_t s) {
-  const int vw = vec_width(y_bf16 && out_bf16, d, ldy | ldo, (y_bf16 ? (uintptr_t)Y : 0) | (out_bf16 ? (uintptr_t)out : 0),
-                           (y_bf16 ? 0 : (uintptr_t)Y) | (out_bf16 ? 0 : (uintptr_t)out));
-  const int64_t nv = d / vw;
+  const int vw = y_bf16 && out_bf16 ? 8 : 4;
+  const int64_t nv = (d + vw - 1) / vw;
   int bx = 64;   // columns of a workgroup; at least a wave, so that a wave's slots are uniform
   while (bx < 256 && bx < nv) bx *= 2;
   const int by = 256 / bx;
   const int64_t cb = (nv + bx - 1) / bx, blocks = cb * ((T + by - 1) / by);
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(bx, by);
-#define NVQ_COMBINE(YT, OT, VW)                                                                                    \
-  hipLaunchKernelGGL((combine_kernel<YT, OT, VW>), grid, block, 0, s, (const YT*)Y, rows, nv, ldy, pos, weights, T, K, \
+#define NVQ_COMBINE(YT, OT, VW)                                                                                   \
+  hipLaunchKernelGGL((combine_kernel<YT, OT, VW>), grid, block, 0, s, (const YT*)Y, rows, d, ldy, pos, weights, T, K, \
                      (OT*)out, ldo, (int)cb)
-  if (y_bf16 && out_bf16) {
-    if (vw > 1) NVQ_COMBINE(uint16_t, uint16_t, 8);
-    else NVQ_COMBINE(uint16_t, uint16_t, 1);
-  } else if (y_bf16) {
-    if (vw > 1) NVQ_COMBINE(uint16_t, float, 4);
-    else NVQ_COMBINE(uint16_t, float, 1);
-  } else if (out_bf16) {
-    if (vw > 1) NVQ_COMBINE(float, uint16_t, 4);
-    else NVQ_COMBINE(float, uint16_t, 1);
-  } else {
-    if (vw > 1) NVQ_COMBINE(float, float, 4);
-    else NVQ_COMBINE(float, float, 1);
-  }
+  if (y_bf16 && out_bf16) NVQ_COMBINE(uint16_t, uint16_t, 8);
+  else if (y_bf16) NVQ_COMBINE(uint16_t, float, 4);
+  else if (out_bf16) NVQ_COMBINE(float, uint16_t, 4);
+  else NVQ_COMBINE(float, float, 4);
 #undef NVQ_COMBINE
   return hipGetLastError();
 }
 
 template <typename G, typename Y, int VW>
-static hipError_t combine_backward_run(const G* dout, int64_t T, int64_t nv, int64_t ldd, const Y* y, int64_t rows,
+static hipError_t combine_backward_run(const G* dout, int64_t T, int64_t d, int64_t ldd, const Y* y, int64_t rows,
                                        int64_t ldy, const int32_t* pos, const float* w, int K, Y* dy, int64_t lddy,
                                        float* dw, hipStream_t s) {
-#define NVQ_COMBINE_BWD(NW)                                                                                         \
-  hipLaunchKernelGGL((combine_backward_kernel<G, Y, VW, NW>), dim3((unsigned)T), dim3(64 * NW), 0, s, dout, T, nv, ldd, \
-                     y, rows, ldy, pos, w, K, dy, lddy, dw)
-  // one wave per token once the tokens fill the device; more for few tokens with long rows
-  if (T >= 4096 || nv <= 64) NVQ_COMBINE_BWD(1);
+#define NVQ_COMBINE_BWD(NW)                                                                                            \
+  hipLaunchKernelGGL((combine_backward_kernel<G, Y, VW, NW>), dim3((unsigned)T), dim3(64 * NW), 0, s, dout, T, d, ldd, y, \
+                     rows, ldy, pos, w, K, dy, lddy, dw)
+  // waves per token: one for short rows, more for few tokens with long rows
+  const int64_t nv = (d + VW - 1) / VW;
+  if (nv <= 64) NVQ_COMBINE_BWD(1);
+  else if (nv <= 128) NVQ_COMBINE_BWD(2);
   else if (T >= 512 || nv <= 256) NVQ_COMBINE_BWD(4);
   else NVQ_COMBINE_BWD(16);
 #undef NVQ_COMBINE_BWD
@@ -739,18 +809,13 @@ static hipError_t combine_backward_run(const G* dout, int64_t T, int64_t nv, int
 hipError_t moe_combine_backward_launch(const void* dout, int dout_bf16, int64_t T, int64_t d, int64_t ldd, const void* Y,
                                        int y_bf16, int64_t rows, int64_t ldy, const int32_t* pos, const float* weights,
                                        int K, void* dY, int64_t lddy, float* dw, hipStream_t s) {
-  const uintptr_t ya = (uintptr_t)Y | (uintptr_t)dY;
-  const int vw = vec_width(dout_bf16 && y_bf16, d, ldd | (Y ? ldy : 0) | (dY ? lddy : 0),
-                           (dout_bf16 ? (uintptr_t)dout : 0) | (y_bf16 ? ya : 0),
-                           (dout_bf16 ? 0 : (uintptr_t)dout) | (y_bf16 ? 0 : ya));
-  const int64_t nv = d / vw;
-#define NVQ_RUN(GT, YT, VW)                                                                                            \
-  combine_backward_run<GT, YT, VW>((const GT*)dout, T, nv, ldd, (const YT*)Y, rows, ldy, pos, weights, K, (YT*)dY, lddy, \
+#define NVQ_RUN(GT, YT, VW)                                                                                           \
+  combine_backward_run<GT, YT, VW>((const GT*)dout, T, d, ldd, (const YT*)Y, rows, ldy, pos, weights, K, (YT*)dY, lddy, \
                                    dw, s)
-  if (dout_bf16 && y_bf16) return vw > 1 ? NVQ_RUN(uint16_t, uint16_t, 8) : NVQ_RUN(uint16_t, uint16_t, 1);
-  if (dout_bf16) return vw > 1 ? NVQ_RUN(uint16_t, float, 4) : NVQ_RUN(uint16_t, float, 1);
-  if (y_bf16) return vw > 1 ? NVQ_RUN(float, uint16_t, 4) : NVQ_RUN(float, uint16_t, 1);
-  return vw > 1 ? NVQ_RUN(float, float, 4) : NVQ_RUN(float, float, 1);
+  if (dout_bf16 && y_bf16) return NVQ_RUN(uint16_t, uint16_t, 8);
+  if (dout_bf16) return NVQ_RUN(uint16_t, float, 4);
+  if (y_bf16) return NVQ_RUN(float, uint16_t, 4);
+  return NVQ_RUN(float, float, 4);
 #undef NVQ_RUN
 }
 

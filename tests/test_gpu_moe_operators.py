@@ -155,7 +155,8 @@ def _sort_ref(ids, E):
 
 
 @pytest.mark.parametrize("T,K,E", [(1, 1, 1), (1, 8, 256), (37, 8, 256), (5, 3, 1024), (1000, 7, 60), (2048, 8, 256),
-                                   (2049, 8, 256), (16385, 1, 1000), (5461, 3, 1), (70001, 5, 128), (9001, 64, 1024)])
+                                   (2049, 8, 256), (16385, 1, 1000), (5461, 3, 1), (70001, 5, 128), (9001, 64, 1024), (1024, 8, 60),
+                                   (1025, 8, 256), (131072, 8, 256), (131073, 8, 1000)])
 @pytest.mark.parametrize("kind", ["uniform", "skewed", "dropped"])
 def test_sort(nvq, T, K, E, kind):
     rng = np.random.default_rng([T, K, E])
