@@ -473,6 +473,7 @@ int nvq_check_finite(const void* A, int dtype, int64_t rows, int64_t cols, int64
  * A slot is a (token, s) pair, 0 <= s < top_k; a row is a sorted slot.
  * tok_idx and grp_off are those of hessian_accumulate_grouped, which takes
  * grp_off on the host.  Sizes that depend on the routing stay on the device.
+ * No output may overlap an input or another output.
  */
 
 /*
@@ -495,15 +496,15 @@ int moe_topk(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, in
 
 /*
  * moe_topk_backward -- gradient of moe_topk's weights with respect to the
- * logits: with c = sum_s dweights_s weights_s and p the softmax over all E
- * (over the chosen experts with renorm, p = 0 elsewhere),
- *   dlogits_j = p_j (sum of dweights_s over the slots with id j - c).
+ * logits: with c = sum_s dweights_s weights_s and p the softmax over all E,
+ *   dlogits_j = p_j (sum of dweights_s over the slots with id j - c),
+ * and with renorm the sum of weights_s (dweights_s - c) over the slots with id j.
  *   logits, ids, weights  as given to and written by moe_topk (with renorm
  *            the logits are not read).
  *   dweights device fp32 [T x top_k]; slots with id -1 are ignored.
  *   dlogits  device [T x ldd] of the logits' dtype, ldd >= E; all E columns of
  *            every row are written (NaN for a rejected row, 0 for one with no
- *            expert left).  May not overlap logits.
+ *            expert left).
  */
 int moe_topk_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const int32_t* ids,
                       const float* weights, const float* dweights, int top_k, int renorm, void* dlogits, int64_t ldd,
@@ -533,16 +534,18 @@ int moe_sort(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int32_t* t
  * computed as g_e (X Q_e^T) with Q = e2m1 * e4m3 exact in bf16, on the bf16
  * matrix cores with fp32 accumulation.
  *
- *   X        device bf16 [n x ldx], 16-byte aligned, ldx >= k, ldx % 8 == 0.
+ *   X        device bf16 [n x ldx], 16-byte aligned, ldx >= k, ldx % 8 == 0,
+ *            n * ldx <= 2^35; n >= 1 if there are rows.
  *   tok_idx  device int32 [rows], or NULL: row r of X itself (rows <= n).  A
  *            row whose token is outside [0, n) is multiplied as zeros.
  *   rows     capacity of tok_idx and Y (T * top_k); rows from grp_off[G] on
  *            are neither read nor written.
  *   grp_off  device int64 [G + 1], non-decreasing, within [0, rows].  (They
  *            are clamped into that range and never lead outside the buffers;
- *            decreasing offsets give undefined rows.)
+ *            decreasing offsets give undefined rows.)  1 <= G < 2^23.
  *   codes [G x m x k/2] (8-byte aligned), scales [G x m x k/16], g [G]: the
- *            experts as gptq_nvfp4_quantize_batched writes them.  k % 16 == 0.
+ *            experts as gptq_nvfp4_quantize_batched writes them.  k % 16 == 0;
+ *            m and k at most 4000000.
  *            A rejected weight row (scales 0x7F) gives NaN.
  *   Y        device [rows x ldy] of y_dtype (fp32 or bf16, RNE), ldy >= m.
  */

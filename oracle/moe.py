@@ -46,15 +46,16 @@ def topk_backward(logits, ids, weights, dweights, renorm):
         if len(s) == 0:
             continue
         e = ids[t][s]
-        d, p = np.zeros(E), np.zeros(E)
-        np.add.at(d, e, np.asarray(dweights[t], dtype=np.float64)[s])
+        dw = np.asarray(dweights[t], dtype=np.float64)[s]
+        w = np.asarray(weights[t], dtype=np.float64)[s]
+        c = float(np.dot(dw, w))
         if renorm:
-            p[e] = weights[t][s]
+            np.add.at(out[t], e, w * (dw - c))
         else:
+            d = np.zeros(E)
+            np.add.at(d, e, dw)
             ex = np.exp(logits[t] - logits[t].max())
-            p = ex / ex.sum()
-        c = float(np.dot(np.asarray(dweights[t], dtype=np.float64)[s], weights[t][s]))
-        out[t] = p * (d - c)
+            out[t] = ex / ex.sum() * (d - c)
     return out
 
 

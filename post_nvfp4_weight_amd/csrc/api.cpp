@@ -779,6 +779,7 @@ int moe_topk_backward(const void* logits, int dtype, int64_t T, int64_t E, int64
   const size_t es = elem_size(dtype);
   if (!aligned(logits, es) || !aligned(dlogits, es) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
     return failp(NVQ_ERR_ALIGN, fn, "pointers must be aligned by their elements");
+  if (dlogits == logits) return failp(NVQ_ERR_VALUE, fn, "dlogits may not be logits");
   return hip_status(moe_topk_backward_launch(logits, dtype == NVQ_DTYPE_BF16, T, E, ld, ids, weights, dweights, top_k,
                                              renorm != 0, dlogits, ldd, (hipStream_t)stream), fn);
 }
@@ -822,6 +823,7 @@ int nvfp4_gemm_grouped(const void* X, int x_dtype, int64_t n, int64_t k, int64_t
   if (!X) return failp(NVQ_ERR_NULL, fn, "X is NULL");
   if (!aligned(X, 16)) return failp(NVQ_ERR_ALIGN, fn, "X must be 16-byte aligned");
   if (!aligned(tok_idx, 4)) return failp(NVQ_ERR_ALIGN, fn, "tok_idx must be 4-byte aligned");
+  if (Y == X) return failp(NVQ_ERR_VALUE, fn, "Y may not be X");
   return hip_status(nvfp4_gemm_grouped_launch((const uint16_t*)X, n, k, ldx, tok_idx, rows, grp_off, G, codes, scales, g,
                                               m, Y, y_dtype == NVQ_DTYPE_BF16, ldy, (hipStream_t)stream), fn);
 }
@@ -837,6 +839,7 @@ int nvfp4_gemm_grouped_dx(const void* dY, int dy_dtype, int64_t rows, int64_t m,
   if (rows == 0) return NVQ_OK;
   if (!dY) return failp(NVQ_ERR_NULL, fn, "dY is NULL");
   if (!aligned(dY, 2)) return failp(NVQ_ERR_ALIGN, fn, "dY must be 2-byte aligned");
+  if (dX == dY) return failp(NVQ_ERR_VALUE, fn, "dX may not be dY");
   return hip_status(nvfp4_gemm_grouped_dx_launch((const uint16_t*)dY, rows, m, lddy, grp_off, G, codes, scales, g, k, dX,
                                                  dx_dtype == NVQ_DTYPE_BF16, lddx, (hipStream_t)stream), fn);
 }
@@ -854,6 +857,7 @@ int moe_combine(const void* Y, int y_dtype, int64_t rows, int64_t d, int64_t ldy
   if ((rows > 0 && !Y) || !pos || !out) return failp(NVQ_ERR_NULL, fn, "Y, pos and out are required");
   if (!aligned(Y, elem_size(y_dtype)) || !aligned(out, elem_size(out_dtype)) || !aligned(pos, 4) || !aligned(weights, 4))
     return failp(NVQ_ERR_ALIGN, fn, "pointers must be aligned by their elements");
+  if (out == Y) return failp(NVQ_ERR_VALUE, fn, "out may not be Y");
   return hip_status(moe_combine_launch(Y, y_dtype == NVQ_DTYPE_BF16, rows, d, ldy, pos, weights, T, (int)top_k, out,
                                        out_dtype == NVQ_DTYPE_BF16, ldo, (hipStream_t)stream), fn);
 }
@@ -876,6 +880,7 @@ int moe_combine_backward(const void* dout, int dout_dtype, int64_t T, int64_t d,
   if (!aligned(dout, elem_size(dout_dtype)) || !aligned(Y, es) || !aligned(dY, es) || !aligned(pos, 4) ||
       !aligned(weights, 4) || !aligned(dweights, 4))
     return failp(NVQ_ERR_ALIGN, fn, "pointers must be aligned by their elements");
+  if (dY && (dY == Y || dY == dout)) return failp(NVQ_ERR_VALUE, fn, "dY may not be Y or dout");
   return hip_status(moe_combine_backward_launch(dout, dout_dtype == NVQ_DTYPE_BF16, T, d, ldd, Y,
                                                 y_dtype == NVQ_DTYPE_BF16, rows, ldy, pos, weights, (int)top_k, dY, lddy,
                                                 dweights, (hipStream_t)stream), fn);

@@ -73,7 +73,9 @@ __device__ __forceinline__ bool find_tile(const int64_t* __restrict__ off, int64
     const uint32_t all = G > 64 * EPL ? turn(x0) : total;   // (one turn: its values are still there)
     if (tile < before + all) {
       const uint32_t first = before + incl - mine;   // of the lane's experts
-      const int src = __ffsll((unsigned long long)__ballot(tile >= first && tile < first + mine)) - 1;
+      const uint64_t who = __ballot(tile >= first && tile < first + mine);
+      if (!who) return false;   // (only decreasing offsets that make the sums overflow)
+      const int src = __ffsll((unsigned long long)who) - 1;
       int at = (int)(tile - first), x = 0, r0 = 0, r1 = 0;
       bool found = false;
 #pragma unroll
@@ -912,7 +914,7 @@ hipError_t nvfp4_gemm_grouped_launch(const uint16_t* X, int64_t n, int64_t k, in
 #define NVQ_LAUNCH(KERNEL, ROWS, COLS, THREADS, ...)                                                                 \
   do {                                                                                                               \
     const int64_t blocks = most_tiles(rows, G, ROWS, (m + (COLS)-1) / (COLS));                                       \
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;                                                            \
+    if (blocks > kMaxThreads / (THREADS)) return hipErrorInvalidValue;                                               \
     hipLaunchKernelGGL((KERNEL), dim3((unsigned)blocks), dim3(THREADS), 0, s, X, n, k, ldx, tok_idx, rows, grp_off, G, \
                        codes, scales, g, m, Y, ldy __VA_OPT__(, ) __VA_ARGS__);                                      \
     return hipGetLastError();                                                                                        \
@@ -954,7 +956,7 @@ hipError_t nvfp4_gemm_grouped_dx_launch(const uint16_t* dY, int64_t rows, int64_
   do {                                                                                                              \
     using TL = GradTile<4, RF, 2>;                                                                                  \
     const int64_t blocks = most_tiles(rows, G, TL::kRows, (k + TL::kCols - 1) / TL::kCols);                         \
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;                                                           \
+    if (blocks > kMaxThreads / 256) return hipErrorInvalidValue;                                                    \
     if (out_bf16)                                                                                                   \
       hipLaunchKernelGGL((grouped_dx_kernel<4, RF, 2, DMA, 1>), dim3((unsigned)blocks), dim3(256), 0, s, dY, rows, m, \
                          lddy, grp_off, G, codes, scales, g, k, dX, lddx, vec);                                     \

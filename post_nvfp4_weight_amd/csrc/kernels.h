@@ -187,6 +187,7 @@ hipError_t nvfp4_gemm_launch(const uint16_t* X, int64_t T, int64_t k, int64_t ld
 // ---- mixture of experts (arguments checked by the caller; see include/nvq.h) ----
 constexpr int64_t kMoeMaxExperts = 1024;   // of the router and the sort
 constexpr int kMoeMaxTopK = 64;            // of the router (one lane per slot)
+constexpr int64_t kMaxThreads = 0xFFFFFFFF;   // of one launch
 hipError_t moe_topk_launch(const void* logits, int bf16, int64_t T, int64_t E, int64_t ld, int K, int renorm,
                            int32_t* ids, float* weights, hipStream_t s);
 hipError_t moe_topk_backward_launch(const void* logits, int bf16, int64_t T, int64_t E, int64_t ld, const int32_t* ids,

@@ -195,10 +195,10 @@ __global__ __launch_bounds__(256) void topk_kernel(const L* __restrict__ logits,
 }
 
 // Gradient of the router: with c = sum_s dw_s w_s, d logit_j is
-// p_j (dw of the slot with id j, if there is one, - c), p_j the softmax over
-// all experts, or with renorm the same over the chosen experts only (w_s in
-// the place of p_j).  LPT lanes per token as in topk_kernel; the slots' terms
-// reach their experts' lanes through a row of LDS.
+// p_j (sum of dw of the slots with id j - c), p_j the softmax over all experts,
+// or with renorm the sum of w_s (dw_s - c) of the slots with id j.  LPT lanes
+// per token as in topk_kernel; the slots' terms reach their experts' lanes
+// through a row of LDS (one addition per slot, lanes of one instruction in order).
 template <typename L, int LPT, int EPL>
 __global__ __launch_bounds__(256) void topk_backward_kernel(const L* __restrict__ logits, int64_t T, int E, int64_t ld,
                                                             const int32_t* __restrict__ ids,
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(256) void topk_backward_kernel(const L* __restrict_
 #pragma unroll
   for (int i = 0; i < EPL; ++i) mine[i * LPT + lane] = 0.0f;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // a group is part of one wave, whose LDS operations run in order
-  if (taken) mine[myid] = renorm ? myw * (mydw - c) : mydw;
+  if (taken) atomicAdd(mine + myid, renorm ? myw * (mydw - c) : mydw);
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   float p[EPL], total = 0.0f, top = 0.0f;
   if (!renorm) {
@@ -689,14 +689,28 @@ hipError_t topk_dispatch(int64_t T, int E, int K, F f) {
   return hipErrorInvalidValue;
 }
 
+// f(t0, nt) for parts of T tokens, as many as a launch of that many threads per token holds.
+template <typename F>
+hipError_t in_parts(int64_t T, int64_t threads, F f) {
+  const int64_t most = kMaxThreads / threads / 64 * 64;   // (whole workgroups: at most 16 tokens each)
+  if (most == 0) return hipErrorInvalidValue;
+  for (int64_t t0 = 0; t0 < T; t0 += most) {
+    f(t0, std::min(most, T - t0));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <typename L>
 hipError_t topk_run(const L* logits, int64_t T, int E, int64_t ld, int K, int renorm, int32_t* ids, float* weights,
                     hipStream_t s) {
   return topk_dispatch(T, E, K, [&]<int LPT, int EPL>() {
     const int64_t per = 256 / LPT;
-    hipLaunchKernelGGL((topk_kernel<L, LPT, EPL>), dim3((unsigned)((T + per - 1) / per)), dim3(256), 0, s, logits, T, E, ld,
-                       K, renorm, ids, weights);
-    return hipGetLastError();
+    return in_parts(T, LPT, [&](int64_t t0, int64_t nt) {
+      hipLaunchKernelGGL((topk_kernel<L, LPT, EPL>), dim3((unsigned)((nt + per - 1) / per)), dim3(256), 0, s,
+                         logits + t0 * ld, nt, E, ld, K, renorm, ids + t0 * K, weights + t0 * K);
+    });
   });
 }
 
@@ -705,9 +719,10 @@ hipError_t topk_backward_run(const L* logits, int64_t T, int E, int64_t ld, cons
                              const float* dw, int K, int renorm, L* dl, int64_t ldd, hipStream_t s) {
   return topk_dispatch(T, E, K, [&]<int LPT, int EPL>() {
     const int64_t per = 256 / LPT;
-    hipLaunchKernelGGL((topk_backward_kernel<L, LPT, EPL>), dim3((unsigned)((T + per - 1) / per)), dim3(256), 0, s, logits,
-                       T, E, ld, ids, w, dw, K, renorm, dl, ldd);
-    return hipGetLastError();
+    return in_parts(T, LPT, [&](int64_t t0, int64_t nt) {
+      hipLaunchKernelGGL((topk_backward_kernel<L, LPT, EPL>), dim3((unsigned)((nt + per - 1) / per)), dim3(256), 0, s,
+                         logits + t0 * ld, nt, E, ld, ids + t0 * K, w + t0 * K, dw + t0 * K, K, renorm, dl + t0 * ldd, ldd);
+    });
   });
 }
 
@@ -767,43 +782,48 @@ hipError_t moe_sort_launch(const int32_t* ids, int64_t n, int K, int64_t E, int3
   return hipGetLastError();
 }
 
-hipError_t moe_combine_launch(const void* Y, int y_bf16, int64_t rows, int64_t d, int64_t ldy, const int32_t* pos,
-                              const float* weights, int64_t T, int K, void* out, int out_bf16, int64_t ldo,
-                              hipStream_t s) {
-  const int vw = y_bf16 && out_bf16 ? 8 : 4;
-  const int64_t nv = (d + vw - 1) / vw;
+template <typename Y, typename O, int VW>
+static hipError_t combine_run(const Y* y, int64_t rows, int64_t d, int64_t ldy, const int32_t* pos, const float* w, int64_t T,
+                              int K, O* out, int64_t ldo, hipStream_t s) {
+  const int64_t nv = (d + VW - 1) / VW;
   int bx = 64;   // columns of a workgroup; at least a wave, so that a wave's slots are uniform
   while (bx < 256 && bx < nv) bx *= 2;
   const int by = 256 / bx;
-  const int64_t cb = (nv + bx - 1) / bx, blocks = cb * ((T + by - 1) / by);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks), block(bx, by);
-#define NVQ_COMBINE(YT, OT, VW)                                                                                   \
-  hipLaunchKernelGGL((combine_kernel<YT, OT, VW>), grid, block, 0, s, (const YT*)Y, rows, d, ldy, pos, weights, T, K, \
-                     (OT*)out, ldo, (int)cb)
-  if (y_bf16 && out_bf16) NVQ_COMBINE(uint16_t, uint16_t, 8);
-  else if (y_bf16) NVQ_COMBINE(uint16_t, float, 4);
-  else if (out_bf16) NVQ_COMBINE(float, uint16_t, 4);
-  else NVQ_COMBINE(float, float, 4);
-#undef NVQ_COMBINE
-  return hipGetLastError();
+  const int64_t cb = (nv + bx - 1) / bx;
+  return in_parts(T, cb * bx, [&](int64_t t0, int64_t nt) {
+    hipLaunchKernelGGL((combine_kernel<Y, O, VW>), dim3((unsigned)(cb * ((nt + by - 1) / by))), dim3(bx, by), 0, s, y, rows,
+                       d, ldy, pos + t0 * K, w ? w + t0 * K : nullptr, nt, K, out + t0 * ldo, ldo, (int)cb);
+  });
+}
+
+hipError_t moe_combine_launch(const void* Y, int y_bf16, int64_t rows, int64_t d, int64_t ldy, const int32_t* pos,
+                              const float* weights, int64_t T, int K, void* out, int out_bf16, int64_t ldo,
+                              hipStream_t s) {
+#define NVQ_RUN(YT, OT, VW) combine_run<YT, OT, VW>((const YT*)Y, rows, d, ldy, pos, weights, T, K, (OT*)out, ldo, s)
+  if (y_bf16 && out_bf16) return NVQ_RUN(uint16_t, uint16_t, 8);
+  if (y_bf16) return NVQ_RUN(uint16_t, float, 4);
+  if (out_bf16) return NVQ_RUN(float, uint16_t, 4);
+  return NVQ_RUN(float, float, 4);
+#undef NVQ_RUN
 }
 
 template <typename G, typename Y, int VW>
 static hipError_t combine_backward_run(const G* dout, int64_t T, int64_t d, int64_t ldd, const Y* y, int64_t rows,
                                        int64_t ldy, const int32_t* pos, const float* w, int K, Y* dy, int64_t lddy,
                                        float* dw, hipStream_t s) {
-#define NVQ_COMBINE_BWD(NW)                                                                                            \
-  hipLaunchKernelGGL((combine_backward_kernel<G, Y, VW, NW>), dim3((unsigned)T), dim3(64 * NW), 0, s, dout, T, d, ldd, y, \
-                     rows, ldy, pos, w, K, dy, lddy, dw)
+  auto run = [&]<int NW>() {
+    return in_parts(T, 64 * NW, [&](int64_t t0, int64_t nt) {
+      hipLaunchKernelGGL((combine_backward_kernel<G, Y, VW, NW>), dim3((unsigned)nt), dim3(64 * NW), 0, s, dout + t0 * ldd,
+                         nt, d, ldd, y, rows, ldy, pos + t0 * K, w ? w + t0 * K : nullptr, K, dy, lddy,
+                         dw ? dw + t0 * K : nullptr);
+    });
+  };
   // waves per token: one for short rows, more for few tokens with long rows
   const int64_t nv = (d + VW - 1) / VW;
-  if (nv <= 64) NVQ_COMBINE_BWD(1);
-  else if (nv <= 128) NVQ_COMBINE_BWD(2);
-  else if (T >= 512 || nv <= 256) NVQ_COMBINE_BWD(4);
-  else NVQ_COMBINE_BWD(16);
-#undef NVQ_COMBINE_BWD
-  return hipGetLastError();
+  if (nv <= 64) return run.template operator()<1>();
+  if (nv <= 128) return run.template operator()<2>();
+  if (T >= 512 || nv <= 256) return run.template operator()<4>();
+  return run.template operator()<16>();
 }
 
 hipError_t moe_combine_backward_launch(const void* dout, int dout_bf16, int64_t T, int64_t d, int64_t ldd, const void* Y,

@@ -596,3 +596,69 @@ def test_python_functions_refuse_wrong_tensors(nvq):
         with pytest.raises(kind):
             call()
             print("accepted", i)
+
+
+# ---- calls at the edges of what is documented -------------------------------------
+@pytest.mark.parametrize("T,E,K", [(5, 6, 4), (9000, 60, 8)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_topk_gradient_of_an_expert_named_twice(nvq, T, E, K, renorm):
+    """The slots of one expert add up (at most K = 8 terms: 8 u of their absolute sum on top of the bound above)."""
+    rng = np.random.default_rng([T, E])
+    l = _dev((rng.standard_normal((T, E))).astype(np.float32))
+    ids = rng.integers(0, 3, (T, K)).astype(np.int32)
+    w = rng.random((T, K)).astype(np.float32)
+    dw = rng.standard_normal((T, K)).astype(np.float32)
+    got = _np(nvq.moe_topk_backward(l, _dev(ids), _dev(w), _dev(dw), renorm=renorm))
+    ref = moe.topk_backward(_np(l), ids, w.astype(np.float64), dw, renorm)
+    D = float((l.max(dim=1).values - l.min(dim=1).values).max())
+    size = np.abs(dw).sum(axis=1, keepdims=True) * (1 + np.abs(w).max() * K)   # above every |term| sum
+    assert np.all(np.abs(got - ref) <= (2 * D + 64 + 2 * K) * U * size)
+
+
+def test_more_tokens_than_one_launch_takes(nvq):
+    """A launch holds fewer than 2^32 threads: 2^28 tokens of the router, 2^26 of the weighted sum (one column)."""
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    T = 2 ** 28 + 70
+    l = torch.randint(-8, 8, (T, 2), generator=gen, device=DEV, dtype=torch.int8).to(torch.bfloat16)
+    ids, w = nvq.moe_topk(l, 1, renorm=False)
+    assert torch.equal(ids[:, 0], (l[:, 1] > l[:, 0]).int())
+    dl = nvq.moe_topk_backward(l, ids, w, w, renorm=False)
+    del l, ids
+    # the two experts' gradients cancel, up to a bf16 rounding of each and 8 fp32 roundings of terms below 1
+    assert bool(((w > 0.49) & (w <= 1)).all())
+    assert bool(((dl[:, 0].float() + dl[:, 1].float()).abs() <= 2 * 2.0 ** -8 * dl[:, 0].float().abs() + 8 * U).all())
+    del w, dl
+    T = 2 ** 26 + 70
+    pos = torch.arange(T - 1, -1, -1, device=DEV, dtype=torch.int32)[:, None]
+    y = torch.randint(-99, 99, (T, 1), generator=gen, device=DEV, dtype=torch.int32).float()
+    w = torch.randint(-9, 9, (T, 1), generator=gen, device=DEV, dtype=torch.int32).float()
+    assert torch.equal(nvq.moe_combine(y, pos, w), y.flip(0) * w)
+    dy, dw = nvq.moe_combine_backward(y, y, pos, w)
+    assert torch.equal(dy, (y * w).flip(0)) and torch.equal(dw, y * y.flip(0))
+
+
+def test_sort_of_the_most_slots(nvq):
+    """3 times 715827882 slots, the largest multiple of 3 below 2^31."""
+    T, K, E = (2 ** 31 - 1) // 3, 3, 5
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    ids = torch.randint(-1, E, (T, K), generator=gen, device=DEV, dtype=torch.int32)
+    tok, off, pos = nvq.moe_sort(ids, E)
+    total, step, where = int(off[E]), 2 ** 22, 0
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        assert hi - lo == sum(int((ids[a:a + 2 ** 27] == e).sum()) for a in range(0, T, 2 ** 27))
+        for a in range(lo, hi - 1, 2 ** 28):   # the tokens of an expert in order
+            assert bool((tok[a + 1:min(a + 2 ** 28 + 1, hi)] >= tok[a:min(a + 2 ** 28, hi - 1)]).all())
+    for a in list(range(0, T, T // 8)) + [T - step]:
+        b = min(a + step, T)
+        i, p = ids[a:b], pos[a:b].long()
+        has = i >= 0
+        assert torch.equal(p >= 0, has)
+        t = torch.arange(a, b, device=DEV)[:, None].expand(b - a, K)[has]
+        assert torch.equal(tok[p[has]].long(), t)
+        assert bool(((off[i[has].long()] <= p[has]) & (p[has] < off[i[has].long() + 1])).all())
+    for a in range(0, T, 2 ** 26):
+        p = pos[a:a + 2 ** 26].reshape(-1)
+        where += int(p[p >= 0].long().sum())
+    assert where == total * (total - 1) // 2
+    assert bool((tok[total:] == -1).all())

@@ -128,3 +128,13 @@ def test_python_functions_refuse_host_tensors(nvq):
                  lambda: nvq.moe_combine_backward(z, z, i)):
         with pytest.raises(ValueError, match="HIP device"):
             call()
+
+
+def test_output_may_not_be_an_input(nvq):
+    l, other = nvq.lib, P(8192)
+    assert l.moe_topk_backward(fake, 0, 4, 8, 8, other, other, other, 2, 1, fake, 8, None) == VALUE
+    assert l.nvfp4_gemm_grouped(fake, 1, 10, 32, 32, other, 20, other, 4, other, other, other, 32, fake, 1, 32, None) == VALUE
+    assert l.nvfp4_gemm_grouped_dx(fake, 1, 20, 32, 32, other, 4, other, other, other, 32, fake, 1, 32, None) == VALUE
+    assert l.moe_combine(fake, 0, 8, 16, 16, other, other, 4, 2, fake, 0, 16, None) == VALUE
+    assert l.moe_combine_backward(other, 0, 4, 16, 16, fake, 0, 8, 16, other, other, 2, fake, 16, None, None) == VALUE
+    assert l.moe_combine_backward(fake, 0, 4, 16, 16, other, 0, 8, 16, other, other, 2, fake, 16, None, None) == VALUE

@@ -65,3 +65,21 @@ def test_gradients_against_differences(renorm):
             down = (_forward(X, W, logits, K, renorm)[0] * G).sum()
             A[i] = keep
             assert abs((up - down) / (2 * h) - d[i]) < 1e-6 * (1 + abs(d[i]))
+
+
+def test_router_gradient_of_an_expert_named_twice():
+    """Slots of one expert add up: the gradient of sum_s dw_s softmax(l[ids])_s, by differences."""
+    rng = np.random.default_rng(11)
+    l, ids, dw = rng.standard_normal((1, 6)), np.array([[2, 4, 2, 2]], dtype=np.int32), rng.standard_normal((1, 4))
+
+    def weights(x, renorm):
+        over = x[0, ids[0]] if renorm else x[0]
+        return np.exp(x[0, ids[0]])[None] / np.exp(over).sum()
+
+    for renorm in (True, False):
+        got = moe.topk_backward(l, ids, weights(l, renorm), dw, renorm)
+        for j in range(6):
+            h = np.zeros((1, 6))
+            h[0, j] = 1e-5
+            d = (dw * (weights(l + h, renorm) - weights(l - h, renorm))).sum() / 2e-5
+            assert abs(d - got[0, j]) < 1e-8
