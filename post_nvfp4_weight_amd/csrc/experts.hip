@@ -123,6 +123,18 @@ __device__ __forceinline__ constexpr int waitcnt_vm_lgkm0(int n) { return (n & 1
 //   (channel / 4) % 4 for the same reason.  (Loaded to registers instead, 32
 //   bytes per channel and load, they took the address unit twice the cycles.)
 //   Scales: 8 bytes per channel and chunk to registers, one chunk ahead.
+// What bounds it, by the rows per expert.  Many: the matrix cores, and with them
+// the power: 16384 tokens x 8 of 256 experts 2048 x 4096 take 1.99 ms (1.1
+// PFLOP/s), the cores busy two thirds of the cycles at 1.3 to 1.6 GHz, the
+// expansion (2.5 vector operations a code) between the products; the library's
+// dense product of as many flops takes 1.42 to 1.75 ms at 85 %.  Few: reading the
+// codes: 64 tokens x 8 read 595 MB in 0.17 to 0.19 ms (3.3 TB/s), the vector
+// units busy half of it with the expansion.  Tried and slower there: smaller and
+// wider tiles (64 x 64, 32 x 128, 32 x 256: 184 to 230 us against 185), other
+// starting places in k for other tiles (208).  Tried and slower for many rows:
+// 256 x 256 tiles on 8 waves and 256 rows on 4 (2.5 ms), 8 waves on 128 x 512
+// (equal), products in groups before their expansion (2.09 ms), each product
+// followed by its own (2.06 ms against 2.04 in the same run).
 template <int NW, int RF, int CF, int CR>
 struct Tile {
   static constexpr int kRows = 32 * RF, kCols = 32 * CF * NW;
@@ -257,8 +269,7 @@ __device__ __forceinline__ void product_step(const char* __restrict__ xb, const 
         qa[p ^ 1][f][piece] = dq_byte(word, s, piece);
       }
       // The copies one by one between the products: issued together, they held
-      // the wave at the full address queue (the gradient at 4099 tokens 250 us
-      // instead of COPY_B).
+      // the wave at the full address queue (16384 tokens 2072 us instead of 1993).
       if (j == 0) copy_x<NX, NW * 1024, FAR>(xd, xsrc, xbound, w.xoff, in, i * NX / RF, (i + 1) * NX / RF);
       if (j == 1 && T == 0) copy_lds<NC, 1024>(cd, csrc, cbound, w.coff, true, i * NC / RF, (i + 1) * NC / RF);
       __builtin_amdgcn_sched_barrier(0);
@@ -328,7 +339,8 @@ __device__ __forceinline__ void store_tile(char* smem, const f32x16 (&acc)[RF][C
 }
 
 // Rows without a token (their number is outside [0, n)) read token 0's and
-// are stored as zeros.
+// are stored as zeros; rows behind the tile's last are zeros that nothing is
+// fetched for (FAR: token 0's).
 template <int NW, int RF, int CF, int CR, int OUT_BF16, bool FAR>
 __device__ __forceinline__ void tile_product(char* smem, const RowTile& tl, const uint16_t* __restrict__ X, int64_t n,
                                              int64_t k, int64_t ldx, const int32_t* __restrict__ tok_idx,
@@ -350,6 +362,7 @@ __device__ __forceinline__ void tile_product(char* smem, const RowTile& tl, cons
     const int64_t r = tl.r0 + 8 * (NW * q + wave) + (lane >> 3);
     const int64_t t = r < tl.r1 ? (tok_idx ? tok_idx[r] : r) : 0;
     w.xoff[q] = (uint32_t)(((t >= 0 && t < n ? t : 0) * ldx + xk) / 8);
+    if (!FAR && r >= tl.r1) w.xoff[q] = 0x0FFFFFFF;   // past the bound: zeros, nothing fetched
   }
   // Bytes of X from step st on (not FAR: below 2^32 - 256).
   auto bound = [&](int64_t st) { return (uint32_t)max((int64_t)0, ((n - 1) * ldx + k - st * 64) * 2); };
@@ -477,6 +490,9 @@ __global__ __launch_bounds__(64 * NW, 2) void grouped_gemm_kernel(const uint16_t
 //   (16 bytes of codes and 2 scales per channel), of channel c and row c.
 // Lanes without a row read the tile's last row's activations and are not
 // stored.  The waves' partial sums are added in wave order through LDS.
+// Bound by one pass of loads over a cold weight: 8 rows on 256 experts 2048 x
+// 4096 read 38 MB in 14 us (2.7 TB/s).  Waves that each take their own channels
+// over all of k instead: 251 us against 197 at 64 tokens.
 constexpr int FW = 8, FROWS = 16, FCG = 2, FCOLS = 16 * FCG, FD = 2;
 typedef float f32x4c __attribute__((ext_vector_type(4)));
 
@@ -631,6 +647,9 @@ __global__ __launch_bounds__(64 * FW, 4) void grouped_few_kernel(const uint16_t*
 // lane's 8 codes come under 8 different scales, which are staged transposed,
 // [block][m].  dY's rows are copied like the activations when m and their
 // stride are multiples of 8 (DMA), else through registers, zeros past m.
+// Bound as the forward product: 4099 tokens x 6 of 64 experts 2048 x 2048 take
+// 230 us (0.9 PFLOP/s), the matrix cores busy 45 %, the vector units (two scales
+// per code pair) about as long.  8 waves on 256 x 256: 289 us against 276.
 template <int NW, int RF, int CF>
 struct GradTile {
   static constexpr int kRows = 32 * RF, kCols = 32 * CF * NW, kStride = kCols / 2;   // bytes of codes per m
@@ -760,7 +779,8 @@ __device__ __forceinline__ void tile_gradient(char* smem, const RowTile& tl, con
   uint32_t yoff[TL::kYLoads], coff[NC];
 #pragma unroll
   for (int q = 0; q < TL::kYLoads; ++q)
-    yoff[q] = (uint32_t)(min((int64_t)(8 * (NW * q + wave) + (lane >> 3)), rows - 1) * lddy + mk) * 2;
+    yoff[q] = 8 * (NW * q + wave) + (lane >> 3) < rows ? (uint32_t)((8 * (NW * q + wave) + (lane >> 3)) * lddy + mk) * 2
+                                                       : 0xFFFFFFF0u;   // past the bound: zeros, nothing fetched
 #pragma unroll
   for (int q = 0; q < NC; ++q) coff[q] = (uint32_t)((8 * (NW * q + wave) + (lane >> 3)) * (k / 2)) + 16 * piece;
   // Bytes from step st on, of the tile's rows (below 2^32: checked on the host) and of the expert's codes.
@@ -964,6 +984,9 @@ hipError_t nvfp4_gemm_grouped_dx_launch(const uint16_t* dY, int64_t rows, int64_
       hipLaunchKernelGGL((grouped_dx_kernel<4, RF, 2, DMA, 0>), dim3((unsigned)blocks), dim3(256), 0, s, dY, rows, m, \
                          lddy, grp_off, G, codes, scales, g, k, dX, lddx, vec);                                     \
   } while (0)
+  // Rows per expert: 128-row tiles from 24 on, else 64.  us with 64 / 128, 8 rows a
+  // token on 256 experts 2048 x 4096: 256 tokens (8 rows per expert) 324 / 387, 1024
+  // tokens 500 / 499, 4096 tokens 942 / 788.
   const int64_t avg = rows / std::min(rows, G);
   if (avg >= 24) {
     if (dma) NVQ_DX(4, true);

@@ -20,8 +20,8 @@ __device__ __forceinline__ void store_f(uint16_t* p, float v) {
 
 // Reductions over LPT = 16 (a DPP row) or 64 lanes, the result in every lane:
 // rotations inside a row, then the row and half swaps.  All are vector
-// instructions; the LDS-unit shuffles that __shfl_xor compiles to took the
-// 256-expert router (65536 tokens) 56 us, this form with 16 lanes per token TOPK_US.
+// instructions; with the LDS-unit shuffles that __shfl_xor compiles to the
+// 256-expert router (65536 tokens, one per wave) took 56 us, with these 35.
 template <int N>
 __device__ __forceinline__ uint32_t ror16(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, false);
@@ -101,10 +101,14 @@ __device__ __forceinline__ void load_row(const L* row, int E, int lane, float (&
 // never chosen (no key above that of -inf is left); a row with a NaN or +inf
 // is rejected.  Weights are a softmax with the row's largest logit
 // subtracted, sums in fp32.
-// What bounds it: 65536 tokens of 256 bf16 logits are 38 MB, 7 us at the copy
-// rate; the rounds' vector instructions cost about twice that.  One token
-// per wave (LPT 64) has a quarter of the elements per lane and a shorter
-// chain, for few tokens, many experts or more than 16 slots.
+// With up to 8 slots (SORTED) a lane first sorts its bf16 keys, of which at
+// most 8 can be chosen: a round then is the maximum over the lanes' first keys,
+// and the lane whose key was taken moves its others up (28 instructions
+// instead of the 70 that look through 16 keys).
+// What bounds it: 65536 tokens of 256 bf16 logits are 38 MB, 7.3 us at the copy
+// rate; vector instructions (keys, sort, rounds) make it 17 us, 19 without the
+// sort.  One token per wave (LPT 64) has a quarter of the elements per lane and a
+// shorter chain, for few tokens, many experts or more than 16 slots.
 constexpr uint32_t kNegInfKey = 0x007FFFFFu;   // ~bits of -inf
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);   // -0 + 0 = +0
@@ -119,7 +123,54 @@ __device__ __forceinline__ float logit_of(uint32_t k) {
   return PACKED ? __uint_as_float(__float_as_uint(key_value(k)) & 0xFFFF0000u) : key_value(k);
 }
 
-template <typename L, int LPT, int EPL>
+// Exchanges v[I] and v[I + D] into falling order.
+template <int I, int D, int EPL>
+__device__ __forceinline__ void exchange(uint32_t (&v)[EPL]) {
+  const uint32_t a = v[I], b = v[I + D];
+  v[I] = max(a, b);
+  v[I + D] = min(a, b);
+}
+// Falling order of v[F .. F + N - 1] by Batcher's odd-even merges: runs of P
+// become runs of 2 P by exchanges at distances D = P, P / 2 .. 1, from place I on.
+template <int F, int N, int P = 1, int D = 1, int I = 0, int EPL>
+__device__ __forceinline__ void sort_keys(uint32_t (&v)[EPL]) {
+  if constexpr (P < N) {
+    if constexpr (I + D < N) {
+      if constexpr (I >= D % P && (I - D % P) / D % 2 == 0 && I / (2 * P) == (I + D) / (2 * P)) exchange<F + I, D>(v);
+      sort_keys<F, N, P, D, I + 1>(v);
+    } else if constexpr (D > 1) {
+      sort_keys<F, N, P, D / 2, 0>(v);
+    } else {
+      sort_keys<F, N, 2 * P, 2 * P, 0>(v);
+    }
+  }
+}
+// The same of a run that rises and falls at most once.
+template <int N, int D = N / 2, int I = 0, int EPL>
+__device__ __forceinline__ void merge_keys(uint32_t (&v)[EPL]) {
+  if constexpr (I < N) {
+    if constexpr ((I & D) == 0) exchange<I, D>(v);
+    merge_keys<N, D, I + 1>(v);
+  } else if constexpr (D > 1) {
+    merge_keys<N, D / 2, 0>(v);
+  }
+}
+// The lane's SORTED largest keys in falling order at the front of v (behind them anything).
+template <int SORTED, int EPL>
+__device__ __forceinline__ void sort_largest(uint32_t (&v)[EPL]) {
+  if constexpr (EPL <= SORTED) {
+    sort_keys<0, EPL>(v);
+  } else {
+    static_assert(EPL == 2 * SORTED, "two sorted runs");
+    sort_keys<0, SORTED>(v);
+    sort_keys<SORTED, SORTED>(v);
+#pragma unroll
+    for (int i = 0; i < SORTED; ++i) v[i] = max(v[i], v[EPL - 1 - i]);
+    merge_keys<SORTED>(v);
+  }
+}
+
+template <typename L, int LPT, int EPL, int SORTED>
 __global__ __launch_bounds__(256) void topk_kernel(const L* __restrict__ logits, int64_t T, int E, int64_t ld, int K,
                                                    int renorm, int32_t* __restrict__ ids,
                                                    float* __restrict__ weights) {
@@ -152,6 +203,7 @@ __global__ __launch_bounds__(256) void topk_kernel(const L* __restrict__ logits,
       rest = group_sum<LPT>(rest);
     }
   }
+  if constexpr (SORTED > 0) sort_largest<SORTED>(key);
   const uint32_t none = kPacked ? kNegInfKey | 0xFFFFu : kNegInfKey;   // keys up to this are -inf
   const float top = logit_of<kPacked>(best);
   float myval = -__builtin_inff();
@@ -160,7 +212,17 @@ __global__ __launch_bounds__(256) void topk_kernel(const L* __restrict__ logits,
     // (a group with nothing left or a rejected row goes on with the wave and takes nothing)
     const bool take = best > none && !bad;
     uint32_t id, own = 0;
-    if (kPacked) {
+    if (SORTED) {
+      id = 0xFFFFu - (best & 0xFFFFu);
+      constexpr int N = EPL < SORTED ? EPL : SORTED;
+      const bool first = key[0] == best;   // the lane whose first key was taken moves its others up
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t here = key[i], next = i + 1 < N ? key[i + 1] : 0u;
+        key[i] = first ? next : here;
+      }
+      own = key[0];
+    } else if (kPacked) {
       id = 0xFFFFu - (best & 0xFFFFu);
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
@@ -272,7 +334,9 @@ __global__ __launch_bounds__(256) void topk_backward_kernel(const L* __restrict_
 // Few assignments: one workgroup and launch.  Many: counts per chunk, their
 // sums, and the rows, three launches.  A chunk's rows are first sorted in LDS
 // and leave in runs per expert: written one by one, 4 bytes each, they took
-// the last launch SORT_A us instead of SORT_B (2^21 assignments, 256 experts).
+// the last launch 15.5 us instead of 12.5 (2^21 assignments, 256 experts).
+// Bound at that size by the ballots' instructions: 19 us over all, of which the
+// 25 MB would take 5; up to 2^16 by the launches' own 11 us.
 constexpr int SORT_T = 1024, SORT_W = SORT_T / 64;
 
 // i / K for 0 <= i < 2^31 as a multiplication: with s = ceil(log2 K) and
@@ -554,7 +618,7 @@ __device__ __forceinline__ void store_vec(E* p, const float (&v)[VW]) {
 
 // One thread per vector of a token's columns: blockDim = (columns, tokens).
 // KC slots' loads are in flight together; sums run in slot order.  Bound by
-// reading the rows once: COMBINE_NOTE
+// reading the rows once: 16384 x 8 rows of 4096 bf16 in 230 us, 5.2 TB/s.
 constexpr int KC = 8;
 template <typename Y, typename O, int VW>
 __global__ __launch_bounds__(256) void combine_kernel(const Y* __restrict__ y, int64_t rows, int64_t d, int64_t ldy,
@@ -594,7 +658,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const Y* __restrict__ y, i
 
 // Its gradients: a workgroup of NW waves per token, dout's row read once for
 // KC slots at a time; each lane sums its columns' products, then lanes and
-// waves are added in a fixed order.
+// waves are added in a fixed order.  Bound by the rows' traffic: 5003 x 6 rows
+// of 2056 fp32 and their gradients (0.54 GB) in 130 us, 4.1 TB/s.
 template <typename G, typename Y, int VW, int NW>
 __global__ __launch_bounds__(64 * NW) void combine_backward_kernel(const G* __restrict__ dout, int64_t T, int64_t d,
                                                                    int64_t ldd, const Y* __restrict__ y, int64_t rows,
@@ -666,8 +731,12 @@ __global__ __launch_bounds__(64 * NW) void combine_backward_kernel(const G* __re
 }
 
 // Calls f(LPT, EPL) with the constants for E experts: 16 lanes per token when
-// there are tokens enough to fill the device that way, at most 256 experts and 16 slots.
-constexpr int64_t kTopkWaves = 8192;   // tokens from which 16 lanes per token are taken
+// there are tokens enough to fill the device that way, at most 256 experts and
+// 16 slots.  us with 64 / 16 lanes: 256 experts bf16, 8 slots, 2048 tokens 3.4 /
+// 3.9, 4096 tokens 4.2 / 3.5, 65536 tokens 33 / 17; 64 experts fp32, 6 slots, 1024
+// tokens 3.1 / 3.2, 4096 tokens 4.1 / 3.3; the gradient with 128 experts fp32, 4096
+// tokens 3.4 / 3.8, 16384 tokens 6.7 / 5.7.
+constexpr int64_t kTopkWaves = 4096;   // tokens from which 16 lanes per token are taken
 template <typename F>
 hipError_t topk_dispatch(int64_t T, int E, int K, F f) {
   const int lanes = T >= kTopkWaves && E <= 256 && K <= 16 ? 16 : 64;
@@ -707,10 +776,15 @@ hipError_t topk_run(const L* logits, int64_t T, int E, int64_t ld, int K, int re
                     hipStream_t s) {
   return topk_dispatch(T, E, K, [&]<int LPT, int EPL>() {
     const int64_t per = 256 / LPT;
-    return in_parts(T, LPT, [&](int64_t t0, int64_t nt) {
-      hipLaunchKernelGGL((topk_kernel<L, LPT, EPL>), dim3((unsigned)((nt + per - 1) / per)), dim3(256), 0, s,
-                         logits + t0 * ld, nt, E, ld, K, renorm, ids + t0 * K, weights + t0 * K);
-    });
+    const auto run = [&]<int SORTED>() {
+      return in_parts(T, LPT, [&](int64_t t0, int64_t nt) {
+        hipLaunchKernelGGL((topk_kernel<L, LPT, EPL, SORTED>), dim3((unsigned)((nt + per - 1) / per)), dim3(256), 0, s,
+                           logits + t0 * ld, nt, E, ld, K, renorm, ids + t0 * K, weights + t0 * K);
+      });
+    };
+    if constexpr (sizeof(L) == 2)
+      if (K <= 8) return run.template operator()<8>();
+    return run.template operator()<0>();
   });
 }
 
@@ -727,9 +801,10 @@ hipError_t topk_backward_run(const L* logits, int64_t T, int E, int64_t ld, cons
 }
 
 // Assignments up to which one workgroup sorts (8192 of them, 256 experts: one
-// workgroup 10.9 us, three launches 12.3), and from which chunks are 8192 long (below: 4096).
+// workgroup 10.9 us, three launches 12.3), and up to which chunks are 4096 long,
+// which gives each CU one; 8192 behind it (2^20: 14.6 / 17.0 us, 2^21: 22.1 / 19.1).
 constexpr int64_t kSortSmall = 8 * SORT_T, kSortLarge = (int64_t)1 << 20;
-int sort_per(int64_t n) { return n >= kSortLarge ? 8 : 4; }
+int sort_per(int64_t n) { return n > kSortLarge ? 8 : 4; }
 int64_t sort_blocks(int64_t n) { return (n + SORT_T * sort_per(n) - 1) / (SORT_T * sort_per(n)); }
 
 }  // namespace
@@ -818,9 +893,13 @@ static hipError_t combine_backward_run(const G* dout, int64_t T, int64_t d, int6
                          dw ? dw + t0 * K : nullptr);
     });
   };
-  // waves per token: one for short rows, more for few tokens with long rows
+  // Waves per token: one for short rows, more for few tokens with long rows.  us
+  // with 1 / 2 / 4 / 16 waves, 8 slots bf16: 4096 tokens d = 512 14.8 / 22.6 / 30.4 /
+  // 96.9, d = 1024 25.2 / 28.0 / 34.4 / 99.1, d = 4096 143 / 148 / 124 / 186; 512 tokens
+  // d = 4096 35.4 / 22.4 / 16.6 / 19.7; 256 tokens 29.6 / 18.2 / 12.3 / 10.4; 8 tokens
+  // d = 1024 8.1 / 6.2 / 6.2 / 6.2, d = 2048 12.4 / 8.2 / 6.4 / 6.3.
   const int64_t nv = (d + VW - 1) / VW;
-  if (nv <= 64) return run.template operator()<1>();
+  if (nv <= (T >= 4096 ? 128 : 64)) return run.template operator()<1>();
   if (nv <= 128) return run.template operator()<2>();
   if (T >= 512 || nv <= 256) return run.template operator()<4>();
   return run.template operator()<16>();
