@@ -79,17 +79,17 @@ __device__ __forceinline__ void load_row(const L* row, int E, int lane, float (&
 #pragma unroll
   for (int c = 0; c < EPL / R::VW; ++c) {
     const int e0 = R::index(lane, c * R::VW);
-    L x[R::VW];
     if (e0 + R::VW <= E) {
       const Vec y = *(const Vec*)(row + e0);
 #pragma unroll
-      for (int i = 0; i < R::VW; ++i) x[i] = y[i];
+      for (int i = 0; i < R::VW; ++i) {
+        const L x = y[i];
+        v[c * R::VW + i] = load_f(&x);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < R::VW; ++i) x[i] = e0 + i < E ? row[e0 + i] : (L)0;
+      for (int i = 0; i < R::VW; ++i) v[c * R::VW + i] = e0 + i < E ? load_f(row + e0 + i) : -__builtin_inff();
     }
-#pragma unroll
-    for (int i = 0; i < R::VW; ++i) v[c * R::VW + i] = e0 + i < E ? load_f(&x[i]) : -__builtin_inff();
   }
 }
 
@@ -106,10 +106,11 @@ __device__ __forceinline__ void load_row(const L* row, int E, int lane, float (&
 // and the lane whose key was taken moves its others up (28 instructions
 // instead of the 70 that look through 16 keys).
 // What bounds it: 65536 tokens of 256 bf16 logits are 38 MB, 7.3 us at the copy
-// rate; vector instructions (keys, sort, rounds) make it 17 us, 19 without the
+// rate; vector instructions (keys, sort, rounds) make it 16 us, 19 without the
 // sort.  One token per wave (LPT 64) has a quarter of the elements per lane and a
 // shorter chain, for few tokens, many experts or more than 16 slots.
 constexpr uint32_t kNegInfKey = 0x007FFFFFu;   // ~bits of -inf
+constexpr uint32_t kPosInfKey = 0xFF800000u;   // bits of +inf, top bit set
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);   // -0 + 0 = +0
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
@@ -182,19 +183,20 @@ __global__ __launch_bounds__(256) void topk_kernel(const L* __restrict__ logits,
   uint32_t key[EPL];
   float rest = 0.0f;   // sum over all experts
   uint32_t best;
-  bool bad = false;
+  bool bad;
   {
     float v[EPL];
     load_row<L, LPT, EPL>(logits + row * ld, E, lane, v);
-    uint32_t own = 0;
+    uint32_t own = 0, least = 0xFFFFFFFFu;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      bad |= !(v[i] < __builtin_inff());
       key[i] = order_key(v[i]);
+      least = min(least, key[i]);
       if (kPacked) key[i] = (key[i] & 0xFFFF0000u) | (0xFFFFu - (uint32_t)R::index(lane, i));
       own = max(own, key[i]);
     }
-    bad = group_any<LPT>(bad);
+    // A NaN's key lies above that of +inf or, with its sign set, below that of -inf.
+    bad = group_any<LPT>(own >= kPosInfKey || least < kNegInfKey);
     best = group_max<LPT>(own);
     if (!renorm) {
       const float top = logit_of<kPacked>(best);
@@ -733,7 +735,7 @@ __global__ __launch_bounds__(64 * NW) void combine_backward_kernel(const G* __re
 // Calls f(LPT, EPL) with the constants for E experts: 16 lanes per token when
 // there are tokens enough to fill the device that way, at most 256 experts and
 // 16 slots.  us with 64 / 16 lanes: 256 experts bf16, 8 slots, 2048 tokens 3.4 /
-// 3.9, 4096 tokens 4.2 / 3.5, 65536 tokens 33 / 17; 64 experts fp32, 6 slots, 1024
+// 3.9, 4096 tokens 4.2 / 3.5, 65536 tokens 33 / 16; 64 experts fp32, 6 slots, 1024
 // tokens 3.1 / 3.2, 4096 tokens 4.1 / 3.3; the gradient with 128 experts fp32, 4096
 // tokens 3.4 / 3.8, 16384 tokens 6.7 / 5.7.
 constexpr int64_t kTopkWaves = 4096;   // tokens from which 16 lanes per token are taken

@@ -662,3 +662,39 @@ def test_sort_of_the_most_slots(nvq):
         where += int(p[p >= 0].long().sum())
     assert where == total * (total - 1) // 2
     assert bool((tok[total:] == -1).all())
+
+
+@pytest.mark.parametrize("T,E", [(5000, e) for e in (1, 3, 16, 17, 60, 128, 200, 256)] +
+                         [(70, e) for e in (2, 64, 65, 200, 512, 1000, 1024)])
+@pytest.mark.parametrize("K", [1, 2, 8, 9, 16])
+def test_topk_choice_for_every_row_length(nvq, T, E, K):
+    """Ids and order against a stable sort, with many equal values and some experts masked."""
+    K = min(K, E)
+    rng = np.random.default_rng([T, E, K])
+    for dtype in DTYPES.values():
+        l = torch.from_numpy(rng.integers(-20, 20, (T, E)).astype(np.float32)).to(dtype)
+        l[:, E // 2:] += torch.from_numpy(rng.standard_normal((T, E - E // 2)).astype(np.float32)).to(dtype)
+        l[torch.from_numpy(rng.random((T, E)) < 0.3)] = float("-inf")
+        v, i = torch.sort(l, dim=1, descending=True, stable=True)
+        ref = torch.where(v[:, :K] == float("-inf"), -1, i[:, :K])
+        ids, _ = nvq.moe_topk(l.to(DEV), K)
+        assert torch.equal(ids.cpu().long(), ref)
+
+
+@pytest.mark.parametrize("T,E,K", [(20, 60, 3), (20, 300, 12), (5000, 60, 3), (5000, 60, 12)])
+def test_topk_rejects_every_nan_and_infinity(nvq, T, E, K):
+    """NaNs of both signs, quiet and signalling, and +inf, anywhere in the row; the largest finite values are kept."""
+    bits = {torch.float32: (torch.int32, [0x7FC00000, 0x7F800001, 0x7FFFFFFF, -0x400000, -0x7FFFFF, -1, 0x7F800000]),
+            torch.bfloat16: (torch.int16, [0x7FC0, 0x7F81, 0x7FFF, -0x40, -0x7F, -1, 0x7F80])}
+    rng = np.random.default_rng([T, E, K])
+    for dtype, (as_int, values) in bits.items():
+        l = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).to(dtype)
+        bad = torch.zeros(T, dtype=torch.bool)
+        for j, b in enumerate(values):
+            for t in (2 * j, T - 1 - 2 * j if T > 100 else 2 * j):
+                l.view(as_int)[t, int(rng.integers(E))] = b
+                bad[t] = True
+        l[1, 3], l[3, 5] = torch.finfo(dtype).max, torch.finfo(dtype).min
+        ids, w = nvq.moe_topk(l.to(DEV), K)
+        assert torch.equal((ids == -1).all(1).cpu(), bad) and torch.equal(torch.isnan(w).all(1).cpu(), bad)
+        assert not torch.isnan(w[~bad.to(DEV)]).any() and int(ids[1, 0]) == 3
