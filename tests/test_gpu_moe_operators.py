@@ -698,3 +698,10 @@ def test_topk_rejects_every_nan_and_infinity(nvq, T, E, K):
         ids, w = nvq.moe_topk(l.to(DEV), K)
         assert torch.equal((ids == -1).all(1).cpu(), bad) and torch.equal(torch.isnan(w).all(1).cpu(), bad)
         assert not torch.isnan(w[~bad.to(DEV)]).any() and int(ids[1, 0]) == 3
+
+
+@pytest.mark.parametrize("k", [128, 384, 496, 512, 528, 640, 656, 768, 784, 896, 1040, 1168])
+@pytest.mark.parametrize("n,rows,G,m", [(900, 5000, 30, 1800), (60, 200, 30, 1800), (3, 9, 30, 64)])
+def test_product_for_every_end_of_k(nvq, n, rows, G, m, k):
+    """Each tile size (128 x 256, 64 x 128, few rows) with k ending in every part of its steps."""
+    test_product(nvq, n, rows, G, m, k, "skewed")
