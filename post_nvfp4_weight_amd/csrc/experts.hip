@@ -122,9 +122,10 @@ __device__ __forceinline__ constexpr int waitcnt_vm_lgkm0(int n) { return (n & 1
 //   to LDS of the wave's own, a ring of CR chunks, pieces swizzled by
 //   (channel / 4) % 4 for the same reason.  (Loaded to registers instead, 32
 //   bytes per channel and load, they took the address unit twice the cycles.)
-//   Scales: 8 bytes per channel and chunk to registers, one chunk ahead.
+//   Scales: 8 bytes per channel and chunk to registers, one chunk ahead (on the
+//   large tile two chunks at a time).
 // What bounds it, by the rows per expert.  Many: the matrix cores, and with them
-// the power: 16384 tokens x 8 of 256 experts 2048 x 4096 take 1.99 ms (1.1
+// the power: 16384 tokens x 8 of 256 experts 2048 x 4096 take 1.96 to 2.04 ms (1.1
 // PFLOP/s), the cores busy two thirds of the cycles at 1.3 to 1.6 GHz, the
 // expansion (2.5 vector operations a code) between the products; the library's
 // dense product of as many flops takes 1.42 to 1.75 ms at 85 %.  Few: reading the
