@@ -537,7 +537,8 @@ int moe_sort(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int32_t* t
  *   X        device bf16 [n x ldx], 16-byte aligned, ldx >= k, ldx % 8 == 0,
  *            n * ldx <= 2^35; n >= 1 if there are rows.
  *   tok_idx  device int32 [rows], or NULL: row r of X itself (rows <= n).  A
- *            row whose token is outside [0, n) is multiplied as zeros.
+ *            row whose token is outside [0, n) is written as zeros, also under
+ *            rejected weight rows and a g that is not finite.
  *   rows     capacity of tok_idx and Y (T * top_k); rows from grp_off[G] on
  *            are neither read nor written.
  *   grp_off  device int64 [G + 1], non-decreasing, within [0, rows].  (They
@@ -546,7 +547,8 @@ int moe_sort(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int32_t* t
  *   codes [G x m x k/2] (8-byte aligned), scales [G x m x k/16], g [G]: the
  *            experts as gptq_nvfp4_quantize_batched writes them.  k % 16 == 0;
  *            m and k at most 4000000.
- *            A rejected weight row (scales 0x7F) gives NaN.
+ *            A rejected weight row (scales 0x7F) gives NaN in its column of
+ *            every row that has a token.
  *   Y        device [rows x ldy] of y_dtype (fp32 or bf16, RNE), ldy >= m.
  */
 int nvfp4_gemm_grouped(const void* X, int x_dtype, int64_t n, int64_t k, int64_t ldx, const int32_t* tok_idx,

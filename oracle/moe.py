@@ -81,14 +81,15 @@ def experts_matrices(packed, scales, g):
 
 
 def grouped_matmul(X, W, grp_off, tok_idx=None):
-    """Rows r of expert e: X[tok_idx[r]] W_e^T (a token outside X: zeros).  Rows no expert has stay 0."""
+    """Rows r of expert e: X[tok_idx[r]] W_e^T (a token outside X: zeros, whatever the weights).  Rows no expert has stay 0."""
     X = np.asarray(X, dtype=np.float64)
     rows = len(X) if tok_idx is None else len(tok_idx)
     Y = np.zeros((rows, W.shape[1]))
     for e in range(len(W)):
         for r in range(int(grp_off[e]), int(grp_off[e + 1])):
             t = r if tok_idx is None else int(tok_idx[r])
-            Y[r] = W[e] @ (X[t] if 0 <= t < len(X) else np.zeros(X.shape[1]))
+            if 0 <= t < len(X):
+                Y[r] = W[e] @ X[t]
     return Y
 
 

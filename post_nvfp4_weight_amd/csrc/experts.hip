@@ -646,11 +646,8 @@ __global__ __launch_bounds__(64 * FW, 4) void grouped_few_kernel(const uint16_t*
   }
   // Accumulator register r of lane l: channel 4 q + r, row c.
 #pragma unroll
-  for (int f = 0; f < FCG; ++f) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) acc[f][r] = token ? acc[f][r] : 0.0f;
-    *(f32x4c*)&part[wave][c][16 * f + 4 * q] = acc[f];
-  }
+  for (int f = 0; f < FCG; ++f) *(f32x4c*)&part[wave][c][16 * f + 4 * q] = acc[f];
+  if (wave == 0 && q == 0) part[0][c][FCOLS] = token ? 1.0f : 0.0f;   // (in the padding)
   __syncthreads();
   const int r = tid / FCOLS, o = tid % FCOLS;
   static_assert(FROWS * FCOLS == 64 * FW, "one output per thread");
@@ -658,7 +655,7 @@ __global__ __launch_bounds__(64 * FW, 4) void grouped_few_kernel(const uint16_t*
   float v = 0.0f;
 #pragma unroll
   for (int w = 0; w < FW; ++w) v += part[w][r][o];
-  v *= gs[tl.expert];
+  v = part[0][r][FCOLS] != 0.0f ? v * gs[tl.expert] : 0.0f;
   const int64_t at = (tl.r0 + r) * ldy + o0 + o;
   if (OUT_BF16) ((__bf16*)Y)[at] = (__bf16)v;
   else ((float*)Y)[at] = v;
