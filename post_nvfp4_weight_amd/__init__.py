@@ -562,7 +562,8 @@ def nvfp4_gemm_grouped(X, codes, scales, g, grp_off, tok_idx=None, out_dtype=tor
 
 
 def nvfp4_gemm_grouped_dx(dY, codes, scales, g, grp_off, out_dtype=torch.float32, dX=None):
-    """Gradient of nvfp4_gemm_grouped with respect to its rows: dX[r] = dY[r] dequant(W_e), dY [rows, m] bf16.  The tokens'
+    """Gradient of nvfp4_gemm_grouped with respect to its rows: dX[r] = dY[r] dequant(W_e), dY [rows, m] bf16 (as
+    moe_combine_backward gives it for products with out_dtype bf16; their default is fp32).  The tokens'
     gradient is moe_combine(dX, pos).  Rows from grp_off[G] on are not written."""
     rows, my, lddy = _matrix(dY, "dY", (_BF16,))
     dev = dY.get_device()
@@ -590,21 +591,30 @@ def moe_combine(Y, pos, weights=None, out_dtype=None, out=None):
     return out
 
 
-def moe_combine_backward(dout, Y, pos, weights=None, dY=None):
+def moe_combine_backward(dout, Y, pos, weights=None, dY=None, need_dY=True, need_dweights=True):
     """Gradients of moe_combine: (dY [rows, d] in Y's dtype, dweights fp32 [T, K]).  Rows of dY that no slot of pos names
-    (past moe_sort's last row) are not written; no row may be named twice."""
+    (past moe_sort's last row) are not written; no row may be named twice.  One that is not needed is None: dweights where
+    the router is frozen (Y is then not read, and may be None beside a dY of the caller's), dY where the experts and what
+    is before them are.  For nvfp4_gemm_grouped_dx, which takes bf16, Y is to be bf16 too."""
     T, d, ldd = _matrix(dout, "dout", _FLOATS)
     dev = dout.get_device()
-    rows, dy, ldy = _matrix(Y, "Y", _FLOATS, dev)
+    if Y is None and (need_dweights or dY is None):
+        raise ValueError("Y is required, but beside a dY and without dweights")
+    if dY is not None and not need_dY:
+        raise ValueError("dY is given, but not needed")
+    like = dY if Y is None else Y
+    rows, dy, ldy = _matrix(like, "dY" if Y is None else "Y", _FLOATS, dev)
     if dy != d:
         raise ValueError(f"dout has {d} columns, Y {dy}")
     K = _table(pos, "pos", T, dev)
     if weights is not None:
         _dense(weights, "weights", _F32, (T, K), dev)
-    if dY is not None and (not isinstance(dY, torch.Tensor) or dY.dtype is not Y.dtype):
+    if dY is not None and (not isinstance(dY, torch.Tensor) or dY.dtype is not like.dtype):
         raise TypeError("dY must be a tensor of Y's dtype")
-    dY, lddy = _output(dY, "dY", Y, rows, d, Y.dtype, dev)
-    dw = dout.new_empty((T, K), dtype=_F32)
-    _call(lib.moe_combine_backward, "moe_combine_backward", dev, dout.data_ptr(), _CODES[dout.dtype], T, d, ldd, Y.data_ptr(), _CODES[Y.dtype], rows,
-          ldy, pos.data_ptr(), _addr(weights), K, dY.data_ptr(), lddy, dw.data_ptr())
+    lddy = d
+    if need_dY:
+        dY, lddy = _output(dY, "dY", like, rows, d, like.dtype, dev)
+    dw = dout.new_empty((T, K), dtype=_F32) if need_dweights else None
+    _call(lib.moe_combine_backward, "moe_combine_backward", dev, dout.data_ptr(), _CODES[dout.dtype], T, d, ldd, _addr(Y), _CODES[like.dtype],
+          rows, ldy, pos.data_ptr(), _addr(weights), K, _addr(dY), lddy, _addr(dw))
     return dY, dw
