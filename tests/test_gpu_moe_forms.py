@@ -88,6 +88,29 @@ def test_gradients_of_the_weighted_sum_refused(nvq):
             call()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,K", [(5, 7, 3), (4100, 100, 8), (33, 300, 20), (5000, 256, 6)])
+def test_router_gradient_between_wider_buffers(nvq, T, E, K, dtype, renorm):
+    """Logits and their gradient as column slices at any element's place: what contiguous ones give, and no other column."""
+    rng = np.random.default_rng([T, E, K])
+    dtype = DTYPES[dtype]
+    wide = _dev(rng.standard_normal((T, E + 10)).astype(np.float32)).to(dtype)
+    dw = _dev(rng.standard_normal((T, K)).astype(np.float32))
+    for at, left in ((3, 1), (8, 5)):
+        logits = wide[:, at:at + E]
+        ids, w = nvq.moe_topk(logits, K, renorm)
+        ref = nvq.moe_topk_backward(logits.contiguous(), ids, w, dw, renorm)
+        assert torch.equal(nvq.moe_topk_backward(logits, ids, w, dw, renorm), ref)
+        out = torch.full((T, E + left + 4), 7.0, dtype=dtype, device=DEV)
+        code = nvq.NVQ_DTYPE_BF16 if dtype == torch.bfloat16 else nvq.NVQ_DTYPE_F32
+        assert nvq.lib.moe_topk_backward(logits.data_ptr(), code, T, E, logits.stride(0), ids.data_ptr(), w.data_ptr(), dw.data_ptr(), K,
+                                         int(renorm), out[:, left:].data_ptr(), out.stride(0),
+                                         torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(out[:, left:left + E], ref)
+        assert (out[:, :left] == 7).all() and (out[:, left + E:] == 7).all()
+
+
 def test_the_chain_in_bf16(nvq):
     """Products in bf16 hand moe_combine_backward a Y whose gradient nvfp4_gemm_grouped_dx takes as it is."""
     rng = np.random.default_rng(21)
