@@ -572,7 +572,7 @@ int nvfp4_gemm_grouped_dx(const void* dY, int dy_dtype, int64_t rows, int64_t m,
 /*
  * moe_combine -- each token's rows back: out[t] = sum_s weights[t][s] *
  * Y[pos[t][s]], summed in fp32 in slot order.
- *   Y        device [rows x ldy] of y_dtype, d columns.
+ *   Y        device [rows x ldy] of y_dtype, 1 <= d <= 2^33 columns.
  *   pos      device int32 [T x top_k] as moe_sort writes it; a slot whose row
  *            is outside [0, rows) counts as a row of zeros (so a NaN weight
  *            still gives NaN).

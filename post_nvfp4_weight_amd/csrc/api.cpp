@@ -848,10 +848,10 @@ int moe_combine(const void* Y, int y_dtype, int64_t rows, int64_t d, int64_t ldy
                 const float* weights, int64_t T, int64_t top_k, void* out, int out_dtype, int64_t ldo, void* stream) {
   const char* fn = "moe_combine";
   if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype)) return failp(NVQ_ERR_DTYPE, fn, "y_dtype %d, out_dtype %d", y_dtype, out_dtype);
-  if (slots(T, top_k) < 0 || rows < 0 || rows > 0x7FFFFFFF || d < 1 || ldy < d || ldo < d)
+  if (slots(T, top_k) < 0 || rows < 0 || rows > 0x7FFFFFFF || d < 1 || d > (1ll << 33) || ldy < d || ldo < d)
     return failp(NVQ_ERR_SHAPE, fn,
                  "T=%lld top_k=%lld rows=%lld d=%lld ldy=%lld ldo=%lld (need T>=0, top_k>0, T*top_k<2^31, "
-                 "0<=rows<2^31, d>0, ldy>=d, ldo>=d)",
+                 "0<=rows<2^31, 0<d<=2^33, ldy>=d, ldo>=d)",
                  (long long)T, (long long)top_k, (long long)rows, (long long)d, (long long)ldy, (long long)ldo);
   if (T == 0) return NVQ_OK;
   if ((rows > 0 && !Y) || !pos || !out) return failp(NVQ_ERR_NULL, fn, "Y, pos and out are required");

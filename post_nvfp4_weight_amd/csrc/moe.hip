@@ -760,10 +760,11 @@ hipError_t topk_dispatch(int64_t T, int E, int K, F f) {
   return hipErrorInvalidValue;
 }
 
-// f(t0, nt) for parts of T tokens, as many as a launch of that many threads per token holds.
+// f(t0, nt) for parts of T tokens, as many as a launch of that many threads per token holds: whole workgroups
+// (at most 16 tokens each, where a token has few threads), or single tokens where fewer than 64 fit.
 template <typename F>
 hipError_t in_parts(int64_t T, int64_t threads, F f) {
-  const int64_t most = kMaxThreads / threads / 64 * 64;   // (whole workgroups: at most 16 tokens each)
+  const int64_t fit = kMaxThreads / threads, most = fit < 64 ? fit : fit / 64 * 64;
   if (most == 0) return hipErrorInvalidValue;
   for (int64_t t0 = 0; t0 < T; t0 += most) {
     f(t0, std::min(most, T - t0));

@@ -132,3 +132,15 @@ def test_the_chain_in_bf16(nvq):
     ref = moe.combine(moe.grouped_matmul_dx(_np(dY), W, _np(off)), _np(pos))
     mag = moe.combine(moe.grouped_matmul_dx(np.abs(_np(dY)), np.abs(W), _np(off)), _np(pos))
     assert np.all(np.abs(_np(dX) - ref) <= mag * ((m / 16 + 16) * 2.0 ** -23 + K * U) + 1e-30)
+
+
+@pytest.mark.parametrize("T", [2, 65])
+def test_weighted_sum_of_rows_of_2_28_columns(nvq, T):
+    """Where one launch holds fewer than 64 tokens, 65 take two.  Small whole numbers: every product and sum is exact."""
+    d = 2 ** 28 + 5
+    y = (torch.arange(d, device=DEV, dtype=torch.int32) % 7 - 3).float()[None]
+    pos = torch.zeros(T, 1, dtype=torch.int32, device=DEV)
+    w = (torch.arange(T, device=DEV) % 5 - 2).float()[:, None]
+    out = nvq.moe_combine(y, pos, w, out_dtype=torch.bfloat16)
+    for t in range(T):
+        assert torch.equal(out[t], (y[0] * float(t % 5 - 2)).to(torch.bfloat16))
