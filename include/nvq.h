@@ -550,6 +550,9 @@ int moe_sort(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int32_t* t
  *            A rejected weight row (scales 0x7F) gives NaN in its column of
  *            every row that has a token.
  *   Y        device [rows x ldy] of y_dtype (fp32 or bf16, RNE), ldy >= m.
+ * One launch holds 2^24 - 8 tiles of the result, of 64 or 128 rows by 128 or
+ * 256 columns; sizes whose offsets could make more are refused
+ * (NVQ_ERR_SHAPE): (rows / 64 + min(rows, G)) ceil(m / 128) up to that always fits.
  */
 int nvfp4_gemm_grouped(const void* X, int x_dtype, int64_t n, int64_t k, int64_t ldx, const int32_t* tok_idx,
                        int64_t rows, const int64_t* grp_off, int64_t G, const uint8_t* codes, const uint8_t* scales,

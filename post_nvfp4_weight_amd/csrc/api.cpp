@@ -751,6 +751,12 @@ int experts_check(const char* fn, int64_t rows, const int64_t* grp_off, int64_t 
     return failp(NVQ_ERR_ALIGN, fn, "grp_off and codes must be 8-byte aligned, g and the output by their elements");
   return NVQ_OK;
 }
+int experts_status(hipError_t e, const char* fn, int64_t rows, int64_t G, int64_t width) {
+  if (e == kTooManyTiles)
+    return failp(NVQ_ERR_SHAPE, fn, "rows=%lld, G=%lld and %lld columns make more tiles than one launch holds", (long long)rows,
+                 (long long)G, (long long)width);
+  return hip_status(e, fn);
+}
 size_t elem_size(int dtype) { return dtype == NVQ_DTYPE_BF16 ? 2 : 4; }
 }  // namespace
 
@@ -824,8 +830,9 @@ int nvfp4_gemm_grouped(const void* X, int x_dtype, int64_t n, int64_t k, int64_t
   if (!aligned(X, 16)) return failp(NVQ_ERR_ALIGN, fn, "X must be 16-byte aligned");
   if (!aligned(tok_idx, 4)) return failp(NVQ_ERR_ALIGN, fn, "tok_idx must be 4-byte aligned");
   if (Y == X) return failp(NVQ_ERR_VALUE, fn, "Y may not be X");
-  return hip_status(nvfp4_gemm_grouped_launch((const uint16_t*)X, n, k, ldx, tok_idx, rows, grp_off, G, codes, scales, g,
-                                              m, Y, y_dtype == NVQ_DTYPE_BF16, ldy, (hipStream_t)stream), fn);
+  return experts_status(nvfp4_gemm_grouped_launch((const uint16_t*)X, n, k, ldx, tok_idx, rows, grp_off, G, codes, scales,
+                                                  g, m, Y, y_dtype == NVQ_DTYPE_BF16, ldy, (hipStream_t)stream),
+                        fn, rows, G, m);
 }
 
 int nvfp4_gemm_grouped_dx(const void* dY, int dy_dtype, int64_t rows, int64_t m, int64_t lddy, const int64_t* grp_off,
@@ -840,8 +847,9 @@ int nvfp4_gemm_grouped_dx(const void* dY, int dy_dtype, int64_t rows, int64_t m,
   if (!dY) return failp(NVQ_ERR_NULL, fn, "dY is NULL");
   if (!aligned(dY, 2)) return failp(NVQ_ERR_ALIGN, fn, "dY must be 2-byte aligned");
   if (dX == dY) return failp(NVQ_ERR_VALUE, fn, "dX may not be dY");
-  return hip_status(nvfp4_gemm_grouped_dx_launch((const uint16_t*)dY, rows, m, lddy, grp_off, G, codes, scales, g, k, dX,
-                                                 dx_dtype == NVQ_DTYPE_BF16, lddx, (hipStream_t)stream), fn);
+  return experts_status(nvfp4_gemm_grouped_dx_launch((const uint16_t*)dY, rows, m, lddy, grp_off, G, codes, scales, g, k,
+                                                     dX, dx_dtype == NVQ_DTYPE_BF16, lddx, (hipStream_t)stream),
+                        fn, rows, G, k);
 }
 
 int moe_combine(const void* Y, int y_dtype, int64_t rows, int64_t d, int64_t ldy, const int32_t* pos,

@@ -959,7 +959,7 @@ hipError_t nvfp4_gemm_grouped_launch(const uint16_t* X, int64_t n, int64_t k, in
 #define NVQ_LAUNCH(KERNEL, ROWS, COLS, THREADS, ...)                                                                 \
   do {                                                                                                               \
     const int64_t blocks = most_tiles(rows, G, ROWS, (m + (COLS)-1) / (COLS));                                       \
-    if (blocks > kMaxThreads / (THREADS)) return hipErrorInvalidValue;                                               \
+    if (blocks > kMaxThreads / (THREADS)) return kTooManyTiles;                                                      \
     hipLaunchKernelGGL((KERNEL), dim3((unsigned)blocks), dim3(THREADS), 0, s, X, n, k, ldx, tok_idx, rows, grp_off, G, \
                        codes, scales, g, m, Y, ldy __VA_OPT__(, ) __VA_ARGS__);                                      \
     return hipGetLastError();                                                                                        \
@@ -1001,7 +1001,7 @@ hipError_t nvfp4_gemm_grouped_dx_launch(const uint16_t* dY, int64_t rows, int64_
   do {                                                                                                              \
     using TL = GradTile<4, RF, 2>;                                                                                  \
     const int64_t blocks = most_tiles(rows, G, TL::kRows, (k + TL::kCols - 1) / TL::kCols);                         \
-    if (blocks > kMaxThreads / 256) return hipErrorInvalidValue;                                                    \
+    if (blocks > kMaxThreads / 256) return kTooManyTiles;                                                           \
     if (out_bf16)                                                                                                   \
       hipLaunchKernelGGL((grouped_dx_kernel<4, RF, 2, DMA, 1>), dim3((unsigned)blocks), dim3(256), 0, s, dY, rows, m, \
                          lddy, grp_off, G, codes, scales, g, k, dX, lddx, vec);                                     \

@@ -188,6 +188,8 @@ hipError_t nvfp4_gemm_launch(const uint16_t* X, int64_t T, int64_t k, int64_t ld
 constexpr int64_t kMoeMaxExperts = 1024;   // of the router and the sort
 constexpr int kMoeMaxTopK = 64;            // of the router (one lane per slot)
 constexpr int64_t kMaxThreads = 0xFFFFFFFF;   // of one launch
+// The experts' products return this, before any launch, where their tiles are more than one launch holds.
+constexpr hipError_t kTooManyTiles = hipErrorInvalidConfiguration;
 hipError_t moe_topk_launch(const void* logits, int bf16, int64_t T, int64_t E, int64_t ld, int K, int renorm,
                            int32_t* ids, float* weights, hipStream_t s);
 hipError_t moe_topk_backward_launch(const void* logits, int bf16, int64_t T, int64_t E, int64_t ld, const int32_t* ids,
