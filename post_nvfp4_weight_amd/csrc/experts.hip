@@ -125,17 +125,17 @@ __device__ __forceinline__ constexpr int waitcnt_vm_lgkm0(int n) { return (n & 1
 //   Scales: 8 bytes per channel and chunk to registers, one chunk ahead (on the
 //   large tile two chunks at a time).
 // What bounds it, by the rows per expert.  Many: the matrix cores, and with them
-// the power: 16384 tokens x 8 of 256 experts 2048 x 4096 take 1.96 to 2.04 ms (1.1
+// the power: 16384 tokens x 8 of 256 experts 2048 x 4096 take 1.94 to 2.07 ms (1.1
 // PFLOP/s), the cores busy two thirds of the cycles at 1.3 to 1.6 GHz, the
 // expansion (2.5 vector operations a code) between the products; the library's
 // dense product of as many flops takes 1.42 to 1.75 ms at 85 %.  Few: reading the
-// codes: 64 tokens x 8 read 595 MB in 0.17 to 0.19 ms (3.3 TB/s), the vector
-// units busy half of it with the expansion.  Tried and slower there: smaller and
-// wider tiles (64 x 64, 32 x 128, 32 x 256: 184 to 230 us against 185), other
-// starting places in k for other tiles (208).  Tried and slower for many rows:
-// 256 x 256 tiles on 8 waves and 256 rows on 4 (2.5 ms), 8 waves on 128 x 512
-// (equal), products in groups before their expansion (2.09 ms), each product
-// followed by its own (2.06 ms against 2.04 in the same run).
+// codes: 64 tokens x 8 (122 to 156 experts in use, 140 on average: 663 MB) take
+// 0.165 ms, 4.0 TB/s, the vector units busy half of it with the expansion.  Tried
+// and slower there: smaller and wider tiles (64 x 64, 32 x 128, 32 x 256: 184 to
+// 230 us against 185), other starting places in k for other tiles (208).  Tried
+// and slower for many rows: 256 x 256 tiles on 8 waves and 256 rows on 4 (2.5 ms),
+// 8 waves on 128 x 512 (equal), products in groups before their expansion (2.09
+// ms), each product followed by its own (2.06 ms against 2.04 in the same run).
 template <int NW, int RF, int CF, int CR>
 struct Tile {
   static constexpr int kRows = 32 * RF, kCols = 32 * CF * NW;
@@ -519,7 +519,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grouped_gemm_kernel(const uint16_t
 // Lanes without a row read the tile's last row's activations and are not
 // stored.  The waves' partial sums are added in wave order through LDS.
 // Bound by one pass of loads over a cold weight: 8 rows on 256 experts 2048 x
-// 4096 read 38 MB in 14 us (2.7 TB/s).  Waves that each take their own channels
+// 4096 read 38 MB in 13.7 us (2.8 TB/s).  Waves that each take their own channels
 // over all of k instead: 251 us against 197 at 64 tokens.
 constexpr int FW = 8, FROWS = 16, FCG = 2, FCOLS = 16 * FCG, FD = 2;
 typedef float f32x4c __attribute__((ext_vector_type(4)));
@@ -673,7 +673,7 @@ __global__ __launch_bounds__(64 * FW, 4) void grouped_few_kernel(const uint16_t*
 // [block][m].  dY's rows are copied like the activations when m and their
 // stride are multiples of 8 (DMA), else through registers, zeros past m.
 // Bound as the forward product: 4099 tokens x 6 of 64 experts 2048 x 2048 take
-// 230 us (0.9 PFLOP/s), the matrix cores busy 45 %, the vector units (two scales
+// 234 us (0.9 PFLOP/s), the matrix cores busy 45 %, the vector units (two scales
 // per code pair) about as long.  8 waves on 256 x 256: 289 us against 276.
 template <int NW, int RF, int CF>
 struct GradTile {

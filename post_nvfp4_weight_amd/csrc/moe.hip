@@ -337,7 +337,7 @@ __global__ __launch_bounds__(256) void topk_backward_kernel(const L* __restrict_
 // sums, and the rows, three launches.  A chunk's rows are first sorted in LDS
 // and leave in runs per expert: written one by one, 4 bytes each, they took
 // the last launch 15.5 us instead of 12.5 (2^21 assignments, 256 experts).
-// Bound at that size by the ballots' instructions: 19 us over all, of which the
+// Bound at that size by the ballots' instructions: 20 us over all, of which the
 // 25 MB would take 5; up to 2^16 by the launches' own 11 us.
 constexpr int SORT_T = 1024, SORT_W = SORT_T / 64;
 
@@ -620,7 +620,7 @@ __device__ __forceinline__ void store_vec(E* p, const float (&v)[VW]) {
 
 // One thread per vector of a token's columns: blockDim = (columns, tokens).
 // KC slots' loads are in flight together; sums run in slot order.  Bound by
-// reading the rows once: 16384 x 8 rows of 4096 bf16 in 230 us, 5.2 TB/s.
+// reading the rows once: 16384 x 8 rows of 4096 bf16 in 225 us, 5.4 TB/s.
 constexpr int KC = 8;
 template <typename Y, typename O, int VW>
 __global__ __launch_bounds__(256) void combine_kernel(const Y* __restrict__ y, int64_t rows, int64_t d, int64_t ldy,
@@ -661,7 +661,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const Y* __restrict__ y, i
 // Its gradients: a workgroup of NW waves per token, dout's row read once for
 // KC slots at a time; each lane sums its columns' products, then lanes and
 // waves are added in a fixed order.  Bound by the rows' traffic: 5003 x 6 rows
-// of 2056 fp32 and their gradients (0.54 GB) in 130 us, 4.1 TB/s.
+// of 2056 fp32 and their gradients (0.54 GB) in 126 us, 4.2 TB/s.
 template <typename G, typename Y, int VW, int NW>
 __global__ __launch_bounds__(64 * NW) void combine_backward_kernel(const G* __restrict__ dout, int64_t T, int64_t d,
                                                                    int64_t ldd, const Y* __restrict__ y, int64_t rows,
