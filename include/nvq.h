@@ -58,6 +58,8 @@ extern "C" {
 /* ---- element types of W, X and dequantized outputs ------------------------ */
 #define NVQ_DTYPE_F32  0
 #define NVQ_DTYPE_BF16 1
+/* activations that mxfp4_quantize has quantized (X of mxfp4_gemm alone) */
+#define NVQ_DTYPE_MXFP4 2
 
 /* ---- flags of gptq_nvfp4_quantize ------------------------------------------ */
 /* Round to nearest without GPTQ updates: U is not read; each block's scale is
@@ -600,6 +602,88 @@ int moe_combine(const void* Y, int y_dtype, int64_t rows, int64_t d, int64_t ldy
 int moe_combine_backward(const void* dout, int dout_dtype, int64_t T, int64_t d, int64_t ldd, const void* Y, int y_dtype,
                          int64_t rows, int64_t ldy, const int32_t* pos, const float* weights, int64_t top_k, void* dY,
                          int64_t lddy, float* dweights, void* stream);
+
+/*
+ * ---- MXFP4: activations and weights in the matrix cores' own 4-bit format -------
+ * Microscaled 4-bit floating point: E2M1 elements as above, 32 consecutive
+ * ones of a row under one power of two (E8M0: byte b stands for 2^(b - 127),
+ * 255 for NaN).  gfx950 multiplies this format without expansion, so a layer
+ * whose activations may be 4-bit too runs mxfp4_quantize -> mxfp4_gemm, beside
+ * the weight-only NVFP4 product.
+ *   codes   uint8 [rows x k/2], two per byte, the even column in the low nibble;
+ *   scales  uint8 [rows x k/32], byte-aligned.
+ */
+
+/*
+ * mxfp4_quantize -- each block of 32 to nearest: E = floor(log2(max|x|)) - 2,
+ * clamped to [-127, 127], byte E + 127; codes the nearest E2M1 value of
+ * x 2^-E, ties to the even code, at most 6 (so a block's largest values lose up
+ * to a quarter where they lie above 6 2^E).  A block of zeros has byte 0 (and
+ * codes 0 up to their signs), one with a NaN or an infinity byte 255 and codes 0:
+ * its values are NaN.
+ *   X       device [n x ldx] of x_dtype (fp32 or bf16), aligned by its elements;
+ *           0 <= n < 2^31, k > 0, k % 32 == 0, k at most 4000000, ldx >= k.
+ *   codes   device, 16-byte aligned; scales device.
+ * The gradient passes straight through: that of the values is taken as that of X.
+ */
+int mxfp4_quantize(const void* X, int x_dtype, int64_t n, int64_t k, int64_t ldx, uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * mxfp4_dequantize -- out = e2m1(code) 2^(byte - 127), exact in fp32 and in bf16
+ * (an infinity above their range).
+ *   codes  16-byte aligned; out device [n x k] of out_dtype, 16-byte aligned.
+ */
+int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, int64_t k, void* out, int out_dtype, void* stream);
+
+/*
+ * mxfp4_gemm -- Y = Q(X) W^T, both operands MXFP4, products exact, sums in fp32
+ * on the block-scaled matrix cores.
+ *   X       device: [n x ldx] bf16 or fp32, aligned by its elements, which the
+ *           call quantizes (the values of mxfp4_quantize); or with x_dtype
+ *           NVQ_DTYPE_MXFP4 codes [n x k/2], 16-byte aligned, ldx = k, and x_scales [n x k/32]
+ *           (not read otherwise).  Sizes as for mxfp4_quantize.
+ *   codes [m x k/2] (16-byte aligned), scales [m x k/32]: the weights; 1 <= m <= 4000000.
+ *   Y       device [n x ldy] of y_dtype (fp32 or bf16, RNE), ldy >= m.
+ *   ws      device workspace of mxfp4_gemm_workspace_size(x_dtype, n, k, m)
+ *           bytes (256-aligned; may be NULL when that is 0).
+ * A block of NaN makes its row of Y NaN, in the weights its column.  Nothing
+ * depends on timing; a row's result depends on n (the sums' order does).
+ */
+size_t mxfp4_gemm_workspace_size(int x_dtype, int64_t n, int64_t k, int64_t m);
+int mxfp4_gemm(const void* X, int x_dtype, const uint8_t* x_scales, int64_t n, int64_t k, int64_t ldx, const uint8_t* codes,
+               const uint8_t* scales, int64_t m, void* Y, int y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * mxfp4_gemm_dx -- gradient of mxfp4_gemm with respect to its quantized
+ * activations, taken as that of X: dX = dY W (the weights are frozen).  W is
+ * exact in bf16; bf16 matrix cores, fp32 sums.
+ *   dY      device bf16 [n x lddy], lddy >= m, aligned by its elements.
+ *   dX      device [n x lddx] of dx_dtype (fp32 or bf16, RNE), lddx >= k.
+ *   The rest as for mxfp4_gemm.
+ */
+int mxfp4_gemm_dx(const void* dY, int dy_dtype, int64_t n, int64_t m, int64_t lddy, const uint8_t* codes, const uint8_t* scales,
+                  int64_t k, void* dX, int dx_dtype, int64_t lddx, void* stream);
+
+/*
+ * ---- the gated activation between the products of an MLP -------------------------
+ * swiglu -- X = [gate | up], out = silu(gate) * up with silu(x) = x / (1 +
+ * exp(-x)), in fp32, rounded once.  Between the products of a dense MLP and
+ * between nvfp4_gemm_grouped's (its sorted rows) alike.
+ *   X       device [n x ldx] of x_dtype: gate in columns 0 .. h - 1, up in h ..
+ *           2h - 1; 0 <= n < 2^31, 1 <= h <= 4000000, ldx >= 2h.
+ *   out     device [n x ldo] of out_dtype, ldo >= h.
+ * fp32 or bf16, pointers aligned by their elements.  All n rows are computed.
+ */
+int swiglu(const void* X, int x_dtype, int64_t n, int64_t h, int64_t ldx, void* out, int out_dtype, int64_t ldo, void* stream);
+
+/*
+ * swiglu_backward -- gradient of swiglu with respect to X: with s the sigmoid
+ * of gate, dgate = dout up s (1 + gate (1 - s)), dup = dout gate s.
+ *   dout    device [n x ldd], X [n x ldx], dX [n x lddx], all of dtype;
+ *           ldd >= h, ldx and lddx >= 2h.  No output may overlap an input.
+ */
+int swiglu_backward(const void* dout, int64_t ldd, const void* X, int dtype, int64_t n, int64_t h, int64_t ldx, void* dX, int64_t lddx,
+                    void* stream);
 
 /* Text of a status code; never NULL. */
 const char* nvq_status_string(int status);

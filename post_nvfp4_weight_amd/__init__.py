@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libnvq.so")
 
 NVQ_DTYPE_F32 = 0
 NVQ_DTYPE_BF16 = 1
+NVQ_DTYPE_MXFP4 = 2
 FLAG_RTN = 1
 FLAG_NO_ERR = 2
 FLAG_FP64 = 4
@@ -38,6 +39,8 @@ EXPORTS = [
     "nvfp4_dequantize", "nvfp4_gemm_workspace_size", "nvfp4_gemm", "nvfp4_gemm_noalloc", "nvq_check_finite",
     "moe_topk", "moe_topk_backward", "moe_sort_workspace_size", "moe_sort",
     "nvfp4_gemm_grouped", "nvfp4_gemm_grouped_dx", "moe_combine", "moe_combine_backward",
+    "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm_workspace_size", "mxfp4_gemm", "mxfp4_gemm_dx",
+    "swiglu", "swiglu_backward",
     "nvq_status_string", "nvq_last_error",
 ]
 
@@ -87,6 +90,13 @@ def _load():
         "nvfp4_gemm_grouped_dx": (I32, [P, I32, I64, I64, I64, P, I64, P, P, P, I64, P, I32, I64, P]),
         "moe_combine": (I32, [P, I32, I64, I64, I64, P, P, I64, I64, P, I32, I64, P]),
         "moe_combine_backward": (I32, [P, I32, I64, I64, I64, P, I32, I64, I64, P, P, I64, P, I64, P, P]),
+        "mxfp4_quantize": (I32, [P, I32, I64, I64, I64, P, P, P]),
+        "mxfp4_dequantize": (I32, [P, P, I64, I64, P, I32, P]),
+        "mxfp4_gemm_workspace_size": (SZ, [I32, I64, I64, I64]),
+        "mxfp4_gemm": (I32, [P, I32, P, I64, I64, I64, P, P, I64, P, I32, I64, P, SZ, P]),
+        "mxfp4_gemm_dx": (I32, [P, I32, I64, I64, I64, P, P, I64, P, I32, I64, P]),
+        "swiglu": (I32, [P, I32, I64, I64, I64, P, I32, I64, P]),
+        "swiglu_backward": (I32, [P, I64, P, I32, I64, I64, I64, P, I64, P]),
         "nvq_status_string": (ctypes.c_char_p, [I32]),
         "nvq_last_error": (ctypes.c_char_p, []),
     }
@@ -618,3 +628,103 @@ def moe_combine_backward(dout, Y, pos, weights=None, dY=None, need_dY=True, need
     _call(lib.moe_combine_backward, "moe_combine_backward", dev, dout.data_ptr(), _CODES[dout.dtype], T, d, ldd, _addr(Y), _CODES[like.dtype],
           rows, ldy, pos.data_ptr(), _addr(weights), K, _addr(dY), lddy, _addr(dw))
     return dY, dw
+
+
+# ---- MXFP4 and the gated activation ----------------------------------------------
+# mxfp4_quantize -> mxfp4_gemm -> swiglu -> mxfp4_gemm is a dense MLP on 4-bit
+# activations and weights; swiglu also stands between the experts' products.
+
+def _mxfp4(codes, scales, name, dev):
+    """(rows, k) of MXFP4 codes [rows, k/2] and scales [rows, k/32] on device number dev (None: any)."""
+    _want(codes, name, (_U8,), (None, None), dev)
+    rows, kh = codes.shape
+    if kh % 16:
+        raise ValueError(f"{name} has {kh} bytes per row, not a multiple of 16 (blocks of 32)")
+    dev = codes.get_device()
+    _dense(codes, name, _U8, (rows, kh), dev)
+    _dense(scales, f"{name}' scales", _U8, (rows, kh // 16), dev)
+    return rows, 2 * kh
+
+
+def mxfp4_quantize(X):
+    """(codes uint8 [n, k/2], scales uint8 [n, k/32]) of X [n, k] bf16 or fp32: E2M1 elements, 32 of a row under one power of
+    two (byte b: 2^(b - 127), 255: NaN).  For gradients the quantization counts as the identity."""
+    n, k, ldx = _matrix(X, "X", _FLOATS)
+    codes = X.new_empty((n, k // 2), dtype=_U8)
+    scales = X.new_empty((n, k // 32), dtype=_U8)
+    _call(lib.mxfp4_quantize, "mxfp4_quantize", X.get_device(), X.data_ptr(), _CODES[X.dtype], n, k, ldx, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, out_dtype=torch.float32):
+    """The values [n, k] of MXFP4 codes and scales, exact in fp32 and in bf16."""
+    n, k = _mxfp4(codes, scales, "codes", None)
+    if out_dtype not in _FLOATS:
+        raise TypeError(f"unsupported dtype {out_dtype}")
+    out = codes.new_empty((n, k), dtype=out_dtype)
+    _call(lib.mxfp4_dequantize, "mxfp4_dequantize", codes.get_device(), codes.data_ptr(), scales.data_ptr(), n, k, out.data_ptr(),
+          _CODES[out_dtype])
+    return out
+
+
+def mxfp4_gemm(X, codes, scales, x_scales=None, out_dtype=torch.float32, Y=None):
+    """Y = Q(X) W^T [n, m] on 4-bit operands, W the MXFP4 codes [m, k/2] and scales [m, k/32].
+
+    X: [n, k] bf16 or fp32, quantized within the call as by mxfp4_quantize; or the codes [n, k/2] that mxfp4_quantize gave,
+    with their x_scales (one quantization for several products of the same activations)."""
+    m, k = _mxfp4(codes, scales, "codes", None)
+    dev = codes.get_device()
+    if x_scales is not None:
+        n, kx = _mxfp4(X, x_scales, "X", dev)
+        ldx, code = kx, NVQ_DTYPE_MXFP4
+    else:
+        n, kx, ldx = _matrix(X, "X", _FLOATS, dev)
+        code = _CODES[X.dtype]
+    if kx != k:
+        raise ValueError(f"X has {kx} columns, the weights {k} inputs")
+    Y, ldy = _output(Y, "Y", X, n, m, out_dtype, dev)
+    need = lib.mxfp4_gemm_workspace_size(code, n, k, m)
+    ws = _workspace(need, X.device) if need else None
+    _call(lib.mxfp4_gemm, "mxfp4_gemm", dev, X.data_ptr(), code, _addr(x_scales), n, k, ldx, codes.data_ptr(), scales.data_ptr(), m,
+          Y.data_ptr(), _CODES[Y.dtype], ldy, _addr(ws), need)
+    return Y
+
+
+def mxfp4_gemm_dx(dY, codes, scales, out_dtype=torch.float32, dX=None):
+    """Gradient of mxfp4_gemm with respect to X (its quantization counts as the identity): dX = dY W, dY [n, m] bf16."""
+    m, k = _mxfp4(codes, scales, "codes", None)
+    dev = codes.get_device()
+    n, my, lddy = _matrix(dY, "dY", (_BF16,), dev)
+    if my != m:
+        raise ValueError(f"dY has {my} columns, the weights {m} outputs")
+    dX, lddx = _output(dX, "dX", dY, n, k, out_dtype, dev)
+    _call(lib.mxfp4_gemm_dx, "mxfp4_gemm_dx", dev, dY.data_ptr(), NVQ_DTYPE_BF16, n, m, lddy, codes.data_ptr(), scales.data_ptr(), k,
+          dX.data_ptr(), _CODES[dX.dtype], lddx)
+    return dX
+
+
+def swiglu(X, out_dtype=None, out=None):
+    """silu(gate) * up [n, h] of X = [gate | up] [n, 2h], bf16 or fp32; out_dtype None: X's."""
+    n, w, ldx = _matrix(X, "X", _FLOATS)
+    if w % 2:
+        raise ValueError(f"X has {w} columns, an odd number")
+    dev = X.get_device()
+    out, ldo = _output(out, "out", X, n, w // 2, out_dtype or X.dtype, dev)
+    _call(lib.swiglu, "swiglu", dev, X.data_ptr(), _CODES[X.dtype], n, w // 2, ldx, out.data_ptr(), _CODES[out.dtype], ldo)
+    return out
+
+
+def swiglu_backward(dout, X, dX=None):
+    """Gradient of swiglu with respect to X [n, 2h]; dout [n, h] of X's dtype, which dX has too."""
+    n, w, ldx = _matrix(X, "X", _FLOATS)
+    if w % 2:
+        raise ValueError(f"X has {w} columns, an odd number")
+    dev = X.get_device()
+    nd, h, ldd = _matrix(dout, "dout", (X.dtype,), dev)
+    if (nd, 2 * h) != (n, w):
+        raise ValueError(f"dout has shape {tuple(dout.shape)}, not {(n, w // 2)}")
+    if dX is not None and (not isinstance(dX, torch.Tensor) or dX.dtype is not X.dtype):
+        raise TypeError("dX must be a tensor of X's dtype")
+    dX, lddx = _output(dX, "dX", X, n, w, X.dtype, dev)
+    _call(lib.swiglu_backward, "swiglu_backward", dev, dout.data_ptr(), ldd, X.data_ptr(), _CODES[X.dtype], n, h, ldx, dX.data_ptr(), lddx)
+    return dX

@@ -894,4 +894,130 @@ int moe_combine_backward(const void* dout, int dout_dtype, int64_t T, int64_t d,
                                                 dweights, (hipStream_t)stream), fn);
 }
 
+// ---- MXFP4: quantization, product, gradient; the gated activation -------------------------
+namespace {
+constexpr int64_t kMaxWidth = 4000000;   // of one row, as for the experts' products
+// n rows of k values in blocks of 32.
+int mx_shape(const char* fn, int64_t n, int64_t k) {
+  if (n < 0 || n > 0x7FFFFFFF || k < 32 || k % 32 != 0 || k > kMaxWidth)
+    return failp(NVQ_ERR_SHAPE, fn, "rows=%lld k=%lld (need 0<=rows<2^31, k>0, k%%32==0, k at most %lld)", (long long)n, (long long)k,
+                 (long long)kMaxWidth);
+  return NVQ_OK;
+}
+int mx_weights(const char* fn, int64_t m, const uint8_t* codes, const uint8_t* scales) {
+  if (!codes || !scales) return failp(NVQ_ERR_NULL, fn, "codes and scales are required");
+  if (!aligned(codes, 16)) return failp(NVQ_ERR_ALIGN, fn, "codes must be 16-byte aligned");
+  return NVQ_OK;
+}
+int tiles_status(hipError_t e, const char* fn, int64_t n, int64_t width) {
+  if (e == kTooManyTiles)
+    return failp(NVQ_ERR_SHAPE, fn, "rows=%lld and %lld columns make more tiles than one launch holds", (long long)n, (long long)width);
+  return hip_status(e, fn);
+}
+}  // namespace
+
+int mxfp4_quantize(const void* X, int x_dtype, int64_t n, int64_t k, int64_t ldx, uint8_t* codes, uint8_t* scales, void* stream) {
+  const char* fn = "mxfp4_quantize";
+  if (!dtype_ok(x_dtype)) return failp(NVQ_ERR_DTYPE, fn, "x_dtype %d", x_dtype);
+  const int rc = mx_shape(fn, n, k);
+  if (rc != NVQ_OK) return rc;
+  if (ldx < k) return failp(NVQ_ERR_SHAPE, fn, "ldx=%lld (need >= k=%lld)", (long long)ldx, (long long)k);
+  if (n == 0) return NVQ_OK;
+  if (!X || !codes || !scales) return failp(NVQ_ERR_NULL, fn, "X, codes and scales are required");
+  if (!aligned(X, elem_size(x_dtype)) || !aligned(codes, 16))
+    return failp(NVQ_ERR_ALIGN, fn, "X must be aligned by its elements, codes 16-byte");
+  return hip_status(mxfp4_quantize_launch(X, x_dtype == NVQ_DTYPE_BF16, n, k, ldx, codes, scales, (hipStream_t)stream), fn);
+}
+
+int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, int64_t k, void* out, int out_dtype, void* stream) {
+  const char* fn = "mxfp4_dequantize";
+  if (!dtype_ok(out_dtype)) return failp(NVQ_ERR_DTYPE, fn, "out_dtype %d", out_dtype);
+  int rc = mx_shape(fn, n, k);
+  if (rc != NVQ_OK || n == 0) return rc;
+  rc = mx_weights(fn, n, codes, scales);
+  if (rc != NVQ_OK) return rc;
+  if (!out) return failp(NVQ_ERR_NULL, fn, "out is required");
+  if (!aligned(out, 16)) return failp(NVQ_ERR_ALIGN, fn, "out must be 16-byte aligned");
+  return hip_status(mxfp4_dequantize_launch(codes, scales, n, k, out, out_dtype == NVQ_DTYPE_BF16, (hipStream_t)stream), fn);
+}
+
+size_t mxfp4_gemm_workspace_size(int x_dtype, int64_t n, int64_t k, int64_t m) {
+  if (n <= 0 || k <= 0 || m <= 0 || (!dtype_ok(x_dtype) && x_dtype != NVQ_DTYPE_MXFP4)) return 0;
+  return align_up(mxfp4_gemm_workspace(x_dtype == NVQ_DTYPE_MXFP4, n, k, m));
+}
+
+int mxfp4_gemm(const void* X, int x_dtype, const uint8_t* x_scales, int64_t n, int64_t k, int64_t ldx, const uint8_t* codes,
+               const uint8_t* scales, int64_t m, void* Y, int y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "mxfp4_gemm";
+  const bool packed = x_dtype == NVQ_DTYPE_MXFP4;
+  if ((!packed && !dtype_ok(x_dtype)) || !dtype_ok(y_dtype)) return failp(NVQ_ERR_DTYPE, fn, "x_dtype %d, y_dtype %d", x_dtype, y_dtype);
+  int rc = mx_shape(fn, n, k);
+  if (rc != NVQ_OK) return rc;
+  if (m < 1 || m > kMaxWidth || (packed ? ldx != k : ldx < k) || ldy < m)
+    return failp(NVQ_ERR_SHAPE, fn, "m=%lld k=%lld ldx=%lld ldy=%lld (need 0<m<=%lld, ldx>=k, ldx==k for MXFP4, ldy>=m)", (long long)m,
+                 (long long)k, (long long)ldx, (long long)ldy, (long long)kMaxWidth);
+  if (n == 0) return NVQ_OK;
+  rc = mx_weights(fn, m, codes, scales);
+  if (rc != NVQ_OK) return rc;
+  if (!X || !Y || (packed && !x_scales)) return failp(NVQ_ERR_NULL, fn, "X, Y and with MXFP4 x_scales are required");
+  if (!aligned(X, packed ? 16 : elem_size(x_dtype)) || !aligned(Y, elem_size(y_dtype)))
+    return failp(NVQ_ERR_ALIGN, fn, "X and Y must be aligned by their elements, MXFP4 codes 16-byte");
+  if (Y == X) return failp(NVQ_ERR_VALUE, fn, "Y may not be X");
+  const size_t need = mxfp4_gemm_workspace(packed, n, k, m);
+  if (need && (!ws || ws_bytes < need || !aligned(ws, kAlign)))
+    return failp(NVQ_ERR_WORKSPACE, fn, "workspace needs %zu bytes (256-aligned), got %zu", need, ws_bytes);
+  return tiles_status(mxfp4_gemm_launch(X, packed, x_dtype == NVQ_DTYPE_BF16, x_scales, n, k, ldx, codes, scales, m, Y,
+                                        y_dtype == NVQ_DTYPE_BF16, ldy, ws, (hipStream_t)stream), fn, n, m);
+}
+
+int mxfp4_gemm_dx(const void* dY, int dy_dtype, int64_t n, int64_t m, int64_t lddy, const uint8_t* codes, const uint8_t* scales,
+                  int64_t k, void* dX, int dx_dtype, int64_t lddx, void* stream) {
+  const char* fn = "mxfp4_gemm_dx";
+  if (dy_dtype != NVQ_DTYPE_BF16) return failp(NVQ_ERR_DTYPE, fn, "dy_dtype %d (gradients must be bf16)", dy_dtype);
+  if (!dtype_ok(dx_dtype)) return failp(NVQ_ERR_DTYPE, fn, "dx_dtype %d", dx_dtype);
+  int rc = mx_shape(fn, n, k);
+  if (rc != NVQ_OK) return rc;
+  if (m < 1 || m > kMaxWidth || lddy < m || lddx < k)
+    return failp(NVQ_ERR_SHAPE, fn, "m=%lld k=%lld lddy=%lld lddx=%lld (need 0<m<=%lld, lddy>=m, lddx>=k)", (long long)m, (long long)k,
+                 (long long)lddy, (long long)lddx, (long long)kMaxWidth);
+  if (n == 0) return NVQ_OK;
+  rc = mx_weights(fn, m, codes, scales);
+  if (rc != NVQ_OK) return rc;
+  if (!dY || !dX) return failp(NVQ_ERR_NULL, fn, "dY and dX are required");
+  if (!aligned(dY, 2) || !aligned(dX, elem_size(dx_dtype))) return failp(NVQ_ERR_ALIGN, fn, "dY and dX must be aligned by their elements");
+  if (dX == dY) return failp(NVQ_ERR_VALUE, fn, "dX may not be dY");
+  return tiles_status(mxfp4_gemm_dx_launch((const uint16_t*)dY, n, m, lddy, codes, scales, k, dX, dx_dtype == NVQ_DTYPE_BF16, lddx,
+                                           (hipStream_t)stream), fn, n, k);
+}
+
+int swiglu(const void* X, int x_dtype, int64_t n, int64_t h, int64_t ldx, void* out, int out_dtype, int64_t ldo, void* stream) {
+  const char* fn = "swiglu";
+  if (!dtype_ok(x_dtype) || !dtype_ok(out_dtype)) return failp(NVQ_ERR_DTYPE, fn, "x_dtype %d, out_dtype %d", x_dtype, out_dtype);
+  if (n < 0 || n > 0x7FFFFFFF || h < 1 || h > kMaxWidth || ldx < 2 * h || ldo < h)
+    return failp(NVQ_ERR_SHAPE, fn, "n=%lld h=%lld ldx=%lld ldo=%lld (need 0<=n<2^31, 0<h<=%lld, ldx>=2h, ldo>=h)", (long long)n,
+                 (long long)h, (long long)ldx, (long long)ldo, (long long)kMaxWidth);
+  if (n == 0) return NVQ_OK;
+  if (!X || !out) return failp(NVQ_ERR_NULL, fn, "X and out are required");
+  if (!aligned(X, elem_size(x_dtype)) || !aligned(out, elem_size(out_dtype)))
+    return failp(NVQ_ERR_ALIGN, fn, "X and out must be aligned by their elements");
+  if (out == X) return failp(NVQ_ERR_VALUE, fn, "out may not be X");
+  return hip_status(swiglu_launch(X, x_dtype == NVQ_DTYPE_BF16, n, h, ldx, out, out_dtype == NVQ_DTYPE_BF16, ldo, (hipStream_t)stream), fn);
+}
+
+int swiglu_backward(const void* dout, int64_t ldd, const void* X, int dtype, int64_t n, int64_t h, int64_t ldx, void* dX, int64_t lddx,
+                    void* stream) {
+  const char* fn = "swiglu_backward";
+  if (!dtype_ok(dtype)) return failp(NVQ_ERR_DTYPE, fn, "dtype %d", dtype);
+  if (n < 0 || n > 0x7FFFFFFF || h < 1 || h > kMaxWidth || ldx < 2 * h || ldd < h || lddx < 2 * h)
+    return failp(NVQ_ERR_SHAPE, fn, "n=%lld h=%lld ldx=%lld ldd=%lld lddx=%lld (need 0<=n<2^31, 0<h<=%lld, ldx and lddx>=2h, ldd>=h)",
+                 (long long)n, (long long)h, (long long)ldx, (long long)ldd, (long long)lddx, (long long)kMaxWidth);
+  if (n == 0) return NVQ_OK;
+  if (!dout || !X || !dX) return failp(NVQ_ERR_NULL, fn, "dout, X and dX are required");
+  const size_t es = elem_size(dtype);
+  if (!aligned(dout, es) || !aligned(X, es) || !aligned(dX, es))
+    return failp(NVQ_ERR_ALIGN, fn, "pointers must be aligned by their elements");
+  if (dX == X || dX == dout) return failp(NVQ_ERR_VALUE, fn, "dX may not be X or dout");
+  return hip_status(swiglu_backward_launch(dout, ldd, X, dtype == NVQ_DTYPE_BF16, n, h, ldx, dX, lddx, (hipStream_t)stream), fn);
+}
+
 }  // extern "C"

@@ -675,10 +675,31 @@ __global__ __launch_bounds__(64 * FW, 4) void grouped_few_kernel(const uint16_t*
 // Bound as the forward product: 4099 tokens x 6 of 64 experts 2048 x 2048 take
 // 234 us (0.9 PFLOP/s), the matrix cores busy 45 %, the vector units (two scales
 // per code pair) about as long.  8 waves on 256 x 256: 289 us against 276.
-template <int NW, int RF, int CF>
+// The two weight formats differ in their scales alone.  F::kBlock: codes per
+// scale.  A scale is staged as it is multiplied by: an E4M3 byte, or the bf16
+// of an E8M0 byte (2^-127 is a bf16 below the normal range, NaN stays NaN).
+struct Nvfp4 {
+  static constexpr int kBlock = 16, kBytes = 1;
+  // Of the scales of 16 m, those of m = 8 v + 2 piece and the next.
+  static __device__ __forceinline__ f32x2c pair(const u32x4 (&s)[1], int v, int piece) {
+    const int w = (int)s[0][2 * v + (piece >> 1)];
+    const f32x2c p = (piece & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8(w, true) : __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
+    return p;
+  }
+};
+struct Mxfp4 {
+  static constexpr int kBlock = 32, kBytes = 2;
+  static __device__ __forceinline__ f32x2c pair(const u32x4 (&s)[2], int v, int piece) {
+    const uint32_t w = s[v][piece];
+    return f32x2c{__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)};
+  }
+  static __device__ __forceinline__ uint32_t bf16_of(uint32_t byte) { return byte == 0 ? 0x0040u : byte == 255 ? 0x7FC0u : byte << 7; }
+};
+
+template <int NW, int RF, int CF, typename F>
 struct GradTile {
   static constexpr int kRows = 32 * RF, kCols = 32 * CF * NW, kStride = kCols / 2;   // bytes of codes per m
-  static constexpr int kYBuf = kRows * 128, kCBuf = 64 * kStride, kSBuf = 64 * kCols / 16;
+  static constexpr int kYBuf = kRows * 128, kCBuf = 64 * kStride, kSBuf = 64 * kCols / F::kBlock * F::kBytes;
   static constexpr int kYLoads = 4 * RF / NW, kCLoads = kCBuf / 1024 / NW;
   static constexpr int kLds = 3 * (kYBuf + kCBuf + kSBuf);
   static_assert(kStride == 128 && NW == 4, "the swizzle and the copies' shapes");
@@ -690,9 +711,8 @@ typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ u32x2 read_tr4(const char* p) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr4_b64_v2i32((__attribute__((address_space(3))) i32x2*)p));
 }
-// Codes m, m + 1 (byte `piece` of word) under their scales (byte pair `piece` % 2 of sw).
-__device__ __forceinline__ uint32_t dq_pair(uint32_t word, uint32_t sw, int piece) {
-  const f32x2c s = (piece & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)sw, true) : __builtin_amdgcn_cvt_pk_f32_fp8((int)sw, false);
+// Codes m, m + 1 (byte `piece` of word) under their scales.
+__device__ __forceinline__ uint32_t dq_pair(uint32_t word, f32x2c s, int piece) {
   f32x2c v;
   switch (piece) {
     case 0: v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 0); break;
@@ -704,18 +724,31 @@ __device__ __forceinline__ uint32_t dq_pair(uint32_t word, uint32_t sw, int piec
 }
 
 // The codes and scales of product pair u of a step, for CF groups of 32 channels.
-template <int CF>
+template <int CF, typename F>
 struct GradCodes {
   u32x2 w[CF];
-  u32x4 s[CF];
+  u32x4 s[CF][F::kBytes];
 };
-template <int CF>
+template <int CF, typename F>
 __device__ __forceinline__ void read_grad_codes(const char* cb, const char* sb, int u, const int (&crd)[CF],
-                                                const int (&srd)[CF], GradCodes<CF>& q) {
+                                                const int (&srd)[CF], GradCodes<CF, F>& q) {
 #pragma unroll
   for (int f = 0; f < CF; ++f) {
     q.w[f] = read_tr4(cb + u * 4096 + crd[f]);
-    q.s[f] = *(const u32x4*)(sb + u * 32 + srd[f]);
+#pragma unroll
+    for (int b = 0; b < F::kBytes; ++b) q.s[f][b] = *(const u32x4*)(sb + u * 32 * F::kBytes + srd[f] + 16 * b);
+  }
+}
+
+// A thread's scales of a step to LDS, [block][m].
+template <typename F>
+__device__ __forceinline__ void store_scale(char* sw, uint32_t v) {
+  if constexpr (F::kBytes == 1) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) sw[b * 64] = (char)(v >> (8 * b));
+  } else {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) *(uint16_t*)(sw + b * 128) = (uint16_t)(v >> (16 * b));
   }
 }
 
@@ -728,32 +761,31 @@ struct GradRows {
 // One step: its four products, the copies of two steps on, and to LDS what
 // registers hold of the next step.  yb, cb, sb: this step's buffers, n: the
 // next step's, d: two steps on; all distinct.
-template <int NW, int RF, int CF, bool DMA>
+template <int NW, int RF, int CF, bool DMA, typename F>
 __device__ __forceinline__ void gradient_step(const char* __restrict__ yb, const char* __restrict__ cb,
                                               const char* __restrict__ sb, const char* __restrict__ yn,
                                               const char* __restrict__ cn, const char* __restrict__ sn,
                                               char* __restrict__ yw, char* __restrict__ sw, char* __restrict__ yd,
                                               char* __restrict__ cd, const uint16_t* ysrc, uint32_t ybound,
                                               const uint8_t* csrc, uint32_t cbound,
-                                              const uint32_t (&yoff)[GradTile<NW, RF, CF>::kYLoads],
-                                              const uint32_t (&coff)[GradTile<NW, RF, CF>::kCLoads], bool in,
+                                              const uint32_t (&yoff)[GradTile<NW, RF, CF, F>::kYLoads],
+                                              const uint32_t (&coff)[GradTile<NW, RF, CF, F>::kCLoads], bool in,
                                               const int (&yrd)[4], const int (&crd)[CF], const int (&srd)[CF],
-                                              GradCodes<CF>& q, bf16x8 (&ya)[RF], u32x4 (&qa)[2][CF],
+                                              GradCodes<CF, F>& q, bf16x8 (&ya)[RF], u32x4 (&qa)[2][CF],
                                               f32x16 (&acc)[RF][CF], uint32_t& sreg, GradRows<RF>& yreg, auto load_next) {
-  using TL = GradTile<NW, RF, CF>;
+  using TL = GradTile<NW, RF, CF, F>;
   constexpr int NY = DMA ? TL::kYLoads : 0, NC = TL::kCLoads;
-  GradCodes<CF> q1;
+  GradCodes<CF, F> q1;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int p = j & 1;
     if (j == 0) {
       // What registers hold of the next step to LDS, then the loads of the step behind it.
-#pragma unroll
-      for (int b = 0; b < 4; ++b) sw[b * 64] = (char)(sreg >> (8 * b));
+      store_scale<F>(sw, sreg);
       if (!DMA)
 #pragma unroll
         for (int r = 0; r < RF; ++r) *(u32x4*)(yw + r * NW * 1024) = yreg.v[r];
-      read_grad_codes<CF>(cb, sb, 1, crd, srd, q1);
+      read_grad_codes<CF, F>(cb, sb, 1, crd, srd, q1);
       __builtin_amdgcn_sched_barrier(0);
       load_next();
       __builtin_amdgcn_sched_barrier(0);
@@ -763,7 +795,7 @@ __device__ __forceinline__ void gradient_step(const char* __restrict__ yb, const
       __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(NY + NC + 1));
       asm volatile("s_barrier" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      read_grad_codes<CF>(cn, sn, 0, crd, srd, q);
+      read_grad_codes<CF, F>(cn, sn, 0, crd, srd, q);
     }
 #pragma unroll
     for (int i = 0; i < RF; ++i) {
@@ -775,8 +807,8 @@ __device__ __forceinline__ void gradient_step(const char* __restrict__ yb, const
       for (int e = i * 4 * CF / RF; e < (i + 1) * 4 * CF / RF; ++e) {
         const int f = e / 4, piece = e % 4, v = (j + 1) & 1;
         // product j + 1: pair 0 or 1 of this step, or pair 0 of the next
-        const GradCodes<CF>& c = j == 1 || j == 2 ? q1 : q;
-        qa[p ^ 1][f][piece] = dq_pair(c.w[f][v], c.s[f][2 * v + (piece >> 1)], piece);
+        const GradCodes<CF, F>& c = j == 1 || j == 2 ? q1 : q;
+        qa[p ^ 1][f][piece] = dq_pair(c.w[f][v], F::pair(c.s[f], v, piece), piece);
       }
       if (DMA && j == 0) copy_lds<TL::kYLoads, NW * 1024>(yd, ysrc, ybound, yoff, in, i * NY / RF, (i + 1) * NY / RF);
       if (j == 1) copy_lds<NC, NW * 1024>(cd, csrc, cbound, coff, true, i * NC / RF, (i + 1) * NC / RF);
@@ -785,16 +817,16 @@ __device__ __forceinline__ void gradient_step(const char* __restrict__ yb, const
   }
 }
 
-template <int NW, int RF, int CF, bool DMA, int OUT_BF16>
+template <int NW, int RF, int CF, bool DMA, int OUT_BF16, typename F>
 __device__ __forceinline__ void tile_gradient(char* smem, const RowTile& tl, const uint16_t* __restrict__ dY, int64_t m,
                                               int64_t lddy, const uint8_t* __restrict__ codes,
                                               const uint8_t* __restrict__ scales, float g, int64_t k,
                                               void* __restrict__ dX, int64_t lddx, bool vec_out) {
-  using TL = GradTile<NW, RF, CF>;
+  using TL = GradTile<NW, RF, CF, F>;
   constexpr int NC = TL::kCLoads;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5;
-  const int64_t kb = k / 16;
+  const int64_t kb = k / F::kBlock;
   const int64_t t0 = tl.col * TL::kCols, o0 = t0 + wave * 32 * CF;   // the tile's and the wave's first channel
 
   // Copy q of a step: rows 8 (NW q + wave) + lane / 8 of dY (of the step's m for codes), 16-byte piece `piece`.
@@ -815,21 +847,23 @@ __device__ __forceinline__ void tile_gradient(char* smem, const RowTile& tl, con
     return (uint32_t)min(max((int64_t)0, (m - 64 * st) * (k / 2) - t0 / 2), (int64_t)0xFFFFFF00);
   };
   auto csrc = [&](int64_t st) { return codes + 64 * st * (k / 2) + t0 / 2; };
-  // Scales: the thread brings 4 blocks of row tid / 4 of the step; zeros past m.
-  const int sm = tid >> 2, sq = (tid & 3) * 4;
+  // Scales: the thread brings 4 bytes to LDS, of SQ blocks of row tid / 4 of the step; zeros past m.
+  constexpr int SQ = 4 / F::kBytes;
+  const int sm = tid >> 2, sq = (tid & 3) * SQ;
   auto load_scale = [&](int64_t st) {
-    const int64_t mm = st * 64 + sm, b0 = t0 / 16 + sq;
+    const int64_t mm = st * 64 + sm, b0 = t0 / F::kBlock + sq;
     uint32_t v = 0;
-    if (kb % 4 == 0) {   // whole words inside the row
+    if (F::kBytes == 1 && kb % 4 == 0) {   // whole words inside the row
       const bool ok = mm < m && b0 < kb;
       v = *(const u32_any*)(scales + (ok ? mm * kb + b0 : 0));
       v = ok ? v : 0;
     } else {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
+      for (int b = 0; b < SQ; ++b) {
         const bool ok = mm < m && b0 + b < kb;
         const uint32_t x = scales[ok ? mm * kb + b0 + b : 0];
-        v |= (ok ? x : 0) << (8 * b);
+        if constexpr (F::kBytes == 1) v |= (ok ? x : 0) << (8 * b);
+        else v |= (ok ? Mxfp4::bf16_of(x) : 0) << (16 * b);
       }
     }
     return v;
@@ -856,7 +890,7 @@ __device__ __forceinline__ void tile_gradient(char* smem, const RowTile& tl, con
 #pragma unroll
   for (int f = 0; f < CF; ++f) {
     crd[f] = (16 * h + (lane & 15)) * 128 + ((wave * CF + f) ^ ((lane & 15) >> 1)) * 16 + 8 * (c >> 4);
-    srd[f] = (wave * 2 * CF + 2 * f + (c >> 4)) * 64 + 16 * h;
+    srd[f] = ((((wave * CF + f) * 32 + c) / F::kBlock) * 64 + 16 * h) * F::kBytes;
   }
 
   f32x16 acc[RF][CF];
@@ -871,13 +905,12 @@ __device__ __forceinline__ void tile_gradient(char* smem, const RowTile& tl, con
   char *y0 = smem, *y1 = y0 + TL::kYBuf, *y2 = y1 + TL::kYBuf;
   char *c0 = smem + 3 * TL::kYBuf, *c1 = c0 + TL::kCBuf, *c2 = c1 + TL::kCBuf;
   char *s0 = smem + 3 * (TL::kYBuf + TL::kCBuf), *s1 = s0 + TL::kSBuf, *s2 = s1 + TL::kSBuf;
-  const int wo = wave * 1024, yo = wo + lane * 16, so = sq * 64 + sm;
+  const int wo = wave * 1024, yo = wo + lane * 16, so = (sq * 64 + sm) * F::kBytes;
   const int nsteps = (int)((m + 63) / 64);
   GradRows<RF> yreg;
   uint32_t sreg = load_scale(0);
   if (!DMA) load_rows(0, yreg);
-#pragma unroll
-  for (int b = 0; b < 4; ++b) s0[so + b * 64] = (char)(sreg >> (8 * b));
+  store_scale<F>(s0 + so, sreg);
   if (!DMA)
 #pragma unroll
     for (int q = 0; q < RF; ++q) *(u32x4*)(y0 + yo + q * NW * 1024) = yreg.v[q];
@@ -893,19 +926,19 @@ __device__ __forceinline__ void tile_gradient(char* smem, const RowTile& tl, con
   __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((DMA ? TL::kYLoads : 0) + NC));   // step 0's have landed
   asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
-  GradCodes<CF> q;
+  GradCodes<CF, F> q;
   u32x4 qa[2][CF];
   bf16x8 ya[RF];
-  read_grad_codes<CF>(c0, s0, 0, crd, srd, q);
+  read_grad_codes<CF, F>(c0, s0, 0, crd, srd, q);
 #pragma unroll
   for (int i = 0; i < RF; ++i) ya[i] = *(const bf16x8*)(y0 + i * 4096 + yrd[0]);
 #pragma unroll
   for (int f = 0; f < CF; ++f)
 #pragma unroll
-    for (int p = 0; p < 4; ++p) qa[0][f][p] = dq_pair(q.w[f][0], q.s[f][p >> 1], p);
+    for (int p = 0; p < 4; ++p) qa[0][f][p] = dq_pair(q.w[f][0], F::pair(q.s[f], 0, p), p);
 
   for (int st = 0; st < nsteps; ++st) {
-    gradient_step<NW, RF, CF, DMA>(y0, c0, s0, y1, c1, s1, y1 + yo, s1 + so, y2 + wo, c2 + wo, dY + 64 * (int64_t)(st + 2),
+    gradient_step<NW, RF, CF, DMA, F>(y0, c0, s0, y1, c1, s1, y1 + yo, s1 + so, y2 + wo, c2 + wo, dY + 64 * (int64_t)(st + 2),
                                    ybound(st + 2), csrc(st + 2), cbound(st + 2), yoff, coff, inside(st + 2), yrd, crd, srd, q,
                                    ya, qa, acc, sreg, yreg, [&]() {
                                      sreg = load_scale(st + 2);
@@ -932,13 +965,37 @@ __global__ __launch_bounds__(64 * NW, 2) void grouped_dx_kernel(const uint16_t* 
                                                                 const uint8_t* __restrict__ scales,
                                                                 const float* __restrict__ gs, int64_t k,
                                                                 void* __restrict__ dX, int64_t lddx, int vec_out) {
-  using TL = GradTile<NW, RF, CF>;
+  using TL = GradTile<NW, RF, CF, Nvfp4>;
   __shared__ __attribute__((aligned(1024))) char smem[TL::kLds];
   RowTile tl;
   if (!find_tile<TL::kRows>(off, G, rows, (uint32_t)((k + TL::kCols - 1) / TL::kCols), &tl)) return;
   for_row_blocks<RF>(tl, [&]<int R>() {
-    tile_gradient<NW, R, CF, DMA, OUT_BF16>(smem, tl, dY, m, lddy, codes + tl.expert * m * (k / 2),
+    tile_gradient<NW, R, CF, DMA, OUT_BF16, Nvfp4>(smem, tl, dY, m, lddy, codes + tl.expert * m * (k / 2),
                                             scales + tl.expert * m * (k / 16), gs[tl.expert], k, dX, lddx, vec_out != 0);
+  });
+}
+
+// The gradient of one MXFP4 matrix's product: row tiles without a search, in
+// contiguous runs per XCD as above.
+template <int NW, int RF, int CF, bool DMA, int OUT_BF16>
+__global__ __launch_bounds__(64 * NW, 2) void mx_dx_kernel(const uint16_t* __restrict__ dY, int64_t rows, int64_t m,
+                                                           int64_t lddy, const uint8_t* __restrict__ codes,
+                                                           const uint8_t* __restrict__ scales, int64_t k,
+                                                           void* __restrict__ dX, int64_t lddx, int vec_out) {
+  using TL = GradTile<NW, RF, CF, Mxfp4>;
+  __shared__ __attribute__((aligned(1024))) char smem[TL::kLds];
+  const uint32_t ncol = (uint32_t)((k + TL::kCols - 1) / TL::kCols);
+  const uint64_t all = (uint64_t)((rows + TL::kRows - 1) / TL::kRows) * ncol, per = (all + 7) / 8;
+  const uint64_t id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= per || id >= all) return;
+  const uint32_t tile = (uint32_t)id / ncol;   // (fewer than 2^31 workgroups)
+  RowTile tl;
+  tl.expert = 0;
+  tl.col = (uint32_t)id - tile * ncol;
+  tl.r0 = (int64_t)tile * TL::kRows;
+  tl.r1 = min(rows, tl.r0 + TL::kRows);
+  for_row_blocks<RF>(tl, [&]<int R>() {
+    tile_gradient<NW, R, CF, DMA, OUT_BF16, Mxfp4>(smem, tl, dY, m, lddy, codes, scales, 1.0f, k, dX, lddx, vec_out != 0);
   });
 }
 
@@ -999,7 +1056,7 @@ hipError_t nvfp4_gemm_grouped_dx_launch(const uint16_t* dY, int64_t rows, int64_
   const bool dma = m % 8 == 0 && lddy % 8 == 0 && (uintptr_t)dY % 16 == 0 && lddy < (1 << 23);
 #define NVQ_DX(RF, DMA)                                                                                             \
   do {                                                                                                              \
-    using TL = GradTile<4, RF, 2>;                                                                                  \
+    using TL = GradTile<4, RF, 2, Nvfp4>;                                                                                  \
     const int64_t blocks = most_tiles(rows, G, TL::kRows, (k + TL::kCols - 1) / TL::kCols);                         \
     if (blocks > kMaxThreads / 256) return kTooManyTiles;                                                           \
     if (out_bf16)                                                                                                   \
@@ -1014,6 +1071,34 @@ hipError_t nvfp4_gemm_grouped_dx_launch(const uint16_t* dY, int64_t rows, int64_
   // tokens 500 / 499, 4096 tokens 942 / 788.
   const int64_t avg = rows / std::min(rows, G);
   if (avg >= 24) {
+    if (dma) NVQ_DX(4, true);
+    else NVQ_DX(4, false);
+  } else {
+    if (dma) NVQ_DX(2, true);
+    else NVQ_DX(2, false);
+  }
+#undef NVQ_DX
+  return hipGetLastError();
+}
+
+hipError_t mxfp4_gemm_dx_launch(const uint16_t* dY, int64_t rows, int64_t m, int64_t lddy, const uint8_t* codes,
+                                const uint8_t* scales, int64_t k, void* dX, int out_bf16, int64_t lddx, hipStream_t s) {
+  const int vec = lddx % (out_bf16 ? 8 : 4) == 0 && (uintptr_t)dX % 16 == 0;
+  const bool dma = m % 8 == 0 && lddy % 8 == 0 && (uintptr_t)dY % 16 == 0 && lddy < (1 << 23);
+#define NVQ_DX(RF, DMA)                                                                                                \
+  do {                                                                                                                 \
+    using TL = GradTile<4, RF, 2, Mxfp4>;                                                                              \
+    const int64_t tiles = ((rows + TL::kRows - 1) / TL::kRows) * ((k + TL::kCols - 1) / TL::kCols);                    \
+    const int64_t blocks = (tiles + 7) / 8 * 8;                                                                        \
+    if (blocks > kMaxThreads / 256) return kTooManyTiles;                                                              \
+    if (out_bf16)                                                                                                      \
+      hipLaunchKernelGGL((mx_dx_kernel<4, RF, 2, DMA, 1>), dim3((unsigned)blocks), dim3(256), 0, s, dY, rows, m, lddy, \
+                         codes, scales, k, dX, lddx, vec);                                                             \
+    else                                                                                                               \
+      hipLaunchKernelGGL((mx_dx_kernel<4, RF, 2, DMA, 0>), dim3((unsigned)blocks), dim3(256), 0, s, dY, rows, m, lddy, \
+                         codes, scales, k, dX, lddx, vec);                                                             \
+  } while (0)
+  if (rows > 512) {
     if (dma) NVQ_DX(4, true);
     else NVQ_DX(4, false);
   } else {

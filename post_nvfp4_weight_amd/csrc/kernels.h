@@ -214,4 +214,21 @@ hipError_t nvfp4_gemm_grouped_dx_launch(const uint16_t* dY, int64_t rows, int64_
                                         const float* g, int64_t k, void* dX, int out_bf16, int64_t lddx,
                                         hipStream_t s);
 
+// ---- MXFP4 and the gated activation (arguments checked by the caller; see include/nvq.h) ----
+hipError_t mxfp4_quantize_launch(const void* X, int bf16, int64_t n, int64_t k, int64_t ldx, uint8_t* codes, uint8_t* scales,
+                                 hipStream_t s);
+hipError_t mxfp4_dequantize_launch(const uint8_t* codes, const uint8_t* scales, int64_t n, int64_t k, void* out, int out_bf16,
+                                   hipStream_t s);
+// x_codes: X is MXFP4 with xscales, else bf16 or fp32 that the call quantizes, into ws where mxfp4_gemm_workspace says so.
+size_t mxfp4_gemm_workspace(int x_codes, int64_t n, int64_t k, int64_t m);
+hipError_t mxfp4_gemm_launch(const void* X, int x_codes, int x_bf16, const uint8_t* xscales, int64_t n, int64_t k, int64_t ldx,
+                             const uint8_t* codes, const uint8_t* scales, int64_t m, void* Y, int out_bf16, int64_t ldy,
+                             void* ws, hipStream_t s);
+hipError_t mxfp4_gemm_dx_launch(const uint16_t* dY, int64_t rows, int64_t m, int64_t lddy, const uint8_t* codes,
+                                const uint8_t* scales, int64_t k, void* dX, int out_bf16, int64_t lddx, hipStream_t s);
+hipError_t swiglu_launch(const void* X, int x_bf16, int64_t n, int64_t h, int64_t ldx, void* out, int out_bf16, int64_t ldo,
+                         hipStream_t s);
+hipError_t swiglu_backward_launch(const void* dout, int64_t ldd, const void* X, int bf16, int64_t n, int64_t h, int64_t ldx,
+                                  void* dX, int64_t lddx, hipStream_t s);
+
 }  // namespace nvq
