@@ -685,6 +685,41 @@ int swiglu(const void* X, int x_dtype, int64_t n, int64_t h, int64_t ldx, void* 
 int swiglu_backward(const void* dout, int64_t ldd, const void* X, int dtype, int64_t n, int64_t h, int64_t ldx, void* dX, int64_t lddx,
                     void* stream);
 
+/*
+ * nvfp4_moe_mlp -- a whole mixture-of-experts MLP for a few tokens (decode): the
+ * router, each token's experts and their weighted sum,
+ *   out[t] = sum_s weights[t][s] D_e (silu(G_e x_t) * (U_e x_t)),  e = ids[t][s],
+ * in two kernels, where moe_topk .. moe_combine with swiglu between two
+ * nvfp4_gemm_grouped take six.  NVFP4 weights expanded to bf16, fp32 sums; the
+ * activation between the products keeps at least 16 significant bits.
+ *
+ *   X        device bf16 [T x ldx], 16-byte aligned, 0 <= T <= 64; d > 0, d % 16
+ *            == 0, ldx >= d, ldx % 8 == 0, (T - 1) ldx + d <= 2^30.
+ *   logits   device [T x ldl] of logits_dtype: ids and weights are chosen from
+ *            them as by moe_topk (1 <= E <= 1024, top_k <= min(E, 64), renorm) and
+ *            written.  Or NULL: ids and weights are read.
+ *   ids      device int32 [T x top_k], weights device fp32 [T x top_k].  A slot
+ *            whose id is outside [0, E) counts as a row of zeros (so a NaN weight
+ *            still gives NaN); an expert named twice counts with both weights.
+ *   gate_up_* the experts' first layer as gptq_nvfp4_quantize_batched writes it:
+ *            codes [E x 2h x d/2] (8-byte aligned), scales [E x 2h x d/16], g [E];
+ *            of each expert's 2h rows the first h are gate, the others up (the
+ *            columns that swiglu takes).  h > 0, h % 16 == 0.
+ *   down_*   their second layer: codes [E x m x h/2], scales [E x m x h/16], g [E].
+ *   out      device [T x ldo] of out_dtype (fp32 or bf16, RNE), ldo >= m.
+ *   ws       device workspace of nvfp4_moe_mlp_workspace_size(T, E, top_k, h)
+ *            bytes (256-aligned).
+ * d, h and m are at most 4000000.  A rejected weight row (scales 0x7F) makes the
+ * results of its expert's tokens NaN, of the others not.  Nothing depends on
+ * timing.  T = 0 does nothing.
+ */
+size_t nvfp4_moe_mlp_workspace_size(int64_t T, int64_t E, int64_t top_k, int64_t h);
+int nvfp4_moe_mlp(const void* X, int x_dtype, int64_t T, int64_t d, int64_t ldx, const void* logits, int logits_dtype, int64_t E,
+                  int64_t ldl, int64_t top_k, int renorm, int32_t* ids, float* weights, const uint8_t* gate_up_codes,
+                  const uint8_t* gate_up_scales, const float* gate_up_g, int64_t h, const uint8_t* down_codes,
+                  const uint8_t* down_scales, const float* down_g, int64_t m, void* out, int out_dtype, int64_t ldo, void* ws,
+                  size_t ws_bytes, void* stream);
+
 /* Text of a status code; never NULL. */
 const char* nvq_status_string(int status);
 /* Reason of the most recent failing call on this thread ("" if none). */

@@ -40,7 +40,7 @@ EXPORTS = [
     "moe_topk", "moe_topk_backward", "moe_sort_workspace_size", "moe_sort",
     "nvfp4_gemm_grouped", "nvfp4_gemm_grouped_dx", "moe_combine", "moe_combine_backward",
     "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm_workspace_size", "mxfp4_gemm", "mxfp4_gemm_dx",
-    "swiglu", "swiglu_backward",
+    "swiglu", "swiglu_backward", "nvfp4_moe_mlp_workspace_size", "nvfp4_moe_mlp",
     "nvq_status_string", "nvq_last_error",
 ]
 
@@ -97,6 +97,9 @@ def _load():
         "mxfp4_gemm_dx": (I32, [P, I32, I64, I64, I64, P, P, I64, P, I32, I64, P]),
         "swiglu": (I32, [P, I32, I64, I64, I64, P, I32, I64, P]),
         "swiglu_backward": (I32, [P, I64, P, I32, I64, I64, I64, P, I64, P]),
+        "nvfp4_moe_mlp_workspace_size": (SZ, [I64, I64, I64, I64]),
+        "nvfp4_moe_mlp": (I32, [P, I32, I64, I64, I64, P, I32, I64, I64, I64, I32, P, P, P, P, P, I64, P, P, P, I64, P, I32, I64, P, SZ,
+                                P]),
         "nvq_status_string": (ctypes.c_char_p, [I32]),
         "nvq_last_error": (ctypes.c_char_p, []),
     }
@@ -728,3 +731,48 @@ def swiglu_backward(dout, X, dX=None):
     dX, lddx = _output(dX, "dX", X, n, w, X.dtype, dev)
     _call(lib.swiglu_backward, "swiglu_backward", dev, dout.data_ptr(), ldd, X.data_ptr(), _CODES[X.dtype], n, h, ldx, dX.data_ptr(), lddx)
     return dX
+
+
+def nvfp4_moe_mlp(X, gate_up, down, logits=None, top_k=None, renorm=True, ids=None, weights=None, out_dtype=torch.bfloat16, out=None):
+    """A whole mixture-of-experts MLP for at most 64 tokens, X [T, d] bf16: (out [T, m], ids int32 [T, K], weights fp32 [T, K]).
+
+    out[t] = sum_s weights[t, s] D_e (silu(G_e x_t) * (U_e x_t)), e = ids[t, s].  The experts are chosen from logits [T, E]
+    (top_k, renorm) as by moe_topk, or given as ids and weights.  gate_up: (codes [E, 2h, d/2], scales [E, 2h, d/16], g [E]),
+    each expert's first h rows gate, the others up; down: (codes [E, m, h/2], scales [E, m, h/16], g [E]), as
+    gptq_nvfp4_quantize_batched gives them.  For more tokens: moe_topk, moe_sort, nvfp4_gemm_grouped, swiglu,
+    nvfp4_gemm_grouped, moe_combine."""
+    T, d, ldx = _matrix(X, "X", (_BF16,))
+    dev = X.get_device()
+    sizes = []
+    for layer, name in ((gate_up, "gate_up"), (down, "down")):
+        codes, scales, g = layer
+        _want(codes, f"{name} codes", (_U8,), (None, None, None), dev)
+        E, rows, kh = codes.shape
+        _dense(codes, f"{name} codes", _U8, (E, rows, kh), dev)
+        _dense(scales, f"{name} scales", _U8, (E, rows, kh // 8), dev)
+        _dense(g, f"{name} g", _F32, (E,), dev)
+        sizes.append((E, rows, 2 * kh))
+    (E, h2, k), (Ed, m, h) = sizes
+    if k != d or Ed != E or h2 != 2 * h:
+        raise ValueError(f"X [{T}, {d}], gate_up of {E} experts [{h2}, {k}] and down of {Ed} experts [{m}, {h}] do not fit together")
+    if logits is not None:
+        if ids is not None or weights is not None or top_k is None:
+            raise ValueError("either logits and top_k, or ids and weights")
+        t, e, ldl = _matrix(logits, "logits", _FLOATS, dev)
+        if (t, e) != (T, E):
+            raise ValueError(f"logits has shape {(t, e)}, not {(T, E)}")
+        K, code = int(top_k), _CODES[logits.dtype]
+        ids = X.new_empty((T, max(0, K)), dtype=_I32)
+        weights = X.new_empty((T, max(0, K)), dtype=_F32)
+    else:
+        if ids is None or weights is None or top_k is not None:
+            raise ValueError("either logits and top_k, or ids and weights")
+        K, ldl, code = _table(ids, "ids", T, dev), 0, 0
+        _dense(weights, "weights", _F32, (T, K), dev)
+    out, ldo = _output(out, "out", X, T, m, out_dtype, dev)
+    need = lib.nvfp4_moe_mlp_workspace_size(T, E, K, h)
+    ws = _workspace(need, X.device) if need else None
+    _call(lib.nvfp4_moe_mlp, "nvfp4_moe_mlp", dev, X.data_ptr(), NVQ_DTYPE_BF16, T, d, ldx, _addr(logits), code, E, ldl, K, bool(renorm),
+          ids.data_ptr(), weights.data_ptr(), gate_up[0].data_ptr(), gate_up[1].data_ptr(), gate_up[2].data_ptr(), h,
+          down[0].data_ptr(), down[1].data_ptr(), down[2].data_ptr(), m, out.data_ptr(), _CODES[out.dtype], ldo, _addr(ws), need)
+    return out, ids, weights

@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvq.so")
 PEAKS_LIB = os.path.join(HERE, "libnvq_peaks.so")
 SOURCES = ["api.cpp", "gemm.hip", "syrk.hip", "factor.hip", "sweep.hip", "consumer.hip", "moe.hip", "experts.hip",
-           "mxfp4.hip", "swiglu.hip"]
+           "mxfp4.hip", "swiglu.hip", "moe_mlp.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

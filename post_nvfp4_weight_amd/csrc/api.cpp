@@ -1020,4 +1020,50 @@ int swiglu_backward(const void* dout, int64_t ldd, const void* X, int dtype, int
   return hip_status(swiglu_backward_launch(dout, ldd, X, dtype == NVQ_DTYPE_BF16, n, h, ldx, dX, lddx, (hipStream_t)stream), fn);
 }
 
+// ---- a whole mixture-of-experts MLP for a few tokens ------------------------------------
+namespace {
+bool moe_mlp_sizes(int64_t T, int64_t E, int64_t top_k, int64_t h) {
+  return T >= 0 && T <= kMoeMlpTokens && E >= 1 && E <= kMoeMaxExperts && top_k >= 1 && top_k <= kMoeMaxTopK && h >= 16 && h % 16 == 0 &&
+         h <= kMaxWidth;
+}
+}  // namespace
+
+size_t nvfp4_moe_mlp_workspace_size(int64_t T, int64_t E, int64_t top_k, int64_t h) {
+  return T > 0 && moe_mlp_sizes(T, E, top_k, h) ? align_up(nvfp4_moe_mlp_workspace(T, E, top_k, h)) : 0;
+}
+
+int nvfp4_moe_mlp(const void* X, int x_dtype, int64_t T, int64_t d, int64_t ldx, const void* logits, int logits_dtype, int64_t E,
+                  int64_t ldl, int64_t top_k, int renorm, int32_t* ids, float* weights, const uint8_t* gate_up_codes,
+                  const uint8_t* gate_up_scales, const float* gate_up_g, int64_t h, const uint8_t* down_codes,
+                  const uint8_t* down_scales, const float* down_g, int64_t m, void* out, int out_dtype, int64_t ldo, void* ws,
+                  size_t ws_bytes, void* stream) {
+  const char* fn = "nvfp4_moe_mlp";
+  if (x_dtype != NVQ_DTYPE_BF16) return failp(NVQ_ERR_DTYPE, fn, "x_dtype %d (activations must be bf16)", x_dtype);
+  if (!dtype_ok(out_dtype) || (logits && !dtype_ok(logits_dtype)))
+    return failp(NVQ_ERR_DTYPE, fn, "logits_dtype %d, out_dtype %d", logits_dtype, out_dtype);
+  if (!moe_mlp_sizes(T, E, std::max<int64_t>(1, std::min<int64_t>(top_k, kMoeMaxTopK)), h) || d < 16 || d % 16 != 0 || d > kMaxWidth ||
+      ldx < d || ldx % 8 != 0 || m < 1 || m > kMaxWidth || ldo < m || (logits && ldl < E) ||
+      ldx > ((1ll << 30) - d) / std::max<int64_t>(1, T - 1))
+    return failp(NVQ_ERR_SHAPE, fn,
+                 "T=%lld d=%lld ldx=%lld E=%lld ldl=%lld h=%lld m=%lld ldo=%lld (need 0<=T<=%lld, 1<=E<=%lld, d and h > 0 and multiples of "
+                 "16, m>0, each at most %lld, ldx>=d, ldx%%8==0, (T-1)*ldx+d<=2^30, ldl>=E, ldo>=m)",
+                 (long long)T, (long long)d, (long long)ldx, (long long)E, (long long)ldl, (long long)h, (long long)m, (long long)ldo,
+                 (long long)kMoeMlpTokens, (long long)kMoeMaxExperts, (long long)kMaxWidth);
+  if (top_k < 1 || top_k > kMoeMaxTopK || (logits && top_k > E))
+    return failp(NVQ_ERR_VALUE, fn, "top_k=%lld (need 1 <= top_k <= %d, and with logits <= E)", (long long)top_k, kMoeMaxTopK);
+  if (T == 0) return NVQ_OK;
+  if (!X || !ids || !weights || !gate_up_codes || !gate_up_scales || !gate_up_g || !down_codes || !down_scales || !down_g || !out)
+    return failp(NVQ_ERR_NULL, fn, "X, ids, weights, both products' codes, scales and g, and out are required");
+  if (!aligned(X, 16) || !aligned(gate_up_codes, 8) || !aligned(down_codes, 8) || !aligned(gate_up_g, 4) || !aligned(down_g, 4) ||
+      !aligned(ids, 4) || !aligned(weights, 4) || !aligned(out, elem_size(out_dtype)) || (logits && !aligned(logits, elem_size(logits_dtype))))
+    return failp(NVQ_ERR_ALIGN, fn, "X must be 16-byte aligned, codes 8-byte, the others by their elements");
+  if (out == X || out == logits) return failp(NVQ_ERR_VALUE, fn, "out may not be X or logits");
+  const size_t need = nvfp4_moe_mlp_workspace_size(T, E, top_k, h);
+  if (!ws || ws_bytes < need || !aligned(ws, kAlign))
+    return failp(NVQ_ERR_WORKSPACE, fn, "workspace needs %zu bytes (256-aligned), got %zu", need, ws_bytes);
+  return hip_status(nvfp4_moe_mlp_launch((const uint16_t*)X, T, d, ldx, logits, logits && logits_dtype == NVQ_DTYPE_BF16, E, ldl, (int)top_k,
+                                         renorm != 0, ids, weights, gate_up_codes, gate_up_scales, gate_up_g, h, down_codes, down_scales,
+                                         down_g, m, out, out_dtype == NVQ_DTYPE_BF16, ldo, ws, (hipStream_t)stream), fn);
+}
+
 }  // extern "C"

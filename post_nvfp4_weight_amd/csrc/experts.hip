@@ -21,17 +21,6 @@ struct RowTile {
   int64_t col;              // column tile
 };
 
-// Inclusive sum over the wave's lanes (row shifts, then the rows' last lanes to the rows behind).
-__device__ __forceinline__ int wave_inclusive(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
-  return v;
-}
-
 // Row tiles of height BT over all experts in order, times ncol column tiles
 // each (column tiles of a row tile next to each other): the one of this
 // workgroup, false if there is none.  The tiles are dealt to the 8 XCDs

@@ -231,4 +231,12 @@ hipError_t swiglu_launch(const void* X, int x_bf16, int64_t n, int64_t h, int64_
 hipError_t swiglu_backward_launch(const void* dout, int64_t ldd, const void* X, int bf16, int64_t n, int64_t h, int64_t ldx,
                                   void* dX, int64_t lddx, hipStream_t s);
 
+// A whole mixture-of-experts MLP for T <= kMoeMlpTokens tokens; logits null: ids and weights are inputs.
+constexpr int64_t kMoeMlpTokens = 64;
+size_t nvfp4_moe_mlp_workspace(int64_t T, int64_t E, int64_t K, int64_t h);
+hipError_t nvfp4_moe_mlp_launch(const uint16_t* X, int64_t T, int64_t d, int64_t ldx, const void* logits, int logits_bf16, int64_t E,
+                                int64_t ldl, int K, int renorm, int32_t* ids, float* weights, const uint8_t* ucodes,
+                                const uint8_t* uscales, const float* ug, int64_t h, const uint8_t* dcodes, const uint8_t* dscales,
+                                const float* dg, int64_t m, void* out, int out_bf16, int64_t ldo, void* ws, hipStream_t s);
+
 }  // namespace nvq
