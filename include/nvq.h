@@ -693,8 +693,8 @@ int swiglu_backward(const void* dout, int64_t ldd, const void* X, int dtype, int
  * nvfp4_gemm_grouped take six.  NVFP4 weights expanded to bf16, fp32 sums; the
  * activation between the products keeps at least 16 significant bits.
  *
- *   X        device bf16 [T x ldx], 16-byte aligned, 0 <= T <= 64; d > 0, d % 16
- *            == 0, ldx >= d, ldx % 8 == 0, (T - 1) ldx + d <= 2^30.
+ *   X        device bf16 [T x ldx], 16-byte aligned, 0 <= T <= 64; d >= 32, d %
+ *            16 == 0, ldx >= d, ldx % 8 == 0, (T - 1) ldx + d <= 2^30.
  *   logits   device [T x ldl] of logits_dtype: ids and weights are chosen from
  *            them as by moe_topk (1 <= E <= 1024, top_k <= min(E, 64), renorm) and
  *            written.  Or NULL: ids and weights are read.
@@ -704,7 +704,7 @@ int swiglu_backward(const void* dout, int64_t ldd, const void* X, int dtype, int
  *   gate_up_* the experts' first layer as gptq_nvfp4_quantize_batched writes it:
  *            codes [E x 2h x d/2] (8-byte aligned), scales [E x 2h x d/16], g [E];
  *            of each expert's 2h rows the first h are gate, the others up (the
- *            columns that swiglu takes).  h > 0, h % 16 == 0.
+ *            columns that swiglu takes).  h >= 32, h % 16 == 0.
  *   down_*   their second layer: codes [E x m x h/2], scales [E x m x h/16], g [E].
  *   out      device [T x ldo] of out_dtype (fp32 or bf16, RNE), ldo >= m.
  *   ws       device workspace of nvfp4_moe_mlp_workspace_size(T, E, top_k, h)

@@ -1023,7 +1023,7 @@ int swiglu_backward(const void* dout, int64_t ldd, const void* X, int dtype, int
 // ---- a whole mixture-of-experts MLP for a few tokens ------------------------------------
 namespace {
 bool moe_mlp_sizes(int64_t T, int64_t E, int64_t top_k, int64_t h) {
-  return T >= 0 && T <= kMoeMlpTokens && E >= 1 && E <= kMoeMaxExperts && top_k >= 1 && top_k <= kMoeMaxTopK && h >= 16 && h % 16 == 0 &&
+  return T >= 0 && T <= kMoeMlpTokens && E >= 1 && E <= kMoeMaxExperts && top_k >= 1 && top_k <= kMoeMaxTopK && h >= 32 && h % 16 == 0 &&
          h <= kMaxWidth;
 }
 }  // namespace
@@ -1041,12 +1041,12 @@ int nvfp4_moe_mlp(const void* X, int x_dtype, int64_t T, int64_t d, int64_t ldx,
   if (x_dtype != NVQ_DTYPE_BF16) return failp(NVQ_ERR_DTYPE, fn, "x_dtype %d (activations must be bf16)", x_dtype);
   if (!dtype_ok(out_dtype) || (logits && !dtype_ok(logits_dtype)))
     return failp(NVQ_ERR_DTYPE, fn, "logits_dtype %d, out_dtype %d", logits_dtype, out_dtype);
-  if (!moe_mlp_sizes(T, E, std::max<int64_t>(1, std::min<int64_t>(top_k, kMoeMaxTopK)), h) || d < 16 || d % 16 != 0 || d > kMaxWidth ||
+  if (!moe_mlp_sizes(T, E, std::max<int64_t>(1, std::min<int64_t>(top_k, kMoeMaxTopK)), h) || d < 32 || d % 16 != 0 || d > kMaxWidth ||
       ldx < d || ldx % 8 != 0 || m < 1 || m > kMaxWidth || ldo < m || (logits && ldl < E) ||
       ldx > ((1ll << 30) - d) / std::max<int64_t>(1, T - 1))
     return failp(NVQ_ERR_SHAPE, fn,
-                 "T=%lld d=%lld ldx=%lld E=%lld ldl=%lld h=%lld m=%lld ldo=%lld (need 0<=T<=%lld, 1<=E<=%lld, d and h > 0 and multiples of "
-                 "16, m>0, each at most %lld, ldx>=d, ldx%%8==0, (T-1)*ldx+d<=2^30, ldl>=E, ldo>=m)",
+                 "T=%lld d=%lld ldx=%lld E=%lld ldl=%lld h=%lld m=%lld ldo=%lld (need 0<=T<=%lld, 1<=E<=%lld, d and h at least 32 and "
+                 "multiples of 16, m>0, each at most %lld, ldx>=d, ldx%%8==0, (T-1)*ldx+d<=2^30, ldl>=E, ldo>=m)",
                  (long long)T, (long long)d, (long long)ldx, (long long)E, (long long)ldl, (long long)h, (long long)m, (long long)ldo,
                  (long long)kMoeMlpTokens, (long long)kMoeMaxExperts, (long long)kMaxWidth);
   if (top_k < 1 || top_k > kMoeMaxTopK || (logits && top_k > E))

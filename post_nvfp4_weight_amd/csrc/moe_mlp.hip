@@ -3,13 +3,25 @@
 //   1. routing (moe_topk's choice, or the caller's), then for each expert in use
 //      and each of its tokens  act = w silu(G x) (U x),  w the token's weight;
 //   2. out[t] = sum over its experts of g_e D act.
-// A token's row is a column of the matrix instructions, so an expert's weights are read and
-// expanded once for all its tokens, and a sum over experts stays in registers.
 // Q = e2m1 * e4m3 is exact in bf16 and g is applied to the sums.  The
 // activation between the products is held as two bf16 parts, hi + lo (16 or more
 // significant bits as long as it is above 2^-110): as one bf16 it would be the one value
 // that the layer rounds to 8 bits before its end, for a product that waits for weights anyway.
-// What bounds it: reading the weights of the experts in use once.
+//
+// What bounds it is reading the weights of the experts in use once, and on the
+// way there the address unit: a load instruction takes it a cycle for each 64
+// bytes that four neighbouring lanes touch in one line, four where they touch four rows, as
+// the matrix instructions' operands ask for (lane l holds row l % 16).  So the
+// lanes are dealt otherwise.  v_mfma_f32_16x16x32_bf16, lane l = 16 q + 4 a + b:
+//   A, load i of a chunk of 512 k:  channel 4 a + i, piece 4 q + b (32 k, 16 bytes), so
+//      that four neighbours read 64 consecutive bytes; row 4 a + b of the product is
+//      channel 4 a + i over the pieces b, 4 + b, 8 + b, 12 + b alone;
+//   B: column 4 t + b is token t over the same pieces.
+// The result at row 4 a + b, column 4 t + b is channel 4 a + i, token t over those
+// pieces, and the sum over b is the whole (entries with another b are
+// not used).  A product thus takes 4 tokens, not 16, which costs nothing: the matrix
+// cores are idle for most of the time.  37 tokens x 8 of 256 experts (2048 x 4096
+// and 4096 x 1024): 172 and 134 us for the two kernels with lanes by rows.
 #include <algorithm>
 
 #include "common.h"
@@ -21,14 +33,22 @@ namespace nvq {
 
 namespace {
 
+// On lambdas: one that is called twice and not inlined keeps what it captures in memory.
+#define NVQ_INLINE __attribute__((always_inline))
+
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
-typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint16_t u16_any __attribute__((aligned(1)));
 
-constexpr int MW = 8;   // waves per workgroup
+constexpr int MW = 8, DW = 8;     // waves per workgroup of the two kernels
+constexpr int kRoutedTokens = 8;   // up to this many are routed by the first kernel, one per wave
+constexpr int kChunk = 512;
+#ifndef UFD
+#define UFD 2
+#define DFD 2
+#endif
 constexpr uint32_t kNone = 0x80000000u;   // an offset past every buffer (checked on the host), also with k's offsets added
 
-// An expert in use: its rows of the activations start at `row`, in the order of its tokens (bits).
+// An expert and some of its tokens (bits), which are rows `row`, `row` + 1, .. of the activations in rising order.
 struct Entry {
   int32_t expert, row;
   uint64_t tokens;
@@ -45,51 +65,75 @@ struct MoeMlp {
   int64_t ldx, ldl, d, h, m, ldo;
   int T, E, K, renorm;
   // workspace
-  int32_t* count;     // experts in use
+  int32_t* count;     // entries
   float* bad;         // per token: 0, or NaN from the weight of a slot without an expert
   Entry* entries;
-  uint16_t *hi, *lo;  // activations [rows x h]
+  uint16_t* act;      // activations, act_row(h) elements per row
 };
 
-// 256 k of 16 CG channels: lane (c = l % 16, q = l / 16) takes the 32 k from 32 q of each 128, of channel c.
-template <int CG>
-struct Pair {
-  u32x4 w[2][CG];
-  uint32_t s[2][CG];
+// A row of the activations: chunks of 512, and in each, for each j of a piece's
+// four times 8 and for hi, then lo, the 16 pieces' 8: what one load takes is 256 bytes in a row.
+__host__ __device__ __forceinline__ int64_t act_row(int64_t h) { return (h + kChunk - 1) / kChunk * kChunk * 2; }
+__device__ __forceinline__ int64_t act_at(int k) { return (int64_t)(k >> 9) * 1024 + ((k >> 3) & 3) * 256 + ((k >> 5) & 15) * 8 + (k & 7); }   // hi; lo 128 behind
+
+// 512 k of 16 channels.  s[i]: two scales, of the piece's halves (16 bits wide, as
+// loaded: a conversion would wait for the load at the loop's end).
+struct Chunk {
+  u32x4 w[4];
+  uint16_t s[4];
 };
-// cp, sp: the channels' first codes and scales (uniform); crow, srow: the lane's offsets, its channel and q included.
-template <int CG>
-__device__ __forceinline__ void load_pair(const uint8_t* const (&cp)[CG], const uint8_t* const (&sp)[CG], uint32_t crow, uint32_t srow,
-                                          int64_t p, int q, int64_t k, Pair<CG>& x) {
-  if ((p + 1) * 256 <= k) {
+// Where a lane reads a tile of 16 channels from: cp, sp the tile's first codes
+// and scales (the same for all lanes), off[i] and soff[i] the lane's channel i and
+// piece in them.  Channels past the last repeat it.
+struct TileAt {
+  const uint8_t *cp, *sp;
+  uint32_t off[4], soff[4];
+  __device__ __forceinline__ void set(const uint8_t* codes, const uint8_t* scales, int64_t first, int64_t left, int64_t k, int lane) {
+    cp = codes + first * (k / 2);
+    sp = scales + first * (k / 16);
+    const int a = (lane >> 2) & 3, piece = 4 * (lane >> 4) + (lane & 3);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int f = 0; f < CG; ++f) {
-        x.w[u][f] = *(const u32x4_any*)(cp[f] + p * 128 + 64 * u + crow);
-        x.s[u][f] = *(const u16_any*)(sp[f] + p * 16 + 8 * u + srow);
-      }
-    return;
-  }
-  // The rest of k: blocks past it as zero codes under zero scales.
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int64_t left = k / 16 - (p * 16 + 8 * u + 2 * q);   // blocks from the lane's first on
-#pragma unroll
-    for (int f = 0; f < CG; ++f) {
-      u32x2 a{0u, 0u}, b{0u, 0u};
-      uint32_t s = 0;
-      if (left > 0) {
-        a = *(const u32x2_any*)(cp[f] + p * 128 + 64 * u + crow);
-        s = sp[f][p * 16 + 8 * u + srow];
-      }
-      if (left > 1) {
-        b = *(const u32x2_any*)(cp[f] + p * 128 + 64 * u + crow + 8);
-        s |= (uint32_t)sp[f][p * 16 + 8 * u + srow + 1] << 8;
-      }
-      x.w[u][f] = u32x4{a[0], a[1], b[0], b[1]};
-      x.s[u][f] = s;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t ch = (uint32_t)min((int64_t)(4 * a + i), left - 1);
+      off[i] = ch * (uint32_t)(k / 2) + 16 * piece;
+      soff[i] = ch * (uint32_t)(k / 16) + 2 * piece;
     }
+  }
+};
+// Chunk ch.  REST: k may end inside it: pieces past k read their channel's first
+// codes, under zero scales, and one that k ends in the middle of is read from 8 bytes
+// before, inside its row, and moved.  The same loads on every path: one that a
+// branch may skip makes the compiler wait for those issued behind it, which are
+// the ones ahead of time.
+template <bool REST>
+__device__ __forceinline__ void load_chunk(const TileAt& t, int ch, int64_t k, int lane, Chunk& x) {
+  const uint32_t left = REST ? (uint32_t)max((int64_t)0, k - (int64_t)ch * kChunk) : 0, at = 32 * (4 * (lane >> 4) + (lane & 3));
+  const bool none = REST && at >= left, half = REST && at + 16 == left;
+  const int64_t c0 = (int64_t)ch * 256, s0 = (int64_t)ch * 32;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (REST) {
+      const int64_t c = none ? (int64_t)t.off[i] - at / 2 : t.off[i] + c0 - (half ? 8 : 0);
+      const int64_t s = none ? (int64_t)t.soff[i] - at / 16 : t.soff[i] + s0 - (half ? 1 : 0);
+      x.w[i] = *(const u32x4_any*)(t.cp + c);
+      x.s[i] = *(const u16_any*)(t.sp + s);
+    } else {
+      x.w[i] = *(const u32x4_any*)(t.cp + c0 + t.off[i]);
+      x.s[i] = *(const u16_any*)(t.sp + s0 + t.soff[i]);
+    }
+  }
+}
+// What load_chunk<true> has loaded, as it stands for (after the wait for it).
+template <bool REST>
+__device__ __forceinline__ void settle(Chunk& x, int ch, int64_t k, int lane) {
+  if (!REST) return;
+  const uint32_t left = (uint32_t)max((int64_t)0, k - (int64_t)ch * kChunk), at = 32 * (4 * (lane >> 4) + (lane & 3));
+  const bool none = at >= left, half = at + 16 == left;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x.w[i][0] = half ? x.w[i][2] : x.w[i][0];
+    x.w[i][1] = half ? x.w[i][3] : x.w[i][1];
+    x.s[i] = none ? (uint16_t)0 : half ? (uint16_t)(x.s[i] >> 8) : x.s[i];
   }
 }
 // The eight k from 8 j of the lane's 32, expanded.
@@ -113,48 +157,80 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint3
   return __amdgpu_buffer_rsrc_t();
 #endif
 }
-// The lane's 32 k of half u of pair p from its row's offset, zeros from k on.
-__device__ __forceinline__ void load_half(__amdgpu_buffer_rsrc_t rs, uint32_t row, int64_t p, int u, int q, int64_t k, u32x4 (&x)[4]) {
-  const int64_t k0 = p * 256 + 128 * u + 32 * q;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x[j] = load16(rs, k0 + 8 * j < k ? row + (uint32_t)(k0 + 8 * j) * 2 : kNone);
-}
-
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-__device__ __forceinline__ Entry uniform_entry(const Entry& e) {
-  Entry r;
-  r.expert = __builtin_amdgcn_readfirstlane(e.expert);
-  r.row = __builtin_amdgcn_readfirstlane(e.row);
-  r.tokens = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)e.tokens) |
-             (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(e.tokens >> 32)) << 32;
-  return r;
-}
 // Tokens before t.
 __device__ __forceinline__ int before(uint64_t tokens, int t) { return __popcll(tokens & ((1ull << t) - 1)); }
+// An entry, the same for the whole wave, and its expert's g.  A lane's column
+// stands for token number 4 g + (l % 16) / 4 of the entry in group g (-1 for none).
+template <int NG>
+struct Columns {
+  Entry e;
+  float scale;
+  int token[NG];
+  __device__ __forceinline__ void set(const Entry& in, float g, int lane) {
+    e.expert = __builtin_amdgcn_readfirstlane(in.expert);
+    e.row = __builtin_amdgcn_readfirstlane(in.row);
+    e.tokens = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)in.tokens) |
+               (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(in.tokens >> 32)) << 32;
+    scale = g;
+    const int mine = (lane >> 2) & 3;
+    uint64_t left = e.tokens;
+#pragma unroll
+    for (int g4 = 0; g4 < NG; ++g4) {
+      token[g4] = -1;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (!left) break;
+        token[g4] = mine == t ? __builtin_ctzll(left) : token[g4];
+        left &= left - 1;
+      }
+    }
+  }
+};
+
+// The sums of 16 channels and 4 tokens out of the four loads' products: the lane
+// gets channel 4 q + b and its column's token, q = l / 16, b = l % 4.
+__device__ __forceinline__ float whole_sum(const f32x4 (&acc)[4], int lane) {
+  const int b = lane & 3;
+  float r = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // (register b of lane 16 q + 4 t + b: row 4 q + b, column 4 t + b)
+    float v = b == 0 ? acc[i][0] : b == 1 ? acc[i][1] : b == 2 ? acc[i][2] : acc[i][3];
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false));   // lanes 1, 0, 3, 2
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false));   // lanes 2, 3, 0, 1
+    r = b == i ? v : r;
+  }
+  return r;
+}
+
+__host__ __device__ __forceinline__ int64_t most_entries(int64_t T, int64_t E, int64_t K, int per) {
+  return (E < T * K ? E : T * K) + T * K / per;
+}
+size_t up_lds(int64_t T, int64_t E, int64_t K, int per) { return E * 8 + T * K * 12 + most_entries(T, E, K, per) * (sizeof(Entry) + 4); }
 
 // Kernel 1.  Every workgroup routes all tokens for itself (a launch for it
-// alone would cost more), lists the experts in use, then takes items, 16
-// channels of gate and of up of one expert, in turn with the other workgroups;
-// the eight waves each a part of k, their sums added in wave order through LDS.
-// NG: groups of 16 tokens.
-size_t up_lds(int64_t T, int64_t E, int64_t K) { return E * 8 + T * K * 8 + std::min(E, T * K) * sizeof(Entry); }
-
-template <typename L, int EPL, int NG>
+// alone would cost more), lists the entries (of up to 4 NG tokens), then takes
+// items, 16 channels of gate and of up of one entry, in turn with the other workgroups;
+// the even waves take gate, the odd ones up, each four a part of k, their
+// sums added in wave order through LDS.  Weights are loaded FD chunks ahead.
+template <typename L, int EPL, int NG, bool REST>
 __global__ __launch_bounds__(64 * MW, NG == 1 ? 4 : 2) void moe_up_kernel(const MoeMlp a) {
-  __shared__ __attribute__((aligned(16))) float part[MW][16][36];
+  constexpr int KP = MW / 2, FD = UFD;
+  __shared__ __attribute__((aligned(16))) float part[MW][4 * NG][16];
   __shared__ int s_count;
   extern __shared__ __attribute__((aligned(16))) char dyn[];
   const int slots = a.T * a.K;
   Entry* list = (Entry*)dyn;
-  uint64_t* mask = (uint64_t*)(list + min(a.E, slots));
+  uint64_t* mask = (uint64_t*)(list + most_entries(a.T, a.E, a.K, 4 * NG));
   int32_t* ids = (int32_t*)(mask + a.E);
   float* ws = (float*)(ids + slots);
+  float* wrow = ws + slots;   // of each row of the activations: its token's weight
+  float* scale = wrow + slots;   // of each entry: its expert's
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int c = lane & 15, q = lane >> 4;
-
   for (int e = tid; e < a.E; e += 64 * MW) mask[e] = 0;
   __syncthreads();
   if (a.logits) {
@@ -184,17 +260,37 @@ __global__ __launch_bounds__(64 * MW, NG == 1 ? 4 : 2) void moe_up_kernel(const 
   if (wave == 0) {
     int n = 0, rows = 0;
     for (int e0 = 0; e0 < a.E; e0 += 64) {
-      const uint64_t tokens = e0 + lane < a.E ? mask[e0 + lane] : 0;
-      const uint64_t used = __ballot(tokens != 0);
-      const int mine = __popcll(tokens), incl = wave_inclusive(mine);
-      if (tokens) list[n + before(used, lane)] = Entry{e0 + lane, rows + incl - mine, tokens};
-      n += __popcll(used);
+      uint64_t tokens = e0 + lane < a.E ? mask[e0 + lane] : 0;
+      const int cnt = __popcll(tokens), ne = (cnt + 4 * NG - 1) / (4 * NG);
+      const int incl = wave_inclusive(cnt), nincl = wave_inclusive(ne);
+      int row = rows + incl - cnt;
+      for (int i = 0; i < ne; ++i, row += 4 * NG) {
+        uint64_t part = tokens;
+        if (i + 1 < ne) {
+          part = 0;
+          for (int b = 0; b < 4 * NG; ++b, tokens &= tokens - 1) part |= tokens & -tokens;
+        }
+        list[n + nincl - ne + i] = Entry{e0 + lane, row, part};
+      }
+      n += __builtin_amdgcn_readlane(nincl, 63);
       rows += __builtin_amdgcn_readlane(incl, 63);
     }
     if (lane == 0) s_count = n;
   }
   __syncthreads();
   const int used = __builtin_amdgcn_readfirstlane(s_count);
+  for (int i = tid; i < used; i += 64 * MW) {
+    const Entry e = list[i];
+    scale[i] = a.ug[e.expert];
+    int row = e.row;
+    for (uint64_t left = e.tokens; left; left &= left - 1, ++row) {
+      const int t = __builtin_ctzll(left);
+      float w = 0.0f;
+      for (int s = 0; s < a.K; ++s) w += ids[t * a.K + s] == e.expert ? ws[t * a.K + s] : 0.0f;
+      wrow[row] = w;
+    }
+  }
+  __syncthreads();
   if (blockIdx.x == 0) {
     if (tid == 0) *a.count = used;
     for (int i = tid; i < used; i += 64 * MW) a.entries[i] = list[i];
@@ -209,269 +305,269 @@ __global__ __launch_bounds__(64 * MW, NG == 1 ? 4 : 2) void moe_up_kernel(const 
   }
 
   const int nt = (int)((a.h + 15) / 16), items = used * nt;
-  const int64_t kh = a.d / 2, kb = a.d / 16;
-  const int npairs = (int)((a.d + 255) / 256), mine = npairs > wave ? (npairs - wave + MW - 1) / MW : 0;
+  if ((int)blockIdx.x >= items) return;
+  const int kp = wave >> 1, f = wave & 1;
+  const int chunks = (int)((a.d + kChunk - 1) / kChunk), mine = chunks > kp ? (chunks - kp + KP - 1) / KP : 0;   // of k, of the wave
   const __amdgpu_buffer_rsrc_t xbuf = buffer_of(a.X, (uint32_t)(((a.T - 1) * a.ldx + a.d) * 2));
-  uint32_t xrow[NG];
-#pragma unroll
-  for (int g = 0; g < NG; ++g) xrow[g] = 16 * g + c < a.T ? (uint32_t)((16 * g + c) * a.ldx * 2) : kNone;
+  const int piece = 4 * (lane >> 4) + (lane & 3);
 
-  // What is loaded next: the li-th of the wave's pairs of item `lit`.
+  // What is loaded next: the li-th of the wave's chunks of item `lit`.
   int lit = blockIdx.x, li = 0;
-  const uint8_t *cp[2], *sp[2];
-  uint32_t crow = 0, srow = 0;
-  auto locate = [&]() {
-    if (lit >= items) return;
-    const int at = lit / nt;
-    const int64_t e = __builtin_amdgcn_readfirstlane(list[at].expert), o0 = 16 * (int64_t)(lit - at * nt);
-    const uint32_t o = (uint32_t)min((int64_t)c, a.h - 1 - o0);   // (channels past h repeat the last one and are not stored)
-    crow = o * (uint32_t)kh + 16 * q;
-    srow = o * (uint32_t)kb + 2 * q;
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      cp[f] = a.ucodes + (e * 2 * a.h + f * a.h + o0) * kh;
-      sp[f] = a.uscales + (e * 2 * a.h + f * a.h + o0) * kb;
-    }
+  TileAt tile;
+  auto locate = [&](int it) NVQ_INLINE {
+    it = min(it, items - 1);   // (behind the last item its weights are loaded again and not used)
+    const int at = it / nt;
+    const int64_t e = __builtin_amdgcn_readfirstlane(list[at].expert), o0 = 16 * (int64_t)(it - at * nt);
+    tile.set(a.ucodes, a.uscales, e * 2 * a.h + f * a.h + o0, a.h - o0, a.d, lane);
   };
-  auto load_next = [&](Pair<2>& b) {
-    if (lit < items) load_pair<2>(cp, sp, crow, srow, wave + MW * li, q, a.d, b);
+  auto load_next = [&](Chunk& b) NVQ_INLINE {
+    load_chunk<REST>(tile, kp + KP * li, a.d, lane, b);
     if (++li == mine) {
       li = 0;
       lit += gridDim.x;
-      locate();
+      locate(lit);
     }
   };
 
-  f32x4 acc[NG][2];
-  auto clear = [&]() {
+  f32x4 acc[NG][4];
+  auto clear = [&]() NVQ_INLINE {
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int f = 0; f < 2; ++f) acc[g][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < 4; ++i) acc[g][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   };
   int item = blockIdx.x;
-  auto finish = [&]() {   // the item's activations
-    const int at = item / nt;
-    const Entry e = uniform_entry(list[at]);
-    const int o0 = 16 * (item - at * nt);
+  Columns<NG> cur;
+  auto enter = [&](int it, Columns<NG>& cols) NVQ_INLINE {
+    it = min(it, items - 1);
+    cols.set(list[it / nt], scale[it / nt], lane);
+  };
+  u32x4 x[NG][4];
+  auto load_x = [&](const Columns<NG>& of, int ch) NVQ_INLINE {   // zeros where there is no token and from k on
+    const int k0 = ch * kChunk + 32 * piece;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const uint32_t here = (uint32_t)(e.tokens >> (16 * g)) & 0xFFFF;
-      if (!here) continue;   // (the same for all waves)
+      const uint32_t row = of.token[g] >= 0 ? (uint32_t)(of.token[g] * a.ldx * 2) : kNone;
 #pragma unroll
-      for (int f = 0; f < 2; ++f) *(f32x4*)&part[wave][c][16 * f + 4 * q] = acc[g][f];
-      __syncthreads();
-      const int col = tid >> 4, ch = tid & 15;
-      if (tid < 256 && (here >> col & 1) && o0 + ch < a.h) {
-        float gate = 0.0f, up = 0.0f;
-#pragma unroll
-        for (int w = 0; w < MW; ++w) {
-          gate += part[w][col][ch];
-          up += part[w][col][16 + ch];
-        }
-        const int t = 16 * g + col;
-        float w = 0.0f;
-        for (int s = 0; s < a.K; ++s) w += ids[t * a.K + s] == e.expert ? ws[t * a.K + s] : 0.0f;
-        const float scale = a.ug[e.expert];
-        gate *= scale;
-        up *= scale;
-        const float z = expf(-fabsf(gate)), one = 1.0f / (1.0f + z);
-        const float v = gate * (gate >= 0.0f ? one : z * one) * up * w;
-        const __bf16 hi = (__bf16)v;
-        const float rest = v - (float)hi;
-        const __bf16 lo = (__bf16)(fabsf((float)hi) < __builtin_inff() ? rest : 0.0f);   // (an infinity or NaN is in hi alone)
-        const int64_t to = (e.row + before(e.tokens, t)) * a.h + o0 + ch;
-        a.hi[to] = __builtin_bit_cast(uint16_t, hi);
-        a.lo[to] = __builtin_bit_cast(uint16_t, lo);
-      }
-      __syncthreads();
+      for (int j = 0; j < 4; ++j) x[g][j] = load16(xbuf, !REST || k0 + 8 * j < a.d ? row + (uint32_t)(k0 + 8 * j) * 2 : kNone);
     }
   };
-  // One half's products.  One group: its activations were loaded ahead.  More:
-  // the weights are expanded once, then each group that the expert has tokens in.
-  uint64_t tokens = 0;   // of the item's expert (more groups only)
-  auto half = [&](const u32x4 (&w)[2], const uint32_t (&s)[2], const u32x4 (&x)[4], int64_t p, int u) {
-    if constexpr (NG == 1) {
+  auto finish = [&]() NVQ_INLINE {   // the item's activations
+    const int o0 = 16 * (item % nt), n = __popcll(cur.e.tokens);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+    for (int g = 0; g < NG; ++g)
+      if (4 * g < n) part[wave][4 * g + ((lane >> 2) & 3)][4 * (lane >> 4) + (lane & 3)] = whole_sum(acc[g], lane);
+    __syncthreads();
+    for (int i = tid; i < 16 * n; i += 64 * MW) {
+      const int t = i >> 4, ch = i & 15, k = o0 + ch;
+      if (k >= a.h) continue;
+      float gate = 0.0f, up = 0.0f;
 #pragma unroll
-        for (int f = 0; f < 2; ++f) acc[0][f] = mfma(expand(w[f], s[f], j), x[j], acc[0][f]);
-    } else {
-      bf16x8 v[4][2];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) v[j][f] = expand(w[f], s[f], j);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        if (!((tokens >> (16 * g)) & 0xFFFF)) continue;
-        u32x4 y[4];
-        load_half(xbuf, xrow[g], p, u, q, a.d, y);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int f = 0; f < 2; ++f) acc[g][f] = mfma(v[j][f], y[j], acc[g][f]);
+      for (int w = 0; w < MW; w += 2) {
+        gate += part[w][t][ch];
+        up += part[w + 1][t][ch];
       }
+      gate *= cur.scale;
+      up *= cur.scale;
+      const float z = expf(-fabsf(gate)), one = 1.0f / (1.0f + z);
+      const float v = gate * (gate >= 0.0f ? one : z * one) * up * wrow[cur.e.row + t];
+      const __bf16 hi = (__bf16)v;
+      const float rest = v - (float)hi;
+      const __bf16 lo = (__bf16)(fabsf((float)hi) < __builtin_inff() ? rest : 0.0f);   // (an infinity or NaN is in hi alone)
+      uint16_t* to = a.act + (cur.e.row + t) * act_row(a.h) + act_at(k);
+      to[0] = __builtin_bit_cast(uint16_t, hi);
+      to[128] = __builtin_bit_cast(uint16_t, lo);
     }
-  };
-  auto enter = [&]() {
-    clear();
-    if (NG > 1 && item < items) tokens = uniform_entry(list[item / nt]).tokens;
+    __syncthreads();
   };
 
-  enter();
-  if (mine == 0) {   // (k has fewer pairs than there are waves)
-    for (; item < items; item += gridDim.x) finish();
+  clear();
+  enter(item, cur);
+  if (mine == 0) {   // (k has fewer chunks than there are parts)
+    for (; item < items; item += gridDim.x) {
+      enter(item, cur);
+      finish();
+    }
     return;
   }
-  Pair<2> b0, b1;
-  u32x4 xa[4], xb[4];
-  locate();
-  load_next(b0);
-  load_next(b1);
-  if (NG == 1) load_half(xbuf, xrow[0], wave, 0, q, a.d, xa);
+  // Loads return in the order of their issue, so what is needed first, the
+  // activations, goes out ahead of the weights of FD chunks on.
+  Chunk buf[FD];
+  locate(lit);
+#pragma unroll
+  for (int b = 0; b < FD; ++b) {
+    load_next(buf[b]);
+    __builtin_amdgcn_sched_barrier(0);
+    if (b == 0) load_x(cur, kp);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   int i = 0;
-  auto consume = [&](Pair<2>& b) {
-    const int64_t p = wave + MW * i;
-    if (NG == 1) load_half(xbuf, xrow[0], p, 1, q, a.d, xb);
+  auto consume = [&](Chunk& b) NVQ_INLINE {
+    settle<REST>(b, kp + KP * i, a.d, lane);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8 v = expand(b.w[n], b.s[n], j);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) acc[g][n] = mfma(v, x[g][j], acc[g][n]);
+      }
     __builtin_amdgcn_sched_barrier(0);
-    half(b.w[0], b.s[0], xa, p, 0);
-    if (NG == 1) load_half(xbuf, xrow[0], wave + MW * (i + 1 == mine ? 0 : i + 1), 0, q, a.d, xa);
+    const bool last = i + 1 == mine;
+    Columns<NG> next = cur;
+    if (last) enter(item + gridDim.x, next);
+    load_x(next, kp + KP * (last ? 0 : i + 1));
     __builtin_amdgcn_sched_barrier(0);
-    half(b.w[1], b.s[1], xb, p, 1);
     load_next(b);
     __builtin_amdgcn_sched_barrier(0);
-    if (++i == mine) {
+    ++i;
+    if (last) {
       finish();
+      clear();
       i = 0;
       item += gridDim.x;
-      enter();
+      cur = next;
     }
   };
-  while (item < items) {
-    consume(b0);
-    if (item >= items) break;
-    consume(b1);
+  for (;;) {   // (left from the inside: a test of its own would be another path to the first chunk)
+#pragma unroll
+    for (int b = 0; b < FD; ++b) {
+      consume(buf[b]);
+      if (item >= items) return;
+    }
   }
 }
 
-// Kernel 2: 16 output channels per workgroup.  The units (256 k of an expert's
-// activations) of all experts in use lie in a row, which the eight waves share
-// in equal runs; a wave adds its experts' sums times g, and the waves' totals are
-// added in wave order through LDS.  A token that does not use an expert has
-// zeros in its column, and the expert's sum is not added to it (a rejected weight
-// row would make it NaN).
-template <int NG, int OUT_BF16>
-__global__ __launch_bounds__(64 * MW, NG == 1 ? 4 : 2) void moe_down_kernel(const MoeMlp a) {
-  __shared__ __attribute__((aligned(16))) float part[MW][16 * NG][20];
+// Kernel 2: 16 output channels per workgroup.  The units (chunks of an entry's
+// activations) of all entries lie in a row, which the eight waves share in equal
+// runs.  A wave adds its entries' sums times g to totals of its own in LDS,
+// [token][channel]; the waves' totals are added in wave order.  Columns without
+// a token are added nowhere (a rejected weight row makes them NaN).
+template <int OUT_BF16, int NG, bool REST>
+__global__ __launch_bounds__(64 * DW, NG == 1 ? 4 : 2) void moe_down_kernel(const MoeMlp a) {
+  constexpr int FD = DFD;
+  extern __shared__ __attribute__((aligned(16))) char dyn[];
+  float* totals = (float*)dyn;   // [wave][token][16]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int c = lane & 15, q = lane >> 4;
-  const int64_t kh = a.h / 2, kb = a.h / 16, o0 = (int64_t)blockIdx.x * 16;
-  const uint32_t o = (uint32_t)min((int64_t)c, a.m - 1 - o0), crow = o * (uint32_t)kh + 16 * q, srow = o * (uint32_t)kb + 2 * q;
-  const int used = *a.count, per = (int)((a.h + 255) / 256), units = used * per;
-  int at = (int)((int64_t)units * wave / MW);
-  const int end = (int)((int64_t)units * (wave + 1) / MW);
+  const int64_t o0 = (int64_t)blockIdx.x * 16, stride = act_row(a.h);
+  const int used = *a.count, per = (int)((a.h + kChunk - 1) / kChunk), units = used * per;
+  int at = (int)((int64_t)units * wave / DW);
+  const int end = (int)((int64_t)units * (wave + 1) / DW);
+  Entry* list = (Entry*)(totals + DW * a.T * 16);
+  float* scale = (float*)(list + most_entries(a.T, a.E, a.K, 4 * NG));
+  for (int i = tid; i < used; i += 64 * DW) {
+    const Entry e = a.entries[i];
+    list[i] = e;
+    scale[i] = a.dg[e.expert];
+  }
+  for (int i = tid; i < DW * a.T * 16; i += 64 * DW) totals[i] = 0.0f;
+  float* mine = totals + wave * a.T * 16 + 4 * (lane >> 4) + (lane & 3);
+  __syncthreads();
 
-  // Loads run FD units ahead: unit lp of entry la.
-  int la = at / per, lp = at - la * per, lu = at;
-  const uint8_t *cp[1], *sp[1];
-  auto locate = [&]() {
-    if (lu >= end) return;
-    const int64_t e = __builtin_amdgcn_readfirstlane(a.entries[la].expert);
-    cp[0] = a.dcodes + (e * a.m + o0) * kh;
-    sp[0] = a.dscales + (e * a.m + o0) * kb;
-  };
-  auto load_next = [&](Pair<1>& b) {
-    if (lu < end) load_pair<1>(cp, sp, crow, srow, lp, q, a.h, b);
-    ++lu;
-    if (++lp == per) {
-      lp = 0;
-      ++la;
-      locate();
-    }
-  };
-  constexpr int FD = 4;
-  Pair<1> buf[FD];
-  locate();
-#pragma unroll
-  for (int d = 0; d < FD; ++d) load_next(buf[d]);
-
-  f32x4 acc[NG], total[NG];
-#pragma unroll
-  for (int g = 0; g < NG; ++g) acc[g] = total[g] = f32x4{0.f, 0.f, 0.f, 0.f};
-  int ea = at / per, ep = at - ea * per;
-  Entry e;
-  __amdgpu_buffer_rsrc_t hbuf, lbuf;
-  uint32_t arow[NG];
-  auto enter = [&]() {
-    e = uniform_entry(a.entries[ea]);
-    const int64_t first = e.row * a.h;
-    const uint32_t bytes = (uint32_t)(__popcll(e.tokens) * a.h * 2);
-    hbuf = buffer_of(a.hi + first, bytes);
-    lbuf = buffer_of(a.lo + first, bytes);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const int t = 16 * g + c;
-      arow[g] = (e.tokens >> t & 1) ? (uint32_t)(before(e.tokens, t) * a.h * 2) : kNone;
-    }
-  };
-  auto leave = [&]() {
-    const float scale = a.dg[e.expert];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) total[g][r] += arow[g] != kNone ? acc[g][r] * scale : 0.0f;
-      acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-  };
-  auto consume = [&](Pair<1>& b) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      bf16x8 v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = expand(b.w[u][0], b.s[u][0], j);
+  if (at < end) {
+    int ea = at / per, ep = at - ea * per, la = ea, lp = ep;   // unit ep of entry ea; the next to load
+    TileAt tile;
+    auto locate = [&](int entry) NVQ_INLINE {
+      const int64_t e = __builtin_amdgcn_readfirstlane(list[entry].expert);
+      tile.set(a.dcodes, a.dscales, e * a.m + o0, a.m - o0, a.h, lane);
+    };
+    auto load_next = [&](Chunk& b) NVQ_INLINE {
+      load_chunk<REST>(tile, lp, a.h, lane, b);
+      if (++lp == per) {
+        lp = 0;
+        la = min(la + 1, used - 1);   // (behind the last entry its weights are loaded again and not used)
+        locate(la);
+      }
+    };
+    const int piece = 4 * (lane >> 4) + (lane & 3);
+    u32x4 x[NG][4][2];
+    auto load_act = [&](const Columns<NG>& of, int p) NVQ_INLINE {   // zeros where there is no token and from h on
+      const __amdgpu_buffer_rsrc_t rs = buffer_of(a.act + of.e.row * stride, (uint32_t)(__popcll(of.e.tokens) * stride * 2));
+      const int k0 = p * kChunk + 32 * piece;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        if (NG > 1 && !((e.tokens >> (16 * g)) & 0xFFFF)) continue;
-        u32x4 h4[4], l4[4];
-        load_half(hbuf, arow[g], ep, u, q, a.h, h4);
-        load_half(lbuf, arow[g], ep, u, q, a.h, l4);
+        const uint32_t row = of.token[g] >= 0 ? (uint32_t)((4 * g + ((lane >> 2) & 3)) * stride * 2 + p * 2048 + piece * 16) : kNone;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          acc[g] = mfma(v[j], h4[j], acc[g]);
-          acc[g] = mfma(v[j], l4[j], acc[g]);
+          const uint32_t off = !REST || k0 + 8 * j < a.h ? row + j * 512 : kNone;
+          x[g][j][0] = load16(rs, off);
+          x[g][j][1] = load16(rs, off + 256);
         }
       }
-    }
-    load_next(b);
-    ++at;
-    if (++ep == per || at == end) {
-      leave();
-      ep = 0;
-      ++ea;
-      if (at < end) enter();
-    }
-  };
-  if (at < end) {
-    enter();
-    while (true) {
+    };
+    f32x4 acc[NG][4];
+    auto clear = [&]() NVQ_INLINE {
 #pragma unroll
-      for (int d = 0; d < FD; ++d) {
-        consume(buf[d]);
-        if (at >= end) break;
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[g][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    };
+    clear();
+    Columns<NG> cur;
+    cur.set(list[ea], scale[ea], lane);
+    Chunk buf[FD];
+    locate(la);
+    // (in the loop's order, as in the first kernel)
+#pragma unroll
+    for (int b = 0; b < FD; ++b) {
+      load_next(buf[b]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (b == 0) load_act(cur, ep);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    auto consume = [&](Chunk& b) NVQ_INLINE {
+      settle<REST>(b, ep, a.h, lane);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bf16x8 v = expand(b.w[n], b.s[n], j);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            acc[g][n] = mfma(v, x[g][j][0], acc[g][n]);
+            acc[g][n] = mfma(v, x[g][j][1], acc[g][n]);
+          }
+        }
+      __builtin_amdgcn_sched_barrier(0);
+      ++at;
+      const bool cross = ep + 1 == per;
+      Columns<NG> next = cur;
+      if (cross) {
+        ea = min(ea + 1, used - 1);
+        next.set(list[ea], scale[ea], lane);
       }
-      if (at >= end) break;
+      ep = cross ? 0 : ep + 1;
+      load_act(next, ep);
+      __builtin_amdgcn_sched_barrier(0);
+      load_next(b);
+      __builtin_amdgcn_sched_barrier(0);
+      if (cross || at == end) {   // the entry's sums to the tokens' totals
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          if (4 * g >= __popcll(cur.e.tokens)) break;
+          const float v = whole_sum(acc[g], lane);
+          if (cur.token[g] >= 0) mine[cur.token[g] * 16] += v * cur.scale;
+        }
+        clear();
+      }
+      cur = next;
+    };
+    for (;;) {
+#pragma unroll
+      for (int b = 0; b < FD; ++b) {
+        consume(buf[b]);
+        if (at >= end) goto done;
+      }
     }
   }
-#pragma unroll
-  for (int g = 0; g < NG; ++g) *(f32x4*)&part[wave][16 * g + c][4 * q] = total[g];
+done:
   __syncthreads();
-  for (int i = tid; i < 256 * NG; i += 64 * MW) {
+  for (int i = tid; i < a.T * 16; i += 64 * DW) {
     const int t = i >> 4, ch = i & 15;
-    if (t >= a.T || o0 + ch >= a.m) continue;
+    if (o0 + ch >= a.m) continue;
     float v = a.bad[t];
 #pragma unroll
-    for (int w = 0; w < MW; ++w) v += part[w][t][ch];
+    for (int w = 0; w < DW; ++w) v += totals[(w * a.T + t) * 16 + ch];
     if (OUT_BF16) ((__bf16*)a.out)[t * a.ldo + o0 + ch] = (__bf16)v;
     else ((float*)a.out)[t * a.ldo + o0 + ch] = v;
   }
@@ -479,11 +575,45 @@ __global__ __launch_bounds__(64 * MW, NG == 1 ? 4 : 2) void moe_down_kernel(cons
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+// Groups of 4 tokens per entry.  An expert with more tokens than an entry holds
+// has its weights expanded again for the next entry.
+int groups(int64_t T, int64_t E, int64_t K) { return T * K <= 2 * E ? 1 : 4; }
+
+template <int NG>
+hipError_t launch(MoeMlp& a, int logits_bf16, int out_bf16, hipStream_t s) {
+  const int64_t items = most_entries(a.T, a.E, a.K, 4 * NG) * ((a.h + 15) / 16);
+  const size_t lds = up_lds(a.T, a.E, a.K, 4 * NG);
+  const dim3 up((unsigned)std::min<int64_t>(items, 512)), down((unsigned)((a.m + 15) / 16));
+#define NVQ_UP(L, EPL)                                                                                          \
+  do {                                                                                                          \
+    if (a.d % kChunk) hipLaunchKernelGGL((moe_up_kernel<L, EPL, NG, true>), up, dim3(64 * MW), lds, s, a);      \
+    else hipLaunchKernelGGL((moe_up_kernel<L, EPL, NG, false>), up, dim3(64 * MW), lds, s, a);                  \
+  } while (0)
+  if (!a.logits) NVQ_UP(float, 1);
+  else if (logits_bf16 && a.E <= 256) NVQ_UP(uint16_t, 4);
+  else if (logits_bf16) NVQ_UP(uint16_t, 16);
+  else if (a.E <= 256) NVQ_UP(float, 4);
+  else NVQ_UP(float, 16);
+#undef NVQ_UP
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const size_t totals = (size_t)DW * a.T * 16 * sizeof(float) + most_entries(a.T, a.E, a.K, 4 * NG) * (sizeof(Entry) + 4);
+#define NVQ_DOWN(OUT)                                                                                           \
+  do {                                                                                                          \
+    if (a.h % kChunk) hipLaunchKernelGGL((moe_down_kernel<OUT, NG, true>), down, dim3(64 * DW), totals, s, a);  \
+    else hipLaunchKernelGGL((moe_down_kernel<OUT, NG, false>), down, dim3(64 * DW), totals, s, a);              \
+  } while (0)
+  if (out_bf16) NVQ_DOWN(1);
+  else NVQ_DOWN(0);
+#undef NVQ_DOWN
+  return hipGetLastError();
+}
+
 }  // namespace
 
-// Layout: count, the tokens' `bad`, the entries, the two parts of the activations.
+// Layout: count, the tokens' `bad`, the entries, the activations.
 size_t nvfp4_moe_mlp_workspace(int64_t T, int64_t E, int64_t K, int64_t h) {
-  return 256 + 256 + up256(std::min(E, T * K) * sizeof(Entry)) + 2 * up256((size_t)(T * K) * h * 2);
+  return 512 + up256(most_entries(T, E, K, 4) * sizeof(Entry)) + (size_t)(T * K) * act_row(h) * 2;
 }
 
 hipError_t nvfp4_moe_mlp_launch(const uint16_t* X, int64_t T, int64_t d, int64_t ldx, const void* logits, int logits_bf16, int64_t E,
@@ -500,38 +630,13 @@ hipError_t nvfp4_moe_mlp_launch(const uint16_t* X, int64_t T, int64_t d, int64_t
   a.count = (int32_t*)p;
   a.bad = (float*)(p + 256);
   a.entries = (Entry*)(p + 512);
-  p += 512 + up256(std::min(E, T * K) * sizeof(Entry));
-  a.hi = (uint16_t*)p;
-  a.lo = (uint16_t*)(p + up256((size_t)(T * K) * h * 2));
-  const int64_t items = std::min(E, T * K) * ((h + 15) / 16);
-  const dim3 up((unsigned)std::min<int64_t>(items, 512)), down((unsigned)((m + 15) / 16)), block(64 * MW);
-  const size_t lds = up_lds(T, E, K);
-#define NVQ_UP(L, EPL)                                                                      \
-  do {                                                                                      \
-    if (T <= 16) hipLaunchKernelGGL((moe_up_kernel<L, EPL, 1>), up, block, lds, s, a);      \
-    else if (T <= 32) hipLaunchKernelGGL((moe_up_kernel<L, EPL, 2>), up, block, lds, s, a); \
-    else hipLaunchKernelGGL((moe_up_kernel<L, EPL, 4>), up, block, lds, s, a);              \
-  } while (0)
-  if (logits && logits_bf16) {
-    if (E <= 256) NVQ_UP(uint16_t, 4);
-    else NVQ_UP(uint16_t, 16);
-  } else {
-    if (E <= 256) NVQ_UP(float, 4);
-    else NVQ_UP(float, 16);
+  a.act = (uint16_t*)(p + 512 + up256(most_entries(T, E, K, 4) * sizeof(Entry)));
+  if (logits && T > kRoutedTokens) {
+    const hipError_t e = moe_topk_launch(logits, logits_bf16, T, E, ldl, K, renorm, ids, weights, s);
+    if (e != hipSuccess) return e;
+    a.logits = nullptr;
   }
-#undef NVQ_UP
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-#define NVQ_DOWN(NG)                                                                                   \
-  do {                                                                                                 \
-    if (out_bf16) hipLaunchKernelGGL((moe_down_kernel<NG, 1>), down, block, 0, s, a);                  \
-    else hipLaunchKernelGGL((moe_down_kernel<NG, 0>), down, block, 0, s, a);                           \
-  } while (0)
-  if (T <= 16) NVQ_DOWN(1);
-  else if (T <= 32) NVQ_DOWN(2);
-  else NVQ_DOWN(4);
-#undef NVQ_DOWN
-  return hipGetLastError();
+  return groups(T, E, K) == 1 ? launch<1>(a, logits_bf16, out_bf16, s) : launch<4>(a, logits_bf16, out_bf16, s);
 }
 
 }  // namespace nvq

@@ -80,7 +80,7 @@ def _inputs(rng, T, d, E, gap=0):
     return X, torch.from_numpy((rng.standard_normal((T, E)) * 2).astype(np.float32)).to(DEV)
 
 
-SIZES = [(1, 1, 1, 16, 16, 1), (1, 8, 2, 256, 256, 64), (1, 64, 8, 512, 128, 96), (2, 3, 3, 48, 80, 17), (5, 16, 4, 272, 304, 33),
+SIZES = [(1, 1, 1, 32, 48, 1), (1, 2, 1, 48, 32, 3), (3, 4, 2, 512, 1024, 20), (2, 8, 8, 4112, 1040, 33), (64, 4, 2, 528, 496, 18), (20, 64, 4, 4096, 512, 48), (1, 8, 2, 256, 256, 64), (1, 64, 8, 512, 128, 96), (2, 3, 3, 48, 80, 17), (5, 16, 4, 272, 304, 33),
          (15, 8, 2, 2064, 48, 16), (16, 32, 6, 256, 272, 40), (17, 8, 1, 528, 64, 100), (31, 60, 8, 128, 160, 31), (33, 1, 1, 256, 512, 48),
          (48, 24, 3, 80, 32, 257), (63, 200, 5, 64, 48, 20), (64, 16, 8, 288, 544, 64)]
 
@@ -108,7 +108,7 @@ def test_routed(nvq, T, E, K, d, h, m, renorm, dtype):
 @pytest.mark.parametrize("T,E,K", [(2, 300, 40), (40, 1024, 64), (64, 1000, 20)])
 def test_many_experts(nvq, T, E, K):
     rng = np.random.default_rng([T, E])
-    gu, dn, wgu, wdn = _layer(rng, E, 32, 16, 24)
+    gu, dn, wgu, wdn = _layer(rng, E, 32, 32, 24)
     X, logits = _inputs(rng, T, 32, E)
     out, ids, w = nvq.nvfp4_moe_mlp(X, gu, dn, logits=logits, top_k=K, out_dtype=torch.float32)
     rid, _ = moe.topk(_np(logits), K, True)
@@ -198,9 +198,9 @@ def test_non_finite_values_stay_with_their_tokens(nvq, T):
 
 def test_infinite_activation_stays_infinite(nvq):
     """A gate and an up value whose product passes fp32's range: infinities, no NaN out of the split into two parts."""
-    d = h = 16
+    d = h = 32
     one = torch.full((1, 2 * h, d // 2), 0x22, dtype=torch.uint8, device=DEV)        # all weights 1
-    sc = torch.full((1, 2 * h, 1), 0x38, dtype=torch.uint8, device=DEV)
+    sc = torch.full((1, 2 * h, 2), 0x38, dtype=torch.uint8, device=DEV)
     g = torch.ones(1, device=DEV)
     X = torch.full((1, d), 3e30, dtype=torch.bfloat16, device=DEV)
     out, _, _ = nvq.nvfp4_moe_mlp(X, (one, sc, g), (one[:, :h].contiguous(), sc[:, :h].contiguous(), g), logits=torch.zeros(1, 1, device=DEV),

@@ -118,14 +118,14 @@ def test_python_refuses_host_tensors_and_types(nvq):
 
 
 def test_moe_mlp(nvq):
-    def f(X=fake, xd=1, T=4, d=32, ldx=32, logits=fake, ld=0, E=8, ldl=8, K=2, ids=fake, w=fake, uc=fake, us=fake, ug=fake, h=16, dc=fake,
+    def f(X=fake, xd=1, T=4, d=64, ldx=64, logits=fake, ld=0, E=8, ldl=8, K=2, ids=fake, w=fake, uc=fake, us=fake, ug=fake, h=32, dc=fake,
           ds=fake, dg=fake, m=24, out=other, od=1, ldo=24, ws=P(1 << 20), wb=1 << 20):
         return nvq.lib.nvfp4_moe_mlp(X, xd, T, d, ldx, logits, ld, E, ldl, K, 1, ids, w, uc, us, ug, h, dc, ds, dg, m, out, od, ldo, ws, wb,
                                      None)
 
     assert f(xd=0) == DTYPE and f(ld=2) == DTYPE and f(od=2) == DTYPE
-    for bad in (dict(T=-1), dict(T=65), dict(d=24), dict(d=0), dict(ldx=16), dict(ldx=36), dict(E=0), dict(E=1025, ldl=1025), dict(ldl=7),
-                dict(h=0), dict(h=24), dict(m=0), dict(ldo=23), dict(T=64, ldx=1 << 25), dict(d=4000016, ldx=4000016), dict(h=4000016),
+    for bad in (dict(T=-1), dict(T=65), dict(d=40), dict(d=16, ldx=16), dict(d=0), dict(ldx=48), dict(ldx=68), dict(E=0), dict(E=1025, ldl=1025), dict(ldl=7),
+                dict(h=0), dict(h=16), dict(h=40), dict(m=0), dict(ldo=23), dict(T=64, ldx=1 << 25), dict(d=4000016, ldx=4000016), dict(h=4000016),
                 dict(m=4000001, ldo=4000001)):
         assert f(**bad) == SHAPE, bad
     for bad in (dict(K=0), dict(K=-1), dict(K=9), dict(K=65, E=1024, ldl=1024), dict(K=65, logits=None), dict(K=1 << 40)):
@@ -135,9 +135,9 @@ def test_moe_mlp(nvq):
     assert f(X=P(4104)) == ALIGN and f(uc=P(4100)) == ALIGN and f(dc=P(4100)) == ALIGN and f(ids=P(4098)) == ALIGN
     assert f(logits=P(4098)) == ALIGN and f(out=P(4097)) == ALIGN
     assert f(out=fake) == VALUE
-    need = nvq.lib.nvfp4_moe_mlp_workspace_size(4, 8, 2, 16)
+    need = nvq.lib.nvfp4_moe_mlp_workspace_size(4, 8, 2, 32)
     assert need > 0 and need % 256 == 0
-    for bad in ((0, 8, 2, 16), (65, 8, 2, 16), (4, 0, 2, 16), (4, 8, 0, 16), (4, 8, 65, 16), (4, 8, 2, 24)):
+    for bad in ((0, 8, 2, 32), (65, 8, 2, 32), (4, 0, 2, 32), (4, 8, 0, 32), (4, 8, 65, 32), (4, 8, 2, 16), (4, 8, 2, 40)):
         assert nvq.lib.nvfp4_moe_mlp_workspace_size(*bad) == 0, bad
     assert f(ws=None) == WORKSPACE and f(wb=need - 1) == WORKSPACE and f(ws=P((1 << 20) + 8)) == WORKSPACE
     assert f(T=0, X=None, ids=None, w=None, uc=None, us=None, ug=None, dc=None, ds=None, dg=None, out=None, ws=None, wb=0) == 0
