@@ -39,13 +39,10 @@ namespace {
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint16_t u16_any __attribute__((aligned(1)));
 
-constexpr int MW = 8, DW = 8;     // waves per workgroup of the two kernels
+constexpr int MW = 8;              // waves per workgroup of the first kernel
+constexpr int down_waves(int NG) { return NG == 1 ? 16 : 8; }   // of the second (groups of 4 tokens need registers)
 constexpr int kRoutedTokens = 8;   // up to this many are routed by the first kernel, one per wave
 constexpr int kChunk = 512;
-#ifndef UFD
-#define UFD 2
-#define DFD 2
-#endif
 constexpr uint32_t kNone = 0x80000000u;   // an offset past every buffer (checked on the host), also with k's offsets added
 
 // An expert and some of its tokens (bits), which are rows `row`, `row` + 1, .. of the activations in rising order.
@@ -218,8 +215,8 @@ size_t up_lds(int64_t T, int64_t E, int64_t K, int per) { return E * 8 + T * K *
 // the even waves take gate, the odd ones up, each four a part of k, their
 // sums added in wave order through LDS.  Weights are loaded FD chunks ahead.
 template <typename L, int EPL, int NG, bool REST>
-__global__ __launch_bounds__(64 * MW, NG == 1 ? 4 : 2) void moe_up_kernel(const MoeMlp a) {
-  constexpr int KP = MW / 2, FD = UFD;
+__global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(const MoeMlp a) {
+  constexpr int KP = MW / 2, FD = NG == 1 ? 2 : 1;
   __shared__ __attribute__((aligned(16))) float part[MW][4 * NG][16];
   __shared__ int s_count;
   extern __shared__ __attribute__((aligned(16))) char dyn[];
@@ -429,23 +426,25 @@ __global__ __launch_bounds__(64 * MW, NG == 1 ? 4 : 2) void moe_up_kernel(const 
       cur = next;
     }
   };
-  for (;;) {   // (left from the inside: a test of its own would be another path to the first chunk)
+  // (no way out from between the chunks, which would be another path to the first)
+  int left = (items - 1 - (int)blockIdx.x) / (int)gridDim.x * mine + mine;
+  for (; left >= FD; left -= FD) {
 #pragma unroll
-    for (int b = 0; b < FD; ++b) {
-      consume(buf[b]);
-      if (item >= items) return;
-    }
+    for (int b = 0; b < FD; ++b) consume(buf[b]);
   }
+#pragma unroll
+  for (int b = 0; b < FD - 1; ++b)
+    if (b < left) consume(buf[b]);
 }
 
 // Kernel 2: 16 output channels per workgroup.  The units (chunks of an entry's
-// activations) of all entries lie in a row, which the eight waves share in equal
+// activations) of all entries lie in a row, which the waves share in equal
 // runs.  A wave adds its entries' sums times g to totals of its own in LDS,
 // [token][channel]; the waves' totals are added in wave order.  Columns without
 // a token are added nowhere (a rejected weight row makes them NaN).
 template <int OUT_BF16, int NG, bool REST>
-__global__ __launch_bounds__(64 * DW, NG == 1 ? 4 : 2) void moe_down_kernel(const MoeMlp a) {
-  constexpr int FD = DFD;
+__global__ __launch_bounds__(64 * down_waves(NG), NG == 1 ? 4 : 3) void moe_down_kernel(const MoeMlp a) {
+  constexpr int DW = down_waves(NG), FD = 1;
   extern __shared__ __attribute__((aligned(16))) char dyn[];
   float* totals = (float*)dyn;   // [wave][token][16]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -552,15 +551,15 @@ __global__ __launch_bounds__(64 * DW, NG == 1 ? 4 : 2) void moe_down_kernel(cons
       }
       cur = next;
     };
-    for (;;) {
+    int left = end - at;
+    for (; left >= FD; left -= FD) {
 #pragma unroll
-      for (int b = 0; b < FD; ++b) {
-        consume(buf[b]);
-        if (at >= end) goto done;
-      }
+      for (int b = 0; b < FD; ++b) consume(buf[b]);
     }
+#pragma unroll
+    for (int b = 0; b < FD - 1; ++b)
+      if (b < left) consume(buf[b]);
   }
-done:
   __syncthreads();
   for (int i = tid; i < a.T * 16; i += 64 * DW) {
     const int t = i >> 4, ch = i & 15;
@@ -576,8 +575,12 @@ done:
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Groups of 4 tokens per entry.  An expert with more tokens than an entry holds
-// has its weights expanded again for the next entry.
-int groups(int64_t T, int64_t E, int64_t K) { return T * K <= 2 * E ? 1 : 4; }
+// has its weights read (from the caches) and expanded again for the next one; two
+// groups take twice the matrix instructions and registers.  us with one / two / four,
+// tokens per expert on average: 37 tokens x 8 of 256 experts (1.2) 203 / 222 / 288,
+// 32 x 6 of 64 (3) 117 / 123 / 166, 16 x 2 of 8 (4) 82 / 81 / 103, 64 x 2 of 8 (16)
+// 187 / 152 / 155.
+int groups(int64_t T, int64_t E, int64_t K) { return T * K < 4 * E ? 1 : 2; }
 
 template <int NG>
 hipError_t launch(MoeMlp& a, int logits_bf16, int out_bf16, hipStream_t s) {
@@ -597,6 +600,7 @@ hipError_t launch(MoeMlp& a, int logits_bf16, int out_bf16, hipStream_t s) {
 #undef NVQ_UP
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  constexpr int DW = down_waves(NG);
   const size_t totals = (size_t)DW * a.T * 16 * sizeof(float) + most_entries(a.T, a.E, a.K, 4 * NG) * (sizeof(Entry) + 4);
 #define NVQ_DOWN(OUT)                                                                                           \
   do {                                                                                                          \
@@ -636,7 +640,7 @@ hipError_t nvfp4_moe_mlp_launch(const uint16_t* X, int64_t T, int64_t d, int64_t
     if (e != hipSuccess) return e;
     a.logits = nullptr;
   }
-  return groups(T, E, K) == 1 ? launch<1>(a, logits_bf16, out_bf16, s) : launch<4>(a, logits_bf16, out_bf16, s);
+  return groups(T, E, K) == 1 ? launch<1>(a, logits_bf16, out_bf16, s) : launch<2>(a, logits_bf16, out_bf16, s);
 }
 
 }  // namespace nvq
