@@ -943,7 +943,7 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, int
 
 size_t mxfp4_gemm_workspace_size(int x_dtype, int64_t n, int64_t k, int64_t m) {
   if (n <= 0 || k <= 0 || m <= 0 || (!dtype_ok(x_dtype) && x_dtype != NVQ_DTYPE_MXFP4)) return 0;
-  return align_up(mxfp4_gemm_workspace(x_dtype == NVQ_DTYPE_MXFP4, n, k, m));
+  return align_up(mxfp4_gemm_workspace(x_dtype == NVQ_DTYPE_MXFP4, x_dtype == NVQ_DTYPE_BF16, n, k, m));
 }
 
 int mxfp4_gemm(const void* X, int x_dtype, const uint8_t* x_scales, int64_t n, int64_t k, int64_t ldx, const uint8_t* codes,
@@ -963,7 +963,7 @@ int mxfp4_gemm(const void* X, int x_dtype, const uint8_t* x_scales, int64_t n, i
   if (!aligned(X, packed ? 16 : elem_size(x_dtype)) || !aligned(Y, elem_size(y_dtype)))
     return failp(NVQ_ERR_ALIGN, fn, "X and Y must be aligned by their elements, MXFP4 codes 16-byte");
   if (Y == X) return failp(NVQ_ERR_VALUE, fn, "Y may not be X");
-  const size_t need = mxfp4_gemm_workspace(packed, n, k, m);
+  const size_t need = mxfp4_gemm_workspace(packed, x_dtype == NVQ_DTYPE_BF16, n, k, m);
   if (need && (!ws || ws_bytes < need || !aligned(ws, kAlign)))
     return failp(NVQ_ERR_WORKSPACE, fn, "workspace needs %zu bytes (256-aligned), got %zu", need, ws_bytes);
   return tiles_status(mxfp4_gemm_launch(X, packed, x_dtype == NVQ_DTYPE_BF16, x_scales, n, k, ldx, codes, scales, m, Y,

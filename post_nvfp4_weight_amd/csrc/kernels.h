@@ -220,7 +220,7 @@ hipError_t mxfp4_quantize_launch(const void* X, int bf16, int64_t n, int64_t k, 
 hipError_t mxfp4_dequantize_launch(const uint8_t* codes, const uint8_t* scales, int64_t n, int64_t k, void* out, int out_bf16,
                                    hipStream_t s);
 // x_codes: X is MXFP4 with xscales, else bf16 or fp32 that the call quantizes, into ws where mxfp4_gemm_workspace says so.
-size_t mxfp4_gemm_workspace(int x_codes, int64_t n, int64_t k, int64_t m);
+size_t mxfp4_gemm_workspace(int x_codes, int x_bf16, int64_t n, int64_t k, int64_t m);
 hipError_t mxfp4_gemm_launch(const void* X, int x_codes, int x_bf16, const uint8_t* xscales, int64_t n, int64_t k, int64_t ldx,
                              const uint8_t* codes, const uint8_t* scales, int64_t m, void* Y, int out_bf16, int64_t ldy,
                              void* ws, hipStream_t s);

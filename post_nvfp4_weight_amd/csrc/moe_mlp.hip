@@ -8,25 +8,16 @@
 // significant bits as long as it is above 2^-110): as one bf16 it would be the one value
 // that the layer rounds to 8 bits before its end, for a product that waits for weights anyway.
 //
-// What bounds it is reading the weights of the experts in use once, and on the
-// way there the address unit: a load instruction takes it a cycle for each 64
-// bytes that four neighbouring lanes touch in one line, four where they touch four rows, as
-// the matrix instructions' operands ask for (lane l holds row l % 16).  So the
-// lanes are dealt otherwise.  v_mfma_f32_16x16x32_bf16, lane l = 16 q + 4 a + b:
-//   A, load i of a chunk of 512 k:  channel 4 a + i, piece 4 q + b (32 k, 16 bytes), so
-//      that four neighbours read 64 consecutive bytes; row 4 a + b of the product is
-//      channel 4 a + i over the pieces b, 4 + b, 8 + b, 12 + b alone;
-//   B: column 4 t + b is token t over the same pieces.
-// The result at row 4 a + b, column 4 t + b is channel 4 a + i, token t over those
-// pieces, and the sum over b is the whole (entries with another b are
-// not used).  A product thus takes 4 tokens, not 16, which costs nothing: the matrix
-// cores are idle for most of the time.  37 tokens x 8 of 256 experts (2048 x 4096
-// and 4096 x 1024): 172 and 134 us for the two kernels with lanes by rows.
+// What bounds it is reading the weights of the experts in use once, and the
+// instructions that expand them.  The lanes are dealt as quads.h says (with
+// lanes by rows the two kernels took 172 and 134 us for 37 tokens x 8 of 256
+// experts, 2048 x 4096 and 4096 x 1024, where the loads alone took 162 and 123).
 #include <algorithm>
 
 #include "common.h"
 #include "dequant.h"
 #include "kernels.h"
+#include "quads.h"
 #include "router.h"
 
 namespace nvq {
@@ -188,22 +179,6 @@ struct Columns {
   }
 };
 
-// The sums of 16 channels and 4 tokens out of the four loads' products: the lane
-// gets channel 4 q + b and its column's token, q = l / 16, b = l % 4.
-__device__ __forceinline__ float whole_sum(const f32x4 (&acc)[4], int lane) {
-  const int b = lane & 3;
-  float r = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // (register b of lane 16 q + 4 t + b: row 4 q + b, column 4 t + b)
-    float v = b == 0 ? acc[i][0] : b == 1 ? acc[i][1] : b == 2 ? acc[i][2] : acc[i][3];
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false));   // lanes 1, 0, 3, 2
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false));   // lanes 2, 3, 0, 1
-    r = b == i ? v : r;
-  }
-  return r;
-}
-
 __host__ __device__ __forceinline__ int64_t most_entries(int64_t T, int64_t E, int64_t K, int per) {
   return (E < T * K ? E : T * K) + T * K / per;
 }
@@ -353,7 +328,7 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(const MoeMlp a) {
     const int o0 = 16 * (item % nt), n = __popcll(cur.e.tokens);
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-      if (4 * g < n) part[wave][4 * g + ((lane >> 2) & 3)][4 * (lane >> 4) + (lane & 3)] = whole_sum(acc[g], lane);
+      if (4 * g < n) part[wave][4 * g + ((lane >> 2) & 3)][4 * (lane >> 4) + (lane & 3)] = quad_sum(acc[g], lane);
     __syncthreads();
     for (int i = tid; i < 16 * n; i += 64 * MW) {
       const int t = i >> 4, ch = i & 15, k = o0 + ch;
@@ -544,7 +519,7 @@ __global__ __launch_bounds__(64 * down_waves(NG), NG == 1 ? 4 : 3) void moe_down
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           if (4 * g >= __popcll(cur.e.tokens)) break;
-          const float v = whole_sum(acc[g], lane);
+          const float v = quad_sum(acc[g], lane);
           if (cur.token[g] >= 0) mine[cur.token[g] * 16] += v * cur.scale;
         }
         clear();

@@ -10,6 +10,7 @@
 
 #include "common.h"
 #include "kernels.h"
+#include "quads.h"
 
 namespace nvq {
 
@@ -151,145 +152,141 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __res
 
 __device__ __forceinline__ i32x8 fragment(u32x4 v) { return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0}; }
 
-// A lane's 32 values of one block, to codes and scale byte; the bits of mx_quantize_kernel.
+// A lane's block of 32 of a row, as loaded, and as codes under a scale byte: with
+// the bits of mx_quantize_kernel, or as they are (T = uint8_t: codes).
 template <typename T>
-__device__ __forceinline__ void quantize_block(const T* __restrict__ p, u32x4& w, uint32_t& byte) {
+struct Block {
   Eight<T> x[4];
+  __device__ __forceinline__ void load(const T* row, const uint8_t*, int64_t block) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) x[j].load(p + 8 * j);
-  byte = scale_byte(max(max(x[0].top_exponent(), x[1].top_exponent()), max(x[2].top_exponent(), x[3].top_exponent())));
-  const float s = scale_operand(byte);
+    for (int j = 0; j < 4; ++j) x[j].load(row + 32 * block + 8 * j);
+  }
+  __device__ __forceinline__ void quantize(u32x4& w, uint32_t& byte) const {
+    byte = scale_byte(max(max(x[0].top_exponent(), x[1].top_exponent()), max(x[2].top_exponent(), x[3].top_exponent())));
+    const float s = scale_operand(byte);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = byte == 255 ? 0u : x[j].codes(s);
-}
+    for (int j = 0; j < 4; ++j) w[j] = byte == 255 ? 0u : x[j].codes(s);
+  }
+};
+template <>
+struct Block<uint8_t> {
+  u32x4 w;
+  uint8_t s;
+  __device__ __forceinline__ void load(const uint8_t* row, const uint8_t* scales, int64_t block) {
+    w = *(const u32x4*)(row + 16 * block);
+    s = scales[block];
+  }
+  __device__ __forceinline__ void quantize(u32x4& v, uint32_t& byte) const {
+    v = w;
+    byte = s;
+  }
+};
 
-// Few rows: 16 CG output channels per workgroup, the eight waves each a part
-// of k, all rows in NG groups of 16.
-//   v_mfma_scale_f32_16x16x128_f8f6f4, A = 16 channels, B = 16 rows: lane
-//   (c = l % 16, q = l / 16) holds block q of a step of 128 k, of channel c and of row c.
-// A wave takes chunks of 512 k (four steps: a channel's 16 scale bytes in one
-// load) in turn with the other waves.  Rows that are not quantized yet are
-// quantized by the lane that multiplies them: its fragment is one block.  The
-// waves' partial sums are added in wave order through LDS.
+// Few rows: 16 output channels per workgroup, the eight waves each a part of k,
+// all rows in NG groups of 4.
+//   v_mfma_scale_f32_16x16x128_f8f6f4: a lane's operand is 32 codes under one
+//   scale byte, which is one piece of quads.h, and one block.
+// A wave takes chunks of 512 k in turn with the other waves.  Rows that are not
+// quantized yet are quantized by the lane that multiplies them.  The waves'
+// partial sums are added in wave order through LDS.
+// Pieces past k: the rows' are zero codes under scale 1, the channels' are read
+// at their row's start (a NaN there makes the channel NaN, as it does in its place).
 constexpr int FW = 8;
 
 // XT: uint8_t (codes, with scales), uint16_t (bf16) or float.
-template <typename XT, int NG, int CG, int OUT_BF16>
-__global__ __launch_bounds__(64 * FW) void mx_few_kernel(const XT* __restrict__ X, const uint8_t* __restrict__ xscales,
-                                                         int64_t n, int64_t k, int64_t ldx,
-                                                         const uint8_t* __restrict__ codes,
-                                                         const uint8_t* __restrict__ scales, int64_t m,
-                                                         void* __restrict__ Y, int64_t ldy) {
+template <typename XT, int NG, int OUT_BF16>
+__global__ __launch_bounds__(64 * FW, NG == 1 && sizeof(XT) < 4 ? 4 : 2) void mx_few_kernel(const XT* __restrict__ X, const uint8_t* __restrict__ xscales,
+                                                            int64_t n, int64_t k, int64_t ldx,
+                                                            const uint8_t* __restrict__ codes,
+                                                            const uint8_t* __restrict__ scales, int64_t m,
+                                                            void* __restrict__ Y, int64_t ldy) {
   constexpr bool kCodes = sizeof(XT) == 1;
-  __shared__ __attribute__((aligned(16))) float part[FW][16 * NG][16 * CG + 4];
+  __shared__ float part[FW][4 * NG][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int c = lane & 15, q = lane >> 4;
-  const int64_t kb = k / 32, o0 = (int64_t)blockIdx.x * (16 * CG);
-  const uint8_t *wc[CG], *wsc[CG];
+  const int piece = quad_piece(lane), col = quad_column(lane);
+  const int64_t kb = k / 32, o0 = (int64_t)blockIdx.x * 16;
+  codes += o0 * (k / 2);
+  scales += o0 * kb;
+  uint32_t row[4], srow[4];   // the lane's channels' first code and scale (channels past m repeat the last one and are not stored)
 #pragma unroll
-  for (int f = 0; f < CG; ++f) {
-    const int64_t o = min(o0 + 16 * f + c, m - 1);   // (channels past m repeat the last one and are not stored)
-    wc[f] = codes + o * (k / 2) + 16 * q;
-    wsc[f] = scales + o * kb;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t o = (uint32_t)min((int64_t)(4 * col + i), m - 1 - o0);
+    row[i] = o * (uint32_t)(k / 2);
+    srow[i] = o * (uint32_t)kb;
   }
   const XT* xr[NG];
   const uint8_t* xs[NG];
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    const int64_t t = min((int64_t)(16 * g + c), n - 1);
-    xr[g] = X + (kCodes ? t * (k / 2) + 16 * q : t * ldx + 32 * q);
+    const int64_t t = min((int64_t)(4 * g + col), n - 1);   // (likewise)
+    xr[g] = X + (kCodes ? t * (k / 2) : t * ldx);
     xs[g] = kCodes ? xscales + t * kb : nullptr;
   }
-  f32x4 acc[NG][CG];
+  const int chunks = (int)((kb + 15) / 16), mine = chunks > wave ? (chunks - wave + FW - 1) / FW : 0;
+
+  struct Chunk {
+    u32x4 w[4];
+    uint8_t s[4];
+  };
+  // (the same loads on every path, behind the last chunk the last one's)
+  auto load_chunk = [&](int i, Chunk& x) __attribute__((always_inline)) {
+    const int block = 16 * (wave + FW * min(i, mine - 1)) + piece;
+    const uint32_t at = block < kb ? block : 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      x.w[c] = *(const u32x4*)(codes + (row[c] + 16 * at));
+      x.s[c] = scales[srow[c] + at];
+    }
+  };
+  f32x4 acc[NG][4];
 #pragma unroll
   for (int g = 0; g < NG; ++g)
 #pragma unroll
-    for (int f = 0; f < CG; ++f) acc[g][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  struct Chunk {
-    u32x4 w[CG][4], s[CG];
+    for (int c = 0; c < 4; ++c) acc[g][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  Block<XT> x[NG];
+  auto load_x = [&](int i) __attribute__((always_inline)) {
+    const int block = 16 * (wave + FW * min(i, mine - 1)) + piece, at = block < kb ? block : 0;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) x[g].load(xr[g], xs[g], at);
   };
-  auto load_chunk = [&](int64_t ch, Chunk& x) {
-#pragma unroll
-    for (int f = 0; f < CG; ++f) {
-      x.s[f] = *(const u32x4_any*)(wsc[f] + 16 * ch);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x.w[f][j] = *(const u32x4*)(wc[f] + 256 * ch + 64 * j);
-    }
-  };
-  auto step = [&](const u32x4 (&w)[CG], const uint32_t (&s)[CG], int g, u32x4 xv, uint32_t xsc) {
-#pragma unroll
-    for (int f = 0; f < CG; ++f)
-      acc[g][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fragment(w[f]), fragment(xv), acc[g][f], 4, 4, 0, (int)s[f], 0, (int)xsc);
-  };
-  const int64_t whole = k / 512;
-  Chunk next;
-  if (wave < whole) load_chunk(wave, next);
-  for (int64_t ch = wave; ch < whole; ch += FW) {
-    const Chunk cur = next;
-    if (ch + FW < whole) load_chunk(ch + FW, next);
-    u32x4 xsv[NG];
-    if (kCodes)
-#pragma unroll
-      for (int g = 0; g < NG; ++g) xsv[g] = *(const u32x4_any*)(xs[g] + 16 * ch);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u32x4 w[CG];
-      uint32_t s[CG];
-#pragma unroll
-      for (int f = 0; f < CG; ++f) {
-        w[f] = cur.w[f][j];
-        s[f] = cur.s[f][j] >> (8 * q);
-      }
+  if (mine > 0) {
+    // Loads return in the order of their issue: a chunk's activations go out
+    // ahead of the next chunk's weights.
+    Chunk buf[2];
+    load_chunk(0, buf[0]);
+    auto consume = [&](int i, const Chunk& w, Chunk& next) __attribute__((always_inline)) {
+      load_x(i);
+      __builtin_amdgcn_sched_barrier(0);
+      load_chunk(i + 1, next);
+      __builtin_amdgcn_sched_barrier(0);
+      const bool in = 16 * (wave + FW * i) + piece < kb;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         u32x4 xv;
         uint32_t xb;
-        if constexpr (kCodes) {
-          xv = *(const u32x4*)(xr[g] + 256 * ch + 64 * j);
-          xb = xsv[g][j] >> (8 * q);
-        } else {
-          quantize_block(xr[g] + 512 * ch + 128 * j, xv, xb);
-        }
-        step(w, s, g, xv, xb);
+        x[g].quantize(xv, xb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) xv[e] = in ? xv[e] : 0u;
+        xb = in ? xb : 127u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          acc[g][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fragment(w.w[c]), fragment(xv), acc[g][c], 4, 4, 0, (int)w.s[c], 0,
+                                                                       (int)xb);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    int i = 0;
+    for (; i + 2 <= mine; i += 2) {
+      consume(i, buf[0], buf[1]);
+      consume(i + 1, buf[1], buf[0]);
     }
+    if (i < mine) consume(i, buf[0], buf[1]);
   }
-  // The rest of k, less than a chunk: blocks past k as zero codes under scale 1.
-  if (wave == whole % FW) {
-    for (int64_t b0 = 16 * whole; b0 < kb; b0 += 4) {
-      const bool in = b0 + q < kb;
-      u32x4 w[CG];
-      uint32_t s[CG];
 #pragma unroll
-      for (int f = 0; f < CG; ++f) {
-        w[f] = in ? *(const u32x4*)(wc[f] + 16 * b0) : u32x4{0u, 0u, 0u, 0u};
-        s[f] = in ? wsc[f][b0 + q] : 127u;
-      }
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        u32x4 xv{0u, 0u, 0u, 0u};
-        uint32_t xb = 127;
-        if (in) {
-          if constexpr (kCodes) {
-            xv = *(const u32x4*)(xr[g] + 16 * b0);
-            xb = xs[g][b0 + q];
-          } else {
-            quantize_block(xr[g] + 32 * b0, xv, xb);
-          }
-        }
-        step(w, s, g, xv, xb);
-      }
-    }
-  }
-  // Accumulator register r of lane l: channel 4 q + r, row c.
-#pragma unroll
-  for (int g = 0; g < NG; ++g)
-#pragma unroll
-    for (int f = 0; f < CG; ++f) *(f32x4*)&part[wave][16 * g + c][16 * f + 4 * q] = acc[g][f];
+  for (int g = 0; g < NG; ++g) part[wave][4 * g + col][4 * (lane >> 4) + (lane & 3)] = quad_sum(acc[g], lane);
   __syncthreads();
-  for (int i = tid; i < 256 * NG * CG; i += 64 * FW) {
-    const int r = i / (16 * CG), o = i % (16 * CG);
+  for (int i = tid; i < 64 * NG; i += 64 * FW) {
+    const int r = i >> 4, o = i & 15;
     if (r >= n || o0 + o >= m) continue;
     float v = 0.0f;
 #pragma unroll
@@ -300,8 +297,8 @@ __global__ __launch_bounds__(64 * FW) void mx_few_kernel(const XT* __restrict__ 
   }
 }
 
-// Many rows: tiles of 32 FA WM output channels x 32 FB WN rows per workgroup of
-// WM x WN waves, each 32 FA channels x 32 FB rows.
+// Tiles of 32 FA WM output channels x 32 FB WN rows per workgroup of WM x WN
+// waves, each 32 FA channels x 32 FB rows.
 //   v_mfma_scale_f32_32x32x64_f8f6f4, A = 32 channels, B = 32 rows: lane
 //   (r = l % 32, h = l / 32) holds one block of channel r and of row r.
 //   k goes in stages of 256, four products deep: a row's 128 bytes of codes
@@ -309,23 +306,41 @@ __global__ __launch_bounds__(64 * FW) void mx_few_kernel(const XT* __restrict__ 
 //   h = 1 (the order of k in the sum is free, as long as both operands agree),
 //   so that the lane's four scale bytes are one word whose byte s the
 //   instruction selects.
-//   Codes are copied to LDS directly, one stage ahead, 16-byte pieces swizzled
-//   by (row / 2) % 8: the 16 rows that are read at once then touch all 64
-//   banks.  Scales go through registers (they may start at any byte).
-template <int WM, int WN, int FA, int FB>
+//   Codes are copied to LDS directly, R - 1 stages ahead into a ring of R, 16-byte
+//   pieces swizzled by (row / 2) % 8: the 16 rows that are read at once then touch
+//   all 64 banks.  Scales (which may start at any byte) go through registers, for
+//   GS stages at a time, one such group ahead.
+template <int WM, int WN, int FA, int FB, int R, int GS>
 struct MxTile {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kM = 32 * FA * WM, kN = 32 * FB * WN, kAll = kM + kN;
-  static constexpr int kWLoads = kM / 8 / kWaves, kXLoads = kN / 8 / kWaves;
-  static constexpr int kWBuf = kM * 128, kXBuf = kN * 128, kSBuf = kAll * 8;
-  static constexpr int kLds = 2 * (kWBuf + kXBuf + kSBuf);
-  static constexpr int kSPer = (kAll + kThreads - 1) / kThreads;   // rows of scales per thread
-  static_assert(kM % (8 * kWaves) == 0 && kN % (8 * kWaves) == 0, "whole copies per wave");
+  static constexpr int kWLoads = kM / 8 / kWaves, kXLoads = kN / 8 / kWaves, kLoads = kWLoads + kXLoads;
+  static constexpr int kBuf = kAll * 128, kSBuf = kAll * 8;   // codes and scales of a stage; the channels' first
+  static constexpr int kLds = R * kBuf + 2 * GS * kSBuf;
+  static_assert(kM % (8 * kWaves) == 0 && kN % (8 * kWaves) == 0 && kWaves % 2 == 0, "whole copies per wave");
+  static_assert(kAll <= kThreads && (GS == 2 || GS == 4), "a thread per row of scales");
 };
 
+// The workgroup's tile of TM channels x TN rows: its first channel and row, false
+// if there is none.  The tiles are dealt to the 8 XCDs (blockIdx.x mod 8) in
+// contiguous runs of an order that walks 8 row tiles, then the next channel tile, so
+// that the tiles that run together in an XCD share operands in its L2.
+__device__ __forceinline__ bool tile_of(int64_t m, int64_t n, int tm, int tn, int64_t& o0, int64_t& t0) {
+  const uint32_t ntm = (uint32_t)((m + tm - 1) / tm), ntn = (uint32_t)((n + tn - 1) / tn);
+  const uint64_t all = (uint64_t)ntm * ntn, per = (all + 7) / 8;
+  const uint64_t id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= per || id >= all) return false;
+  const uint64_t panel = id / (8ull * ntm), in_panel = id - panel * 8 * ntm;
+  const uint32_t high = (uint32_t)min((uint64_t)8, ntn - panel * 8);
+  o0 = (int64_t)(in_panel / high) * tm;
+  t0 = (int64_t)(panel * 8 + in_panel % high) * tn;
+  return true;
+}
+
+__device__ __forceinline__ constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 __device__ __forceinline__ constexpr int waitcnt_vm_lgkm0(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
 
-// NL copies of 1024 bytes to LDS (16 per lane), from `src` + off[q]; offsets at or past the bound bring zeros.
+// NL copies of 1024 bytes to LDS (16 per lane), from `src` + off[q] + add; offsets at or past the bound bring zeros.
 template <int NL, int STRIDE>
 __device__ __forceinline__ void copy_rows(char* __restrict__ dst, const void* src, uint32_t bound, const uint32_t (&off)[NL],
                                           uint32_t add, bool in) {
@@ -338,9 +353,9 @@ __device__ __forceinline__ void copy_rows(char* __restrict__ dst, const void* sr
 #endif
 }
 
-// One stage: four products deep from wb, xb (codes) and sw, sx (scales); the
-// buffers that the copies in flight fill are others, which the restrict
-// qualifiers state, so that reads need not wait for them.
+// One stage, from wb, xb (codes) and sw, sx (scales); the buffers that the copies
+// in flight fill are others, which the restrict qualifiers state, so that reads
+// need not wait for them.
 template <int S, int FA, int FB>
 __device__ __forceinline__ void mx_product(const u32x4 (&a)[FA], const u32x4 (&b)[FB], const uint32_t (&sa)[FA],
                                            const uint32_t (&sb)[FB], f32x16 (&acc)[FA][FB]) {
@@ -376,39 +391,41 @@ __device__ __forceinline__ void mx_stage(const char* __restrict__ wb, const char
   mx_product<3, FA, FB>(a[1], b[1], sa, sb, acc);
 }
 
-// A row's 8 scale bytes of the stage, `left` blocks to the end of k (zeros
-// stand for what is behind it: its codes are zeros too).
-__device__ __forceinline__ u32x2 stage_scales(const uint8_t* __restrict__ p, int64_t left) {
-  if (left >= 8) return *(const u32x2_any*)p;
-  u32x2 v{0u, 0u};
+// A row's 8 GS scale bytes of a group, `left` blocks to the end of k (zeros stand
+// for what is behind it: its codes are zeros too).
+template <int GS>
+__device__ __forceinline__ void group_scales(const uint8_t* __restrict__ p, int64_t left, u32x4 (&v)[GS / 2]) {
+  if (left >= 8 * GS) {
 #pragma unroll
-  for (int b = 0; b < 8; ++b)
-    if (b < left) v[b >> 2] |= (uint32_t)p[b] << (8 * (b & 3));
-  return v;
+    for (int i = 0; i < GS / 2; ++i) v[i] = *(const u32x4_any*)(p + 16 * i);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < GS / 2; ++i)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t x = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (16 * i + 4 * w + b < left) x |= (uint32_t)p[16 * i + 4 * w + b] << (8 * b);
+      v[i][w] = x;
+    }
 }
 
-template <int WM, int WN, int FA, int FB, int OUT_BF16>
+template <int WM, int WN, int FA, int FB, int R, int GS, int OUT_BF16>
 __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const uint8_t* __restrict__ xcodes,
-                                                               const uint8_t* __restrict__ xscales, int64_t n, int64_t k,
-                                                               const uint8_t* __restrict__ codes,
-                                                               const uint8_t* __restrict__ scales, int64_t m,
-                                                               void* __restrict__ Y, int64_t ldy) {
-  using TL = MxTile<WM, WN, FA, FB>;
+                                                                    const uint8_t* __restrict__ xscales, int64_t n, int64_t k,
+                                                                    const uint8_t* __restrict__ codes,
+                                                                    const uint8_t* __restrict__ scales, int64_t m,
+                                                                    void* __restrict__ Y, int64_t ldy) {
+  using TL = MxTile<WM, WN, FA, FB, R, GS>;
   constexpr int NW = TL::kWaves;
   __shared__ __attribute__((aligned(1024))) char smem[TL::kLds];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5, wm = wave / WN, wn = wave % WN;
 
-  // The tiles are dealt to the 8 XCDs (blockIdx.x mod 8) in contiguous runs of
-  // an order that walks 8 row tiles, then the next channel tile, so that the
-  // tiles that run together in an XCD share operands in its L2.
-  const uint32_t ntm = (uint32_t)((m + TL::kM - 1) / TL::kM), ntn = (uint32_t)((n + TL::kN - 1) / TL::kN);
-  const uint64_t all = (uint64_t)ntm * ntn, per = (all + 7) / 8;
-  const uint64_t id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= per || id >= all) return;
-  const uint64_t panel = id / (8ull * ntm), in_panel = id - panel * 8 * ntm;
-  const uint32_t high = (uint32_t)min((uint64_t)8, ntn - panel * 8);
-  const int64_t o0 = (int64_t)(in_panel / high) * TL::kM, t0 = (int64_t)(panel * 8 + in_panel % high) * TL::kN;
+  int64_t o0, t0;
+  if (!tile_of(m, n, TL::kM, TL::kN, o0, t0)) return;
 
   const int64_t kh = k / 2, kb = k / 32;
   const int64_t om = min((int64_t)TL::kM, m - o0), tn = min((int64_t)TL::kN, n - t0);   // channels and rows that are there
@@ -431,34 +448,29 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const uint8_t* __
     const int row = 8 * (NW * q + wave) + (lane >> 3);
     xoff[q] = row < tn ? (uint32_t)(row * kh) + 16 * piece : 0xC0000000u;
   }
-  char *w0 = smem, *w1 = w0 + TL::kWBuf, *x0 = w1 + TL::kWBuf, *x1 = x0 + TL::kXBuf, *s0 = x1 + TL::kXBuf, *s1 = s0 + TL::kSBuf;
-  const int64_t nst = (k + 255) / 256;
-  auto copy = [&](int64_t st, char* w, char* x) {
+  const int nst = (int)((k + 255) / 256);
+  char* const ring = smem;
+  char* const sring = smem + R * TL::kBuf;   // [group % 2][stage in it][row][8]
+  auto copy = [&](int st, int slot) {   // (past the last stage: zeros that nothing is fetched for)
     const bool in = st * 128 + 16 * piece < kh;
-    copy_rows<TL::kWLoads, NW * 1024>(w + wave * 1024, codes, wbound, woff, (uint32_t)(st * 128), in);
-    copy_rows<TL::kXLoads, NW * 1024>(x + wave * 1024, xcodes, xbound, xoff, (uint32_t)(st * 128), in);
+    char* to = ring + slot * TL::kBuf + wave * 1024;
+    copy_rows<TL::kWLoads, NW * 1024>(to, codes, wbound, woff, (uint32_t)st * 128, in);
+    copy_rows<TL::kXLoads, NW * 1024>(to + TL::kM * 128, xcodes, xbound, xoff, (uint32_t)st * 128, in);
   };
-  u32x2 sreg[TL::kSPer];
-  auto load_scales = [&](int64_t st) {
+  u32x4 sreg[GS / 2];
+  const uint8_t* const srow =
+      tid < TL::kM ? scales + min((int64_t)tid, om - 1) * kb : xscales + min((int64_t)min(tid, TL::kAll - 1) - TL::kM, tn - 1) * kb;
+  auto load_scales = [&](int grp) { group_scales<GS>(srow + (int64_t)grp * 8 * GS, kb - (int64_t)grp * 8 * GS, sreg); };
+  auto store_scales = [&](int grp) {
+    if (tid < TL::kAll)
 #pragma unroll
-    for (int q = 0; q < TL::kSPer; ++q) {
-      const int row = q * TL::kThreads + tid;
-      if (row >= TL::kAll) continue;
-      const uint8_t* p = row < TL::kM ? scales + min((int64_t)row, om - 1) * kb : xscales + min((int64_t)(row - TL::kM), tn - 1) * kb;
-      sreg[q] = stage_scales(p + 8 * st, kb - 8 * st);
-    }
-  };
-  auto store_scales = [&](char* s) {
-#pragma unroll
-    for (int q = 0; q < TL::kSPer; ++q) {
-      const int row = q * TL::kThreads + tid;
-      if (row < TL::kAll) *(u32x2*)(s + row * 8) = sreg[q];
-    }
+      for (int s = 0; s < GS; ++s)
+        *(u32x2*)(sring + ((grp & 1) * GS + s) * TL::kSBuf + tid * 8) = u32x2{sreg[s / 2][2 * (s & 1)], sreg[s / 2][2 * (s & 1) + 1]};
   };
   int rd[4];
 #pragma unroll
   for (int s = 0; s < 4; ++s) rd[s] = r * 128 + (((4 * h + s) ^ ((r >> 1) & 7)) * 16);
-  const int wrow = wm * 32 * FA, xrow = wn * 32 * FB;
+  const int wrow = wm * 32 * FA, xrow = TL::kM + wn * 32 * FB;
 
   f32x16 acc[FA][FB];
 #pragma unroll
@@ -469,39 +481,42 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const uint8_t* __
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
   load_scales(0);
-  copy(0, w0, x0);
-  store_scales(s0);
+#pragma unroll
+  for (int s = 0; s < R - 1; ++s) copy(s, s);
+  store_scales(0);
+  int slot = 0;
+  for (int st = 0; st < nst; st += GS) {
+    const int grp = st / GS;
+#pragma unroll
+    for (int s = 0; s < GS; ++s) {
+      if (s > 0 && st + s >= nst) break;
+      // Stage st + s is there once at most R - 2 stages of copies are in flight,
+      // and every wave is through with the stage before, whose place is filled next.
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((R - 2) * TL::kLoads));
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      if (s == 0 && st + GS < nst) load_scales(grp + 1);
+      copy(st + s + R - 1, slot == 0 ? R - 1 : slot - 1);
+      __builtin_amdgcn_sched_barrier(0);
+      const char* b = ring + slot * TL::kBuf;
+      const char* sc = sring + ((grp & 1) * GS + s) * TL::kSBuf + 4 * h;
+      mx_stage<FA, FB>(b + wrow * 128, b + xrow * 128, sc + (wrow + r) * 8, sc + (xrow + r) * 8, rd, acc);
+      slot = slot + 1 == R ? 0 : slot + 1;
+      if (s == GS - 1) store_scales(grp + 1);
+    }
+  }
   __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
   asm volatile("s_barrier" ::: "memory");
-  for (int64_t st = 0; st < nst; ++st) {
-    if (st + 1 < nst) {
-      load_scales(st + 1);
-      copy(st + 1, w1, x1);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    mx_stage<FA, FB>(w0 + wrow * 128, x0 + xrow * 128, s0 + (wrow + r) * 8 + 4 * h, s0 + (TL::kM + xrow + r) * 8 + 4 * h, rd, acc);
-    __builtin_amdgcn_sched_barrier(0);
-    if (st + 1 < nst) store_scales(s1);
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-    asm volatile("s_barrier" ::: "memory");
-    char* t = w0;
-    w0 = w1;
-    w1 = t;
-    t = x0;
-    x0 = x1;
-    x1 = t;
-    t = s0;
-    s0 = s1;
-    s1 = t;
-  }
 
   // Accumulator: lane l, register e -> channel 8 (e / 4) + 4 h + e % 4, row r.
+  constexpr int ES = OUT_BF16 ? 2 : 4;
   // 32 rows at a time go through LDS of the wave's own, so that a row's
   // channels leave in 16-byte pieces side by side.
-  constexpr int ES = OUT_BF16 ? 2 : 4, ROW = 32 * FA * ES + 16, PR = 32 * FA * ES / 16;
+  constexpr int ROW = 32 * FA * ES + 16, PR = 32 * FA * ES / 16;
   static_assert(NW * 32 * ROW <= TL::kLds, "output staging");
   char* stage = smem + wave * 32 * ROW;
-  const int64_t oc = o0 + wrow;
+  const int64_t oc = o0 + wrow, tr = t0 + wn * 32 * FB;
 #pragma unroll
   for (int j = 0; j < FB; ++j) {
 #pragma unroll
@@ -522,7 +537,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const uint8_t* __
     for (int q = 0; q < 32 * PR / 64; ++q) {
       const int e = q * 64 + lane, row = e / PR, pc = e % PR;
       const u32x4 v = *(const u32x4*)(stage + row * ROW + pc * 16);
-      const int64_t t = t0 + xrow + 32 * j + row, o = oc + pc * (16 / ES);
+      const int64_t t = tr + 32 * j + row, o = oc + pc * (16 / ES);
       if (t >= n) continue;
       if (o + 16 / ES <= m) {
         *(u32x4_a2*)((char*)Y + (t * ldy + o) * ES) = v;
@@ -536,6 +551,179 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const uint8_t* __
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
+// Tiles of 32 output channels x 32 FB rows for sizes that make few tiles: the
+// four waves of a workgroup share k instead, in pairs of stages of 256 in turn, in
+// LDS of their own, so that none waits for another (with the waves at the four
+// products of one stage and a barrier for each, 53 rows x 4096 x 14336 took 13.4 us
+// beside the quantization, with this 11).
+//   Operands as above.  A wave copies a stage's rows itself, one stage ahead.  A
+//   pair's 16 scale bytes per row are loaded into the row's two lanes, 8 each, and
+//   exchanged between the wave's halves.  (Loaded word by word in their place they
+//   took the address unit as long as the codes.)
+// The rest of k behind the last pair goes to the first waves, byte by byte where
+// scales are concerned.  The waves' sums are added in wave order through LDS.
+constexpr int TW = 4;
+template <int FB>
+struct MxThin {
+  static constexpr int kRows = 32 + 32 * FB, kBuf = kRows * 128, kLoads = kRows / 8;
+  static constexpr int kLd = 36, kRing = TW * 2 * kBuf, kSums = TW * 32 * FB * kLd * 4;
+  static constexpr int kLds = kRing > kSums ? kRing : kSums;
+};
+
+template <int FB>
+__device__ __forceinline__ void thin_stage(const char* __restrict__ b, const int (&rd)[4], const uint32_t (&s)[1 + FB],
+                                           f32x16 (&acc)[1][FB]) {
+  u32x4 w[4][1], x[4][FB];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i][0] = *(const u32x4*)(b + rd[i]);
+#pragma unroll
+    for (int j = 0; j < FB; ++j) x[i][j] = *(const u32x4*)(b + 4096 * (1 + j) + rd[i]);
+  }
+  uint32_t sw[1] = {s[0]}, sx[FB];
+#pragma unroll
+  for (int j = 0; j < FB; ++j) sx[j] = s[1 + j];
+  __builtin_amdgcn_sched_barrier(0);   // (all reads go out before the first product)
+  mx_product<0, 1, FB>(w[0], x[0], sw, sx, acc);
+  mx_product<1, 1, FB>(w[1], x[1], sw, sx, acc);
+  mx_product<2, 1, FB>(w[2], x[2], sw, sx, acc);
+  mx_product<3, 1, FB>(w[3], x[3], sw, sx, acc);
+}
+
+template <int FB, int OUT_BF16>
+__global__ __launch_bounds__(64 * TW) void mx_thin_kernel(const uint8_t* __restrict__ xcodes, const uint8_t* __restrict__ xscales,
+                                                          int64_t n, int64_t k, const uint8_t* __restrict__ codes,
+                                                          const uint8_t* __restrict__ scales, int64_t m, void* __restrict__ Y,
+                                                          int64_t ldy) {
+  using TL = MxThin<FB>;
+  __shared__ __attribute__((aligned(1024))) char smem[TL::kLds];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 31, h = lane >> 5;
+  int64_t o0, t0;
+  if (!tile_of(m, n, 32, 32 * FB, o0, t0)) return;
+  const int64_t kh = k / 2, kb = k / 32;
+  const int64_t om = min((int64_t)32, m - o0), tn = min((int64_t)32 * FB, n - t0);
+  codes += o0 * kh;
+  scales += o0 * kb;
+  xcodes += t0 * kh;
+  xscales += t0 * kb;
+  const uint32_t wbound = (uint32_t)(om * kh), xbound = (uint32_t)(tn * kh);
+
+  // Copy q: rows 8 q + lane / 8 of the stage's channels (q < 4), then of its rows;
+  // piece (lane % 8) ^ (row / 2) % 8, which depends on q % 2.
+  constexpr uint32_t kPast = 0x20000000u;   // past every bound (below 2^28: checked on the host), also with k's offsets added; two of them too
+  int piece[2];
+  uint32_t off[TL::kLoads];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) piece[p] = (lane & 7) ^ (4 * p + (lane >> 4));
+#pragma unroll
+  for (int q = 0; q < TL::kLoads; ++q) {
+    const int row = 8 * (q < 4 ? q : q - 4) + (lane >> 3);
+    off[q] = row < (q < 4 ? om : tn) ? (uint32_t)(row * kh) + 16 * piece[q & 1] : kPast;
+  }
+  char* const ring = smem + wave * 2 * TL::kBuf;
+  auto copy = [&](int slot, uint32_t add, int64_t left) __attribute__((always_inline)) {   // left: bytes of a row from there on
+#if __HIP_DEVICE_COMPILE__
+    const __amdgpu_buffer_rsrc_t wrs = __builtin_amdgcn_make_buffer_rsrc((void*)codes, (short)0, wbound, 0x00020000);
+    const __amdgpu_buffer_rsrc_t xrs = __builtin_amdgcn_make_buffer_rsrc((void*)xcodes, (short)0, xbound, 0x00020000);
+#pragma unroll
+    for (int q = 0; q < TL::kLoads; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(q < 4 ? wrs : xrs, (__attribute__((address_space(3))) void*)(ring + slot * TL::kBuf + q * 1024),
+                                               16, left >= 128 || 16 * piece[q & 1] < left ? off[q] + add : kPast, 0, 0, 0);
+#endif
+  };
+  uint32_t soff[1 + FB];   // scales of channel r, of rows r, 32 + r, .. (past the last it)
+  soff[0] = (uint32_t)(min(r, (int)om - 1) * kb);
+#pragma unroll
+  for (int j = 0; j < FB; ++j) soff[1 + j] = (uint32_t)(min(32 * j + r, (int)tn - 1) * kb);
+
+  int rd[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) rd[s] = r * 128 + (((4 * h + s) ^ ((r >> 1) & 7)) * 16);
+  f32x16 acc[1][FB];
+#pragma unroll
+  for (int j = 0; j < FB; ++j)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[0][j][e] = 0.0f;
+
+  const int pairs = (int)(k / 512), mine = pairs > wave ? (pairs - wave + TW - 1) / TW : 0;   // the wave's i-th is wave + TW i
+  if (mine > 0) {
+    u32x2 raw[1 + FB];
+    auto load_scales = [&](int i) __attribute__((always_inline)) {   // (behind the last pair the last one's)
+      const int at = 16 * (wave + TW * min(i, mine - 1)) + 8 * h;
+#pragma unroll
+      for (int j = 0; j <= FB; ++j) raw[j] = *(const u32x2_any*)((j ? xscales : scales) + (soff[j] + at));
+    };
+    auto copy_stage = [&](int i, int p) __attribute__((always_inline)) {
+      copy(p, i < mine ? (uint32_t)(wave + TW * i) * 256 + 128 * p : kPast, 128);
+    };
+    load_scales(0);
+    copy_stage(0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < mine; ++i) {
+      copy_stage(i, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(TL::kLoads));   // the first stage and the pair's scales are there
+      __builtin_amdgcn_sched_barrier(0);
+      // Lane (r, h) holds the words of stage h: h = 0's of its row, then h = 1's.
+      uint32_t s0[1 + FB], s1[1 + FB];
+#pragma unroll
+      for (int j = 0; j <= FB; ++j) {
+        const auto v = __builtin_amdgcn_permlane32_swap(raw[j][0], raw[j][1], false, false);
+        s0[j] = v[0];
+        s1[j] = v[1];
+      }
+      thin_stage<FB>(ring, rd, s0, acc);
+      __builtin_amdgcn_sched_barrier(0);
+      load_scales(i + 1);
+      copy_stage(i + 1, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(TL::kLoads + 1 + FB));   // the second stage
+      __builtin_amdgcn_sched_barrier(0);
+      thin_stage<FB>(ring + TL::kBuf, rd, s1, acc);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  const int st = 2 * pairs + wave;   // of the rest, at most two stages
+  if ((int64_t)st * 256 < k) {
+    copy(0, (uint32_t)st * 128, kh - (int64_t)st * 128);
+    uint32_t s[1 + FB];
+    const int64_t b0 = (int64_t)st * 8 + 4 * h;
+#pragma unroll
+    for (int j = 0; j <= FB; ++j) {
+      s[j] = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (b0 + b < kb) s[j] |= (uint32_t)(j ? xscales : scales)[soff[j] + (uint32_t)b0 + b] << (8 * b);
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __builtin_amdgcn_sched_barrier(0);
+    thin_stage<FB>(ring, rd, s, acc);
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+  asm volatile("s_barrier" ::: "memory");
+
+  // Accumulator: lane l, register e -> channel 8 (e / 4) + 4 h + e % 4, row r.
+  float* sum = (float*)smem;   // [wave][row][channel]
+#pragma unroll
+  for (int j = 0; j < FB; ++j)
+#pragma unroll
+    for (int e4 = 0; e4 < 4; ++e4)
+      *(f32x4*)(sum + (wave * 32 * FB + 32 * j + r) * TL::kLd + 8 * e4 + 4 * h) =
+          f32x4{acc[0][j][4 * e4], acc[0][j][4 * e4 + 1], acc[0][j][4 * e4 + 2], acc[0][j][4 * e4 + 3]};
+  __syncthreads();
+  for (int e = tid; e < 1024 * FB; e += 64 * TW) {
+    const int row = e >> 5, ch = e & 31;
+    if (row >= tn || ch >= om) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < TW; ++w) v += sum[(w * 32 * FB + row) * TL::kLd + ch];
+    const int64_t at = (t0 + row) * ldy + o0 + ch;
+    if (OUT_BF16) ((__bf16*)Y)[at] = (__bf16)v;
+    else ((float*)Y)[at] = v;
   }
 }
 
@@ -567,28 +755,46 @@ hipError_t mxfp4_dequantize_launch(const uint8_t* codes, const uint8_t* scales, 
   return hipGetLastError();
 }
 
-// Rows that are not quantized yet are quantized within the product's kernel up to this many.
-constexpr int64_t kFusedRows = 16;
-constexpr int64_t kFewRows = 64;
+// Whether the few-row kernel takes a product: it saves the launch that quantizes
+// the rows (about 4 us), but every 16 channels quantize them again, and its columns
+// serve 4 rows each.  us, few-row kernel / quantization and tiles, by rows and m x k:
+//   bf16   4 rows: 4096 x 4096 4.3 / 8.0, 28672 x 4096 15.2 / 17.2, 8192 x 28672 32 / 37;  8 rows: 4096 x 14336 10.6 / 11.6,
+//          16384 x 4096 15.3 / 12.6;  16 rows: 4096 x 4096 7.0 / 8.4, 8192 x 4096 11.9 / 10.1
+//   MXFP4  4 rows: 4096 x 14336 7.4 / 8.0, 28672 x 4096 12.9 / 12.9;  8 rows: 4096 x 14336 7.9 / 8.2, 28672 x 4096 13.5 / 12.8;
+//          16 rows: 4096 x 4096 4.3 / 5.1, 8192 x 4096 7.6 / 6.9
+//   fp32   4 rows: 4096 x 4096 5.6 / 7.6, 8192 x 4096 9.6 / 9.4;  8 rows: 4096 x 4096 7.8 / 7.7
+bool few_rows(int x_codes, int x_bf16, int64_t n, int64_t k, int64_t m) {
+  const int64_t size = m * k;
+  if (!x_codes && !x_bf16) return n <= 4 && size <= 1 << 24;
+  if (n <= 4) return !x_codes || size < 1 << 26;
+  return n <= 8 ? size < 1 << 26 : n <= 16 && size <= 1 << 24;
+}
 
-size_t mxfp4_gemm_workspace(int x_codes, int64_t n, int64_t k, int64_t m) {
-  return x_codes || n <= kFusedRows ? 0 : (size_t)n * (k / 2) + (size_t)n * (k / 32);
+size_t mxfp4_gemm_workspace(int x_codes, int x_bf16, int64_t n, int64_t k, int64_t m) {
+  return x_codes || few_rows(x_codes, x_bf16, n, k, m) ? 0 : (size_t)n * (k / 2) + (size_t)n * (k / 32);
 }
 
 hipError_t mxfp4_gemm_launch(const void* X, int x_codes, int x_bf16, const uint8_t* xscales, int64_t n, int64_t k, int64_t ldx,
                              const uint8_t* codes, const uint8_t* scales, int64_t m, void* Y, int out_bf16, int64_t ldy,
                              void* ws, hipStream_t s) {
-#define NVQ_FEW_(XT, NG, CG, OUT)                                                                                              \
-  hipLaunchKernelGGL((mx_few_kernel<XT, NG, CG, OUT>), dim3((unsigned)((m + 16 * CG - 1) / (16 * CG))), dim3(64 * FW), 0, s,   \
-                     (const XT*)X, xscales, n, k, ldx, codes, scales, m, Y, ldy)
-#define NVQ_FEW(XT, NG)                  \
-  do {                                   \
-    if (out_bf16) NVQ_FEW_(XT, NG, 1, 1); \
-    else NVQ_FEW_(XT, NG, 1, 0);          \
-    return hipGetLastError();            \
+#define NVQ_FEW_(XT, NG, OUT)                                                                                                   \
+  hipLaunchKernelGGL((mx_few_kernel<XT, NG, OUT>), dim3((unsigned)((m + 15) / 16)), dim3(64 * FW), 0, s, (const XT*)X, xscales, \
+                     n, k, ldx, codes, scales, m, Y, ldy)
+#define NVQ_FEW(XT, NG)                    \
+  do {                                     \
+    if (out_bf16) NVQ_FEW_(XT, NG, 1);     \
+    else NVQ_FEW_(XT, NG, 0);              \
+    return hipGetLastError();              \
   } while (0)
-  if (!x_codes && n <= kFusedRows) {
-    if (x_bf16) NVQ_FEW(uint16_t, 1);
+#define NVQ_FEW_BY(XT)            \
+  do {                            \
+    if (n <= 4) NVQ_FEW(XT, 1);   \
+    if (n <= 8) NVQ_FEW(XT, 2);   \
+    NVQ_FEW(XT, 4);               \
+  } while (0)
+  if (few_rows(x_codes, x_bf16, n, k, m)) {
+    if (x_codes) NVQ_FEW_BY(uint8_t);
+    if (x_bf16) NVQ_FEW_BY(uint16_t);
     NVQ_FEW(float, 1);
   }
   if (!x_codes) {
@@ -599,25 +805,43 @@ hipError_t mxfp4_gemm_launch(const void* X, int x_codes, int x_bf16, const uint8
     X = xc;
     xscales = xsc;
   }
-  if (n <= 16) NVQ_FEW(uint8_t, 1);
-  if (n <= 32) NVQ_FEW(uint8_t, 2);
-  if (n <= kFewRows) NVQ_FEW(uint8_t, 4);
-#define NVQ_TILE(WM, WN, FA, FB)                                                                                              \
+#define NVQ_LAUNCH(KERNEL, TM, TN, THREADS, ...)                                                                               \
   do {                                                                                                                        \
-    using TL = MxTile<WM, WN, FA, FB>;                                                                                        \
-    const int64_t tiles = ((m + TL::kM - 1) / TL::kM) * ((n + TL::kN - 1) / TL::kN), blocks = (tiles + 7) / 8 * 8;            \
-    if (blocks > kMaxThreads / TL::kThreads) return kTooManyTiles;                                                            \
+    const int64_t blocks = (((m + (TM)-1) / (TM)) * ((n + (TN)-1) / (TN)) + 7) / 8 * 8;                                       \
+    if (blocks > kMaxThreads / (THREADS)) return kTooManyTiles;                                                               \
     if (out_bf16)                                                                                                             \
-      hipLaunchKernelGGL((mx_tile_kernel<WM, WN, FA, FB, 1>), dim3((unsigned)blocks), dim3(TL::kThreads), 0, s,               \
-                         (const uint8_t*)X, xscales, n, k, codes, scales, m, Y, ldy);                                         \
+      hipLaunchKernelGGL((KERNEL<__VA_ARGS__, 1>), dim3((unsigned)blocks), dim3(THREADS), 0, s, (const uint8_t*)X, xscales, n, k, \
+                         codes, scales, m, Y, ldy);                                                                           \
     else                                                                                                                      \
-      hipLaunchKernelGGL((mx_tile_kernel<WM, WN, FA, FB, 0>), dim3((unsigned)blocks), dim3(TL::kThreads), 0, s,               \
-                         (const uint8_t*)X, xscales, n, k, codes, scales, m, Y, ldy);                                         \
+      hipLaunchKernelGGL((KERNEL<__VA_ARGS__, 0>), dim3((unsigned)blocks), dim3(THREADS), 0, s, (const uint8_t*)X, xscales, n, k, \
+                         codes, scales, m, Y, ldy);                                                                           \
     return hipGetLastError();                                                                                                 \
   } while (0)
-  if (((m + 255) / 256) * ((n + 255) / 256) >= 192) NVQ_TILE(2, 4, 4, 2);
-  NVQ_TILE(2, 2, 2, 2);
+#define NVQ_TILE(...)                                                                   \
+  do {                                                                                  \
+    using TL = MxTile<__VA_ARGS__>;                                                     \
+    NVQ_LAUNCH(mx_tile_kernel, TL::kM, TL::kN, TL::kThreads, __VA_ARGS__);              \
+  } while (0)
+#define NVQ_THIN(FB) NVQ_LAUNCH(mx_thin_kernel, 32, 32 * FB, 64 * TW, FB)
+  // The largest tile that the rows fill more than half of and that gives three
+  // quarters of the device's 256 CUs a tile.  us with 32 x 32 / 32 x 64 / 64 x 64 /
+  // 128 x 64 / 128 x 128 / 256 x 256 (channels x rows), quantization included: 64 rows x
+  // 4096 x 4096 9.1 / 11.1 / 11.7 / 13.5 / 18.3 / -; 128 rows 11.9 / 11.1 / 11.9 / 14.0 /
+  // 18.4 / -; 256 rows 18.8 / 15.1 / 12.8 / 14.8 / 18.9 / -; 512 rows - / 24 / 20 / 16.4 /
+  // 20.1 / -; 1024 rows - / - / 35 / 28 / 22.8 / 24; 64 rows x 28672 x 4096 28 / 24 / 21 / 18 /
+  // 24 / -; 512 rows - / - / 110 / 82 / 58 / 49; 8192 rows - / - / - / 1075 / 656 / 572.
+  auto tiles = [&](int64_t tm, int64_t tn) { return ((m + tm - 1) / tm) * ((n + tn - 1) / tn); };
+  constexpr int64_t kEnough = 192;
+  if (n > 128 && tiles(256, 256) >= kEnough) NVQ_TILE(2, 4, 4, 2, 2, 2);
+  if (n > 64 && tiles(128, 128) >= kEnough) NVQ_TILE(2, 2, 2, 2, 2, 4);
+  if (tiles(128, 64) >= kEnough) NVQ_TILE(2, 2, 2, 1, 4, 4);
+  if (tiles(64, 64) >= kEnough) NVQ_TILE(2, 2, 1, 1, 6, 4);
+  if (n > 32 && tiles(32, 64) >= kEnough) NVQ_THIN(2);
+  NVQ_THIN(1);
+#undef NVQ_THIN
 #undef NVQ_TILE
+#undef NVQ_LAUNCH
+#undef NVQ_FEW_BY
 #undef NVQ_FEW
 #undef NVQ_FEW_
 }
