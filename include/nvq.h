@@ -659,10 +659,15 @@ int mxfp4_gemm(const void* X, int x_dtype, const uint8_t* x_scales, int64_t n, i
  * exact in bf16; bf16 matrix cores, fp32 sums.
  *   dY      device bf16 [n x lddy], lddy >= m, aligned by its elements.
  *   dX      device [n x lddx] of dx_dtype (fp32 or bf16, RNE), lddx >= k.
+ *   ws      device workspace of mxfp4_gemm_dx_workspace_size(n, m, k) bytes
+ *           (256-aligned; may be NULL when that is 0): for many rows the weights
+ *           are expanded to bf16 once, into it, instead of in every tile; for few
+ *           it holds fp32 sums over parts of m, which are added in their order.
  *   The rest as for mxfp4_gemm.
  */
+size_t mxfp4_gemm_dx_workspace_size(int64_t n, int64_t m, int64_t k);
 int mxfp4_gemm_dx(const void* dY, int dy_dtype, int64_t n, int64_t m, int64_t lddy, const uint8_t* codes, const uint8_t* scales,
-                  int64_t k, void* dX, int dx_dtype, int64_t lddx, void* stream);
+                  int64_t k, void* dX, int dx_dtype, int64_t lddx, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * ---- the gated activation between the products of an MLP -------------------------

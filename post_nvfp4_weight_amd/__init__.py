@@ -39,7 +39,8 @@ EXPORTS = [
     "nvfp4_dequantize", "nvfp4_gemm_workspace_size", "nvfp4_gemm", "nvfp4_gemm_noalloc", "nvq_check_finite",
     "moe_topk", "moe_topk_backward", "moe_sort_workspace_size", "moe_sort",
     "nvfp4_gemm_grouped", "nvfp4_gemm_grouped_dx", "moe_combine", "moe_combine_backward",
-    "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm_workspace_size", "mxfp4_gemm", "mxfp4_gemm_dx",
+    "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm_workspace_size", "mxfp4_gemm",
+    "mxfp4_gemm_dx_workspace_size", "mxfp4_gemm_dx",
     "swiglu", "swiglu_backward", "nvfp4_moe_mlp_workspace_size", "nvfp4_moe_mlp",
     "nvq_status_string", "nvq_last_error",
 ]
@@ -94,7 +95,8 @@ def _load():
         "mxfp4_dequantize": (I32, [P, P, I64, I64, P, I32, P]),
         "mxfp4_gemm_workspace_size": (SZ, [I32, I64, I64, I64]),
         "mxfp4_gemm": (I32, [P, I32, P, I64, I64, I64, P, P, I64, P, I32, I64, P, SZ, P]),
-        "mxfp4_gemm_dx": (I32, [P, I32, I64, I64, I64, P, P, I64, P, I32, I64, P]),
+        "mxfp4_gemm_dx_workspace_size": (SZ, [I64, I64, I64]),
+        "mxfp4_gemm_dx": (I32, [P, I32, I64, I64, I64, P, P, I64, P, I32, I64, P, SZ, P]),
         "swiglu": (I32, [P, I32, I64, I64, I64, P, I32, I64, P]),
         "swiglu_backward": (I32, [P, I64, P, I32, I64, I64, I64, P, I64, P]),
         "nvfp4_moe_mlp_workspace_size": (SZ, [I64, I64, I64, I64]),
@@ -701,8 +703,10 @@ def mxfp4_gemm_dx(dY, codes, scales, out_dtype=torch.float32, dX=None):
     if my != m:
         raise ValueError(f"dY has {my} columns, the weights {m} outputs")
     dX, lddx = _output(dX, "dX", dY, n, k, out_dtype, dev)
+    need = lib.mxfp4_gemm_dx_workspace_size(n, m, k)
+    ws = _workspace(need, dY.device) if need else None
     _call(lib.mxfp4_gemm_dx, "mxfp4_gemm_dx", dev, dY.data_ptr(), NVQ_DTYPE_BF16, n, m, lddy, codes.data_ptr(), scales.data_ptr(), k,
-          dX.data_ptr(), _CODES[dX.dtype], lddx)
+          dX.data_ptr(), _CODES[dX.dtype], lddx, _addr(ws), need)
     return dX
 
 

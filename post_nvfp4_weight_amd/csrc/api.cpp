@@ -970,8 +970,20 @@ int mxfp4_gemm(const void* X, int x_dtype, const uint8_t* x_scales, int64_t n, i
                                         y_dtype == NVQ_DTYPE_BF16, ldy, ws, (hipStream_t)stream), fn, n, m);
 }
 
+// The first rows on expanded weights, the rest after them in the same workspace; or
+// all in the second form, if dY's alignment asks for it.
+static size_t dx_workspace(int64_t n, int64_t m, int64_t k) {
+  const int64_t rows = mxfp4_gemm_dx_expanded_rows(n, m, k);
+  return std::max({rows ? (size_t)m * k * 2 : 0, n > rows ? mxfp4_gemm_dx_split_workspace(n - rows, m, k) : 0,
+                   mxfp4_gemm_dx_split_workspace(n, m, k)});
+}
+
+size_t mxfp4_gemm_dx_workspace_size(int64_t n, int64_t m, int64_t k) {
+  return n > 0 && n <= 0x7FFFFFFF && m > 0 && m <= kMaxWidth && k > 0 && k <= kMaxWidth ? align_up(dx_workspace(n, m, k)) : 0;
+}
+
 int mxfp4_gemm_dx(const void* dY, int dy_dtype, int64_t n, int64_t m, int64_t lddy, const uint8_t* codes, const uint8_t* scales,
-                  int64_t k, void* dX, int dx_dtype, int64_t lddx, void* stream) {
+                  int64_t k, void* dX, int dx_dtype, int64_t lddx, void* ws, size_t ws_bytes, void* stream) {
   const char* fn = "mxfp4_gemm_dx";
   if (dy_dtype != NVQ_DTYPE_BF16) return failp(NVQ_ERR_DTYPE, fn, "dy_dtype %d (gradients must be bf16)", dy_dtype);
   if (!dtype_ok(dx_dtype)) return failp(NVQ_ERR_DTYPE, fn, "dx_dtype %d", dx_dtype);
@@ -986,8 +998,19 @@ int mxfp4_gemm_dx(const void* dY, int dy_dtype, int64_t n, int64_t m, int64_t ld
   if (!dY || !dX) return failp(NVQ_ERR_NULL, fn, "dY and dX are required");
   if (!aligned(dY, 2) || !aligned(dX, elem_size(dx_dtype))) return failp(NVQ_ERR_ALIGN, fn, "dY and dX must be aligned by their elements");
   if (dX == dY) return failp(NVQ_ERR_VALUE, fn, "dX may not be dY");
-  return tiles_status(mxfp4_gemm_dx_launch((const uint16_t*)dY, n, m, lddy, codes, scales, k, dX, dx_dtype == NVQ_DTYPE_BF16, lddx,
-                                           (hipStream_t)stream), fn, n, k);
+  const size_t need = dx_workspace(n, m, k);
+  if (need && (!ws || ws_bytes < need || !aligned(ws, kAlign)))
+    return failp(NVQ_ERR_WORKSPACE, fn, "workspace needs %zu bytes (256-aligned), got %zu", need, ws_bytes);
+  const uint16_t* d = (const uint16_t*)dY;
+  const int bf16 = dx_dtype == NVQ_DTYPE_BF16;
+  int64_t rows = lddy % 8 == 0 && aligned(d, 16) && lddy < 1 << 22 ? mxfp4_gemm_dx_expanded_rows(n, m, k) : 0;
+  if (rows) {
+    const int rc =
+        tiles_status(mxfp4_gemm_dx_expanded_launch(d, rows, m, lddy, codes, scales, k, dX, bf16, lddx, ws, (hipStream_t)stream), fn, n, k);
+    if (rc != NVQ_OK || rows == n) return rc;
+  }
+  return tiles_status(mxfp4_gemm_dx_launch(d + rows * lddy, n - rows, m, lddy, codes, scales, k,
+                                           (char*)dX + rows * lddx * (bf16 ? 2 : 4), bf16, lddx, ws, (hipStream_t)stream), fn, n, k);
 }
 
 int swiglu(const void* X, int x_dtype, int64_t n, int64_t h, int64_t ldx, void* out, int out_dtype, int64_t ldo, void* stream) {

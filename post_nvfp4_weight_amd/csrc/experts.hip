@@ -965,18 +965,23 @@ __global__ __launch_bounds__(64 * NW, 2) void grouped_dx_kernel(const uint16_t* 
 }
 
 // The gradient of one MXFP4 matrix's product: row tiles without a search, in
-// contiguous runs per XCD as above.
+// contiguous runs per XCD as above.  Where tiles are few, m is cut into `splits`
+// parts of mper (a multiple of 64), each with a tile of its own, whose fp32 sums go
+// to dX + part * rows * k (dX is then the workspace, mx_dx_sum_kernel adds them).
 template <int NW, int RF, int CF, bool DMA, int OUT_BF16>
 __global__ __launch_bounds__(64 * NW, 2) void mx_dx_kernel(const uint16_t* __restrict__ dY, int64_t rows, int64_t m,
                                                            int64_t lddy, const uint8_t* __restrict__ codes,
                                                            const uint8_t* __restrict__ scales, int64_t k,
-                                                           void* __restrict__ dX, int64_t lddx, int vec_out) {
+                                                           void* __restrict__ dX, int64_t lddx, int vec_out, int64_t mper,
+                                                           uint32_t splits) {
   using TL = GradTile<NW, RF, CF, Mxfp4>;
   __shared__ __attribute__((aligned(1024))) char smem[TL::kLds];
   const uint32_t ncol = (uint32_t)((k + TL::kCols - 1) / TL::kCols);
-  const uint64_t all = (uint64_t)((rows + TL::kRows - 1) / TL::kRows) * ncol, per = (all + 7) / 8;
-  const uint64_t id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  const uint64_t all = (uint64_t)((rows + TL::kRows - 1) / TL::kRows) * ncol * splits, per = (all + 7) / 8;
+  uint64_t id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
   if ((blockIdx.x >> 3) >= per || id >= all) return;
+  const int64_t part = (uint32_t)id % splits, m0 = part * mper;
+  id /= splits;
   const uint32_t tile = (uint32_t)id / ncol;   // (fewer than 2^31 workgroups)
   RowTile tl;
   tl.expert = 0;
@@ -984,8 +989,32 @@ __global__ __launch_bounds__(64 * NW, 2) void mx_dx_kernel(const uint16_t* __res
   tl.r0 = (int64_t)tile * TL::kRows;
   tl.r1 = min(rows, tl.r0 + TL::kRows);
   for_row_blocks<RF>(tl, [&]<int R>() {
-    tile_gradient<NW, R, CF, DMA, OUT_BF16, Mxfp4>(smem, tl, dY, m, lddy, codes, scales, 1.0f, k, dX, lddx, vec_out != 0);
+    tile_gradient<NW, R, CF, DMA, OUT_BF16, Mxfp4>(smem, tl, dY + m0, min(mper, m - m0), lddy, codes + m0 * (k / 2),
+                                                   scales + m0 * (k / 32), 1.0f, k,
+                                                   (char*)dX + part * rows * k * (OUT_BF16 ? 2 : 4), lddx, vec_out != 0);
   });
+}
+
+// dX = the parts' sums, in their order; four columns per thread (k is a multiple of 32).
+template <int OUT_BF16>
+__global__ __launch_bounds__(256) void mx_dx_sum_kernel(const float* __restrict__ parts, int64_t rows, int64_t k, uint32_t splits,
+                                                        void* __restrict__ dX, int64_t lddx) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = k / 4;
+  if (i >= rows * quads) return;
+  const int64_t row = i / quads, col = 4 * (i - row * quads);
+  f32x4 v = *(const f32x4*)(parts + 4 * i);
+#pragma unroll 4
+  for (uint32_t s = 1; s < splits; ++s) {
+    const f32x4 p = *(const f32x4*)(parts + s * rows * k + 4 * i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += p[e];
+  }
+  const int64_t at = row * lddx + col;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (OUT_BF16) ((__bf16*)dX)[at + e] = (__bf16)v[e];
+    else ((float*)dX)[at + e] = v[e];
+  }
 }
 
 // Workgroups for every row tile of height bt that rows over G experts can
@@ -1070,24 +1099,55 @@ hipError_t nvfp4_gemm_grouped_dx_launch(const uint16_t* dY, int64_t rows, int64_
   return hipGetLastError();
 }
 
+// Tiles of 128 or 64 rows x 256 columns, and parts of m: as many as give the
+// device's 512 places a tile each, of at least four steps of 64, whose sums are at
+// most 64 MiB.  (Without parts 64 rows x 28672 x 4096 took 518 us, with them 43.)
+// 128 rows where there are more than 512, or where more than 64 have parts of at
+// least 1024 to share the expansion over.  us with 64 / 128 rows: 513 x 4096 x 4096 49 /
+// 41, 2048 rows 105 / 93, 512 rows 42 / 47 (parts of 512), 256 rows 29 / 32, 512 x 14336 x
+// 4096 108 / 88 (parts of 1792), 512 x 28672 x 4096 209 / 150, 333 x 1004 x 1056 17 / 24.
+namespace {
+struct DxSplit {
+  int64_t height, mper, splits;
+};
+DxSplit dx_split(int64_t rows, int64_t m, int64_t k) {
+  DxSplit d{128, 0, 0};
+  for (;;) {
+    const int64_t tiles = ((rows + d.height - 1) / d.height) * ((k + 255) / 256);
+    const int64_t want = std::max<int64_t>(1, std::min({512 / tiles, (m + 255) / 256, (int64_t)(64 << 20) / (rows * k * 4)}));
+    d.mper = ((m + want - 1) / want + 63) / 64 * 64;
+    d.splits = (m + d.mper - 1) / d.mper;
+    if (d.height == 64 || rows > 512 || (rows > 64 && d.mper >= 1024)) return d;
+    d.height = 64;
+  }
+}
+}  // namespace
+
+size_t mxfp4_gemm_dx_split_workspace(int64_t rows, int64_t m, int64_t k) {
+  const DxSplit d = dx_split(rows, m, k);
+  return d.splits > 1 ? (size_t)d.splits * rows * k * 4 : 0;
+}
+
 hipError_t mxfp4_gemm_dx_launch(const uint16_t* dY, int64_t rows, int64_t m, int64_t lddy, const uint8_t* codes,
-                                const uint8_t* scales, int64_t k, void* dX, int out_bf16, int64_t lddx, hipStream_t s) {
-  const int vec = lddx % (out_bf16 ? 8 : 4) == 0 && (uintptr_t)dX % 16 == 0;
+                                const uint8_t* scales, int64_t k, void* dX, int out_bf16, int64_t lddx, void* ws, hipStream_t s) {
+  const DxSplit d = dx_split(rows, m, k);
+  const bool split = d.splits > 1;
+  void* to = split ? ws : dX;
+  const int64_t ldo = split ? k : lddx;
+  const int to_bf16 = split ? 0 : out_bf16;
+  const int vec = ldo % (to_bf16 ? 8 : 4) == 0 && (uintptr_t)to % 16 == 0;
   const bool dma = m % 8 == 0 && lddy % 8 == 0 && (uintptr_t)dY % 16 == 0 && lddy < (1 << 23);
-#define NVQ_DX(RF, DMA)                                                                                                \
-  do {                                                                                                                 \
-    using TL = GradTile<4, RF, 2, Mxfp4>;                                                                              \
-    const int64_t tiles = ((rows + TL::kRows - 1) / TL::kRows) * ((k + TL::kCols - 1) / TL::kCols);                    \
-    const int64_t blocks = (tiles + 7) / 8 * 8;                                                                        \
-    if (blocks > kMaxThreads / 256) return kTooManyTiles;                                                              \
-    if (out_bf16)                                                                                                      \
-      hipLaunchKernelGGL((mx_dx_kernel<4, RF, 2, DMA, 1>), dim3((unsigned)blocks), dim3(256), 0, s, dY, rows, m, lddy, \
-                         codes, scales, k, dX, lddx, vec);                                                             \
-    else                                                                                                               \
-      hipLaunchKernelGGL((mx_dx_kernel<4, RF, 2, DMA, 0>), dim3((unsigned)blocks), dim3(256), 0, s, dY, rows, m, lddy, \
-                         codes, scales, k, dX, lddx, vec);                                                             \
+  const int64_t blocks = (((rows + d.height - 1) / d.height) * ((k + 255) / 256) * d.splits + 7) / 8 * 8;
+  if (blocks > kMaxThreads / 256) return kTooManyTiles;
+#define NVQ_DX_(RF, DMA, OUT)                                                                                               \
+  hipLaunchKernelGGL((mx_dx_kernel<4, RF, 2, DMA, OUT>), dim3((unsigned)blocks), dim3(256), 0, s, dY, rows, m, lddy, codes, \
+                     scales, k, to, ldo, vec, d.mper, (uint32_t)d.splits)
+#define NVQ_DX(RF, DMA)                       \
+  do {                                        \
+    if (to_bf16) NVQ_DX_(RF, DMA, 1);         \
+    else NVQ_DX_(RF, DMA, 0);                 \
   } while (0)
-  if (rows > 512) {
+  if (d.height == 128) {
     if (dma) NVQ_DX(4, true);
     else NVQ_DX(4, false);
   } else {
@@ -1095,6 +1155,12 @@ hipError_t mxfp4_gemm_dx_launch(const uint16_t* dY, int64_t rows, int64_t m, int
     else NVQ_DX(2, false);
   }
 #undef NVQ_DX
+#undef NVQ_DX_
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !split) return e;
+  const dim3 grid((unsigned)((rows * (k / 4) + 255) / 256));
+  if (out_bf16) hipLaunchKernelGGL((mx_dx_sum_kernel<1>), grid, dim3(256), 0, s, (const float*)ws, rows, k, (uint32_t)d.splits, dX, lddx);
+  else hipLaunchKernelGGL((mx_dx_sum_kernel<0>), grid, dim3(256), 0, s, (const float*)ws, rows, k, (uint32_t)d.splits, dX, lddx);
   return hipGetLastError();
 }
 

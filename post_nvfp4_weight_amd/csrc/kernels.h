@@ -224,8 +224,15 @@ size_t mxfp4_gemm_workspace(int x_codes, int x_bf16, int64_t n, int64_t k, int64
 hipError_t mxfp4_gemm_launch(const void* X, int x_codes, int x_bf16, const uint8_t* xscales, int64_t n, int64_t k, int64_t ldx,
                              const uint8_t* codes, const uint8_t* scales, int64_t m, void* Y, int out_bf16, int64_t ldy,
                              void* ws, hipStream_t s);
+size_t mxfp4_gemm_dx_split_workspace(int64_t rows, int64_t m, int64_t k);
 hipError_t mxfp4_gemm_dx_launch(const uint16_t* dY, int64_t rows, int64_t m, int64_t lddy, const uint8_t* codes,
-                                const uint8_t* scales, int64_t k, void* dX, int out_bf16, int64_t lddx, hipStream_t s);
+                                const uint8_t* scales, int64_t k, void* dX, int out_bf16, int64_t lddx, void* ws, hipStream_t s);
+// The same on weights that are expanded into ws (2 m k bytes) first; how many of n
+// rows it is meant for.  dY 16-byte aligned, lddy a multiple of 8 below 2^22.
+int64_t mxfp4_gemm_dx_expanded_rows(int64_t n, int64_t m, int64_t k);
+hipError_t mxfp4_gemm_dx_expanded_launch(const uint16_t* dY, int64_t n, int64_t m, int64_t lddy, const uint8_t* codes,
+                                         const uint8_t* scales, int64_t k, void* dX, int out_bf16, int64_t lddx, void* ws,
+                                         hipStream_t s);
 hipError_t swiglu_launch(const void* X, int x_bf16, int64_t n, int64_t h, int64_t ldx, void* out, int out_bf16, int64_t ldo,
                          hipStream_t s);
 hipError_t swiglu_backward_launch(const void* dout, int64_t ldd, const void* X, int bf16, int64_t n, int64_t h, int64_t ldx,

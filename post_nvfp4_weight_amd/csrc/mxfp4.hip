@@ -310,13 +310,15 @@ __global__ __launch_bounds__(64 * FW, NG == 1 && sizeof(XT) < 4 ? 4 : 2) void mx
 //   pieces swizzled by (row / 2) % 8: the 16 rows that are read at once then touch
 //   all 64 banks.  Scales (which may start at any byte) go through registers, for
 //   GS stages at a time, one such group ahead.
-template <int WM, int WN, int FA, int FB, int R, int GS>
+// BF16: both operands bf16 (the gradient on weights that were expanded before):
+// a row's 128 bytes are 64 k, a piece 8 k of v_mfma_f32_32x32x16_bf16; no scales.
+template <int WM, int WN, int FA, int FB, int R, int GS, bool BF16 = false>
 struct MxTile {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kM = 32 * FA * WM, kN = 32 * FB * WN, kAll = kM + kN;
   static constexpr int kWLoads = kM / 8 / kWaves, kXLoads = kN / 8 / kWaves, kLoads = kWLoads + kXLoads;
-  static constexpr int kBuf = kAll * 128, kSBuf = kAll * 8;   // codes and scales of a stage; the channels' first
-  static constexpr int kLds = R * kBuf + 2 * GS * kSBuf;
+  static constexpr int kBuf = kAll * 128, kSBuf = BF16 ? 0 : kAll * 8;   // codes and scales of a stage; the channels' first
+  static constexpr int kRing = R * kBuf + 2 * GS * kSBuf, kOut = kWaves * 32 * (32 * FA * 4 + 16), kLds = kRing > kOut ? kRing : kOut;
   static_assert(kM % (8 * kWaves) == 0 && kN % (8 * kWaves) == 0 && kWaves % 2 == 0, "whole copies per wave");
   static_assert(kAll <= kThreads && (GS == 2 || GS == 4), "a thread per row of scales");
 };
@@ -366,14 +368,30 @@ __device__ __forceinline__ void mx_product(const u32x4 (&a)[FA], const u32x4 (&b
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fragment(a[i]), fragment(b[j]), acc[i][j], 4, 4, S, (int)sa[i], S,
                                                                   (int)sb[j]);
 }
-template <int FA, int FB>
+template <int S, int FA, int FB, bool BF16>
+__device__ __forceinline__ void multiply(const u32x4 (&a)[FA], const u32x4 (&b)[FB], const uint32_t (&sa)[FA], const uint32_t (&sb)[FB],
+                                         f32x16 (&acc)[FA][FB]) {
+  if constexpr (!BF16) {
+    mx_product<S, FA, FB>(a, b, sa, sb, acc);
+  } else {
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+      for (int j = 0; j < FB; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a[i]), __builtin_bit_cast(bf16x8, b[j]), acc[i][j],
+                                                            0, 0, 0);
+  }
+}
+template <int FA, int FB, bool BF16>
 __device__ __forceinline__ void mx_stage(const char* __restrict__ wb, const char* __restrict__ xb, const char* __restrict__ sw,
                                          const char* __restrict__ sx, const int (&rd)[4], f32x16 (&acc)[FA][FB]) {
   uint32_t sa[FA], sb[FB];
+  if (!BF16) {
 #pragma unroll
-  for (int i = 0; i < FA; ++i) sa[i] = *(const uint32_t*)(sw + i * 256);
+    for (int i = 0; i < FA; ++i) sa[i] = *(const uint32_t*)(sw + i * 256);
 #pragma unroll
-  for (int j = 0; j < FB; ++j) sb[j] = *(const uint32_t*)(sx + j * 256);
+    for (int j = 0; j < FB; ++j) sb[j] = *(const uint32_t*)(sx + j * 256);
+  }
   u32x4 a[2][FA], b[2][FB];
   auto read = [&](int s, int p) {
 #pragma unroll
@@ -383,12 +401,12 @@ __device__ __forceinline__ void mx_stage(const char* __restrict__ wb, const char
   };
   read(0, 0);
   read(1, 1);
-  mx_product<0, FA, FB>(a[0], b[0], sa, sb, acc);
+  multiply<0, FA, FB, BF16>(a[0], b[0], sa, sb, acc);
   read(2, 0);
-  mx_product<1, FA, FB>(a[1], b[1], sa, sb, acc);
+  multiply<1, FA, FB, BF16>(a[1], b[1], sa, sb, acc);
   read(3, 1);
-  mx_product<2, FA, FB>(a[0], b[0], sa, sb, acc);
-  mx_product<3, FA, FB>(a[1], b[1], sa, sb, acc);
+  multiply<2, FA, FB, BF16>(a[0], b[0], sa, sb, acc);
+  multiply<3, FA, FB, BF16>(a[1], b[1], sa, sb, acc);
 }
 
 // A row's 8 GS scale bytes of a group, `left` blocks to the end of k (zeros stand
@@ -412,28 +430,30 @@ __device__ __forceinline__ void group_scales(const uint8_t* __restrict__ p, int6
     }
 }
 
-template <int WM, int WN, int FA, int FB, int R, int GS, int OUT_BF16>
-__global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const uint8_t* __restrict__ xcodes,
-                                                                    const uint8_t* __restrict__ xscales, int64_t n, int64_t k,
-                                                                    const uint8_t* __restrict__ codes,
-                                                                    const uint8_t* __restrict__ scales, int64_t m,
-                                                                    void* __restrict__ Y, int64_t ldy) {
-  using TL = MxTile<WM, WN, FA, FB, R, GS>;
+// kbytes: bytes of a row that are multiplied; xs, ws (BF16): from one row to the next.
+template <int WM, int WN, int FA, int FB, int R, int GS, bool BF16, int OUT_BF16>
+__global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const uint8_t* __restrict__ xcodes, int64_t xs,
+                                                               const uint8_t* __restrict__ xscales, int64_t n, int64_t kbytes,
+                                                               const uint8_t* __restrict__ codes, int64_t ws,
+                                                               const uint8_t* __restrict__ scales, int64_t m,
+                                                               void* __restrict__ Y, int64_t ldy) {
+  using TL = MxTile<WM, WN, FA, FB, R, GS, BF16>;
   constexpr int NW = TL::kWaves;
   __shared__ __attribute__((aligned(1024))) char smem[TL::kLds];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5, wm = wave / WN, wn = wave % WN;
-
   int64_t o0, t0;
   if (!tile_of(m, n, TL::kM, TL::kN, o0, t0)) return;
 
-  const int64_t kh = k / 2, kb = k / 32;
+  const int64_t kb = BF16 ? 0 : kbytes / 16, xstride = BF16 ? xs : kbytes, wstride = BF16 ? ws : kbytes;
   const int64_t om = min((int64_t)TL::kM, m - o0), tn = min((int64_t)TL::kN, n - t0);   // channels and rows that are there
-  codes += o0 * kh;
-  scales += o0 * kb;
-  xcodes += t0 * kh;
-  xscales += t0 * kb;
-  const uint32_t wbound = (uint32_t)(om * kh), xbound = (uint32_t)(tn * kh);   // (below 2^32: checked on the host)
+  codes += o0 * wstride;
+  xcodes += t0 * xstride;
+  if (!BF16) {
+    scales += o0 * kb;
+    xscales += t0 * kb;
+  }
+  const uint32_t wbound = (uint32_t)((om - 1) * wstride + kbytes), xbound = (uint32_t)((tn - 1) * xstride + kbytes);   // (below 0xC0000000: checked on the host)
 
   // Copy q of a stage: rows 8 (NW q + wave) + lane / 8, piece (lane % 8) ^ (row / 2) % 8.
   const int piece = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));
@@ -441,25 +461,25 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const uint8_t* __
 #pragma unroll
   for (int q = 0; q < TL::kWLoads; ++q) {
     const int row = 8 * (NW * q + wave) + (lane >> 3);
-    woff[q] = row < om ? (uint32_t)(row * kh) + 16 * piece : 0xC0000000u;
+    woff[q] = row < om ? (uint32_t)(row * wstride) + 16 * piece : 0xC0000000u;
   }
 #pragma unroll
   for (int q = 0; q < TL::kXLoads; ++q) {
     const int row = 8 * (NW * q + wave) + (lane >> 3);
-    xoff[q] = row < tn ? (uint32_t)(row * kh) + 16 * piece : 0xC0000000u;
+    xoff[q] = row < tn ? (uint32_t)(row * xstride) + 16 * piece : 0xC0000000u;
   }
-  const int nst = (int)((k + 255) / 256);
+  const int nst = (int)((kbytes + 127) / 128);
   char* const ring = smem;
   char* const sring = smem + R * TL::kBuf;   // [group % 2][stage in it][row][8]
   auto copy = [&](int st, int slot) {   // (past the last stage: zeros that nothing is fetched for)
-    const bool in = st * 128 + 16 * piece < kh;
+    const bool in = (int64_t)st * 128 + 16 * piece < kbytes;
     char* to = ring + slot * TL::kBuf + wave * 1024;
     copy_rows<TL::kWLoads, NW * 1024>(to, codes, wbound, woff, (uint32_t)st * 128, in);
     copy_rows<TL::kXLoads, NW * 1024>(to + TL::kM * 128, xcodes, xbound, xoff, (uint32_t)st * 128, in);
   };
   u32x4 sreg[GS / 2];
   const uint8_t* const srow =
-      tid < TL::kM ? scales + min((int64_t)tid, om - 1) * kb : xscales + min((int64_t)min(tid, TL::kAll - 1) - TL::kM, tn - 1) * kb;
+      BF16 ? nullptr : tid < TL::kM ? scales + min((int64_t)tid, om - 1) * kb : xscales + min((int64_t)min(tid, TL::kAll - 1) - TL::kM, tn - 1) * kb;
   auto load_scales = [&](int grp) { group_scales<GS>(srow + (int64_t)grp * 8 * GS, kb - (int64_t)grp * 8 * GS, sreg); };
   auto store_scales = [&](int grp) {
     if (tid < TL::kAll)
@@ -471,6 +491,11 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const uint8_t* __
 #pragma unroll
   for (int s = 0; s < 4; ++s) rd[s] = r * 128 + (((4 * h + s) ^ ((r >> 1) & 7)) * 16);
   const int wrow = wm * 32 * FA, xrow = TL::kM + wn * 32 * FB;
+  // A wave without a channel or a row only copies.  In the large tile the branch also
+  // keeps the compiler from moving reads of the next stage up, for which it spilled
+  // (578 us with it, 682 without, at 8192 rows x 28672 x 4096); the small ones are a
+  // twentieth faster without (8.3 us against 8.9 at 1537 x 1003 x 1056).
+  const bool live = FA * FB < 8 || (wrow < om && wn * 32 * FB < tn);
 
   f32x16 acc[FA][FB];
 #pragma unroll
@@ -480,10 +505,10 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const uint8_t* __
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  load_scales(0);
+  if (!BF16) load_scales(0);
 #pragma unroll
   for (int s = 0; s < R - 1; ++s) copy(s, s);
-  store_scales(0);
+  if (!BF16) store_scales(0);
   int slot = 0;
   for (int st = 0; st < nst; st += GS) {
     const int grp = st / GS;
@@ -496,14 +521,14 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const uint8_t* __
       __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((R - 2) * TL::kLoads));
       asm volatile("s_barrier" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      if (s == 0 && st + GS < nst) load_scales(grp + 1);
+      if (!BF16 && s == 0 && st + GS < nst) load_scales(grp + 1);
       copy(st + s + R - 1, slot == 0 ? R - 1 : slot - 1);
       __builtin_amdgcn_sched_barrier(0);
       const char* b = ring + slot * TL::kBuf;
       const char* sc = sring + ((grp & 1) * GS + s) * TL::kSBuf + 4 * h;
-      mx_stage<FA, FB>(b + wrow * 128, b + xrow * 128, sc + (wrow + r) * 8, sc + (xrow + r) * 8, rd, acc);
+      if (live) mx_stage<FA, FB, BF16>(b + wrow * 128, b + xrow * 128, sc + (wrow + r) * 8, sc + (xrow + r) * 8, rd, acc);
       slot = slot + 1 == R ? 0 : slot + 1;
-      if (s == GS - 1) store_scales(grp + 1);
+      if (!BF16 && s == GS - 1) store_scales(grp + 1);
     }
   }
   __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
@@ -551,6 +576,40 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const uint8_t* __
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
+// W [m x k] to bf16 W^T [k x m]: 64 m x 64 k per workgroup, through LDS.
+// Thread (row tid / 4, quarter tid % 4) expands 16 codes of a row under one scale
+// and writes them down a column of LDS; 16 m of a column leave as two vectors.
+__global__ __launch_bounds__(256) void mx_transpose_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                           int64_t m, int64_t k, uint16_t* __restrict__ out) {
+  constexpr int LD = 64 + 8;   // (rows apart by 36 banks)
+  __shared__ __attribute__((aligned(16))) uint16_t t[64][LD];
+  const int64_t m0 = (int64_t)blockIdx.x * 64, k0 = (int64_t)blockIdx.y * 64;
+  const int row = threadIdx.x >> 2, part = threadIdx.x & 3;
+  if (m0 + row < m && k0 + 16 * part < k) {
+    const u32x2 w = *(const u32x2*)(codes + (m0 + row) * (k / 2) + k0 / 2 + 8 * part);
+    const float s = scale_value(scales[(m0 + row) * (k / 32) + k0 / 32 + part / 2]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t v = w[i];
+      const f32x2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 1),
+                          __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 3)};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const __bf16 b = (__bf16)((e & 1 ? p[e / 2].y : p[e / 2].x) * s);
+        t[16 * part + 8 * i + e][row] = __builtin_bit_cast(uint16_t, b);
+      }
+    }
+  }
+  __syncthreads();
+  if (k0 + row < k) {   // column `row` of the tile, m 16 part ..
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t mm = m0 + 16 * part + 8 * i;   // (m is a multiple of 8)
+      if (mm < m) *(u32x4*)(out + (k0 + row) * m + mm) = *(const u32x4*)&t[row][16 * part + 8 * i];
+    }
   }
 }
 
@@ -805,24 +864,30 @@ hipError_t mxfp4_gemm_launch(const void* X, int x_codes, int x_bf16, const uint8
     X = xc;
     xscales = xsc;
   }
-#define NVQ_LAUNCH(KERNEL, TM, TN, THREADS, ...)                                                                               \
-  do {                                                                                                                        \
-    const int64_t blocks = (((m + (TM)-1) / (TM)) * ((n + (TN)-1) / (TN)) + 7) / 8 * 8;                                       \
-    if (blocks > kMaxThreads / (THREADS)) return kTooManyTiles;                                                               \
-    if (out_bf16)                                                                                                             \
-      hipLaunchKernelGGL((KERNEL<__VA_ARGS__, 1>), dim3((unsigned)blocks), dim3(THREADS), 0, s, (const uint8_t*)X, xscales, n, k, \
-                         codes, scales, m, Y, ldy);                                                                           \
-    else                                                                                                                      \
-      hipLaunchKernelGGL((KERNEL<__VA_ARGS__, 0>), dim3((unsigned)blocks), dim3(THREADS), 0, s, (const uint8_t*)X, xscales, n, k, \
-                         codes, scales, m, Y, ldy);                                                                           \
-    return hipGetLastError();                                                                                                 \
+#define NVQ_GRID(TM, TN, THREADS)                                                          \
+  const int64_t blocks = (((m + (TM)-1) / (TM)) * ((n + (TN)-1) / (TN)) + 7) / 8 * 8;     \
+  if (blocks > kMaxThreads / (THREADS)) return kTooManyTiles;
+#define NVQ_TILE_(OUT, ...)                                                                                                    \
+  hipLaunchKernelGGL((mx_tile_kernel<__VA_ARGS__, false, OUT>), dim3((unsigned)blocks), dim3(TL::kThreads), 0, s, (const uint8_t*)X, \
+                     k / 2, xscales, n, k / 2, codes, k / 2, scales, m, Y, ldy)
+#define NVQ_TILE(...)                            \
+  do {                                           \
+    using TL = MxTile<__VA_ARGS__>;              \
+    NVQ_GRID(TL::kM, TL::kN, TL::kThreads)       \
+    if (out_bf16) NVQ_TILE_(1, __VA_ARGS__);     \
+    else NVQ_TILE_(0, __VA_ARGS__);              \
+    return hipGetLastError();                    \
   } while (0)
-#define NVQ_TILE(...)                                                                   \
-  do {                                                                                  \
-    using TL = MxTile<__VA_ARGS__>;                                                     \
-    NVQ_LAUNCH(mx_tile_kernel, TL::kM, TL::kN, TL::kThreads, __VA_ARGS__);              \
+#define NVQ_THIN_(FB, OUT)                                                                                                   \
+  hipLaunchKernelGGL((mx_thin_kernel<FB, OUT>), dim3((unsigned)blocks), dim3(64 * TW), 0, s, (const uint8_t*)X, xscales, n, k, codes, \
+                     scales, m, Y, ldy)
+#define NVQ_THIN(FB)                     \
+  do {                                   \
+    NVQ_GRID(32, 32 * FB, 64 * TW)       \
+    if (out_bf16) NVQ_THIN_(FB, 1);      \
+    else NVQ_THIN_(FB, 0);               \
+    return hipGetLastError();            \
   } while (0)
-#define NVQ_THIN(FB) NVQ_LAUNCH(mx_thin_kernel, 32, 32 * FB, 64 * TW, FB)
   // The largest tile that the rows fill more than half of and that gives three
   // quarters of the device's 256 CUs a tile.  us with 32 x 32 / 32 x 64 / 64 x 64 /
   // 128 x 64 / 128 x 128 / 256 x 256 (channels x rows), quantization included: 64 rows x
@@ -839,11 +904,46 @@ hipError_t mxfp4_gemm_launch(const void* X, int x_codes, int x_bf16, const uint8
   if (n > 32 && tiles(32, 64) >= kEnough) NVQ_THIN(2);
   NVQ_THIN(1);
 #undef NVQ_THIN
+#undef NVQ_THIN_
 #undef NVQ_TILE
-#undef NVQ_LAUNCH
+#undef NVQ_TILE_
+#undef NVQ_GRID
 #undef NVQ_FEW_BY
 #undef NVQ_FEW
 #undef NVQ_FEW_
+}
+
+// The gradient of many rows: the weights are expanded and transposed once, into
+// the workspace, and the product runs on bf16 tiles without any expansion.
+// The device's 256 CUs hold one 256 x 256 tile each; the rows that this form takes
+// are all full ones where the last round of tiles is at least four fifths full, else
+// those of the full rounds before it, of which there must be two.  us for m = k =
+// 4096 with this / with tiles that expand for themselves: 4096 rows 129 / 140, 8195
+// rows 251 / 315, 16384 rows 459 / 536; below a round 2048 rows 105 / 92.
+int64_t mxfp4_gemm_dx_expanded_rows(int64_t n, int64_t m, int64_t k) {
+  if (m % 8 != 0) return 0;   // (a row of W^T is copied in pieces of 16 bytes)
+  const int64_t across = (k + 255) / 256, full = n / 256 * across, rounds = full / 256, left = full % 256;
+  if (full >= 256 ? left == 0 || 5 * left >= 4 * 256 : 5 * left >= 4 * 256) return n / 256 * 256;
+  return rounds >= 2 ? 256 * rounds / across * 256 : 0;
+}
+
+hipError_t mxfp4_gemm_dx_expanded_launch(const uint16_t* dY, int64_t n, int64_t m, int64_t lddy, const uint8_t* codes,
+                                         const uint8_t* scales, int64_t k, void* dX, int out_bf16, int64_t lddx, void* ws,
+                                         hipStream_t s) {
+  const dim3 grid((unsigned)((m + 63) / 64), (unsigned)((k + 63) / 64));
+  hipLaunchKernelGGL(mx_transpose_kernel, grid, dim3(256), 0, s, codes, scales, m, k, (uint16_t*)ws);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  using TL = MxTile<2, 4, 4, 2, 2, 2, true>;
+  const int64_t blocks = (((k + TL::kM - 1) / TL::kM) * ((n + TL::kN - 1) / TL::kN) + 7) / 8 * 8;
+  if (blocks > kMaxThreads / TL::kThreads) return kTooManyTiles;
+#define NVQ_DX(OUT)                                                                                                            \
+  hipLaunchKernelGGL((mx_tile_kernel<2, 4, 4, 2, 2, 2, true, OUT>), dim3((unsigned)blocks), dim3(TL::kThreads), 0, s, (const uint8_t*)dY,   \
+                     2 * lddy, nullptr, n, 2 * m, (const uint8_t*)ws, 2 * m, nullptr, k, dX, lddx)
+  if (out_bf16) NVQ_DX(1);
+  else NVQ_DX(0);
+#undef NVQ_DX
+  return hipGetLastError();
 }
 
 }  // namespace nvq

@@ -66,8 +66,8 @@ def test_gemm(nvq):
 
 
 def test_gemm_dx(nvq):
-    def f(dY=fake, dd=1, n=4, m=16, lddy=16, codes=fake, scales=fake, k=64, dX=other, xd=0, lddx=64):
-        return nvq.lib.mxfp4_gemm_dx(dY, dd, n, m, lddy, codes, scales, k, dX, xd, lddx, None)
+    def f(dY=fake, dd=1, n=4, m=16, lddy=16, codes=fake, scales=fake, k=64, dX=other, xd=0, lddx=64, ws=None, wb=0):
+        return nvq.lib.mxfp4_gemm_dx(dY, dd, n, m, lddy, codes, scales, k, dX, xd, lddx, ws, wb, None)
 
     assert f(dd=0) == DTYPE and f(xd=2) == DTYPE
     for bad in (dict(k=48), dict(m=0), dict(lddy=15), dict(lddx=63), dict(n=-1), dict(n=1 << 31), dict(m=4000001, lddy=4000001)):
@@ -77,6 +77,10 @@ def test_gemm_dx(nvq):
     assert f(dY=P(4097)) == ALIGN and f(codes=P(4104)) == ALIGN and f(dX=P(4098)) == ALIGN
     assert f(dX=fake) == VALUE
     assert f(n=0, dY=None, codes=None, scales=None, dX=None) == 0
+    need = nvq.lib.mxfp4_gemm_dx_workspace_size(65536, 16, 64)
+    assert need >= 16 * 64 * 2 and nvq.lib.mxfp4_gemm_dx_workspace_size(0, 16, 64) == 0
+    for bad in (dict(), dict(ws=P(1 << 20), wb=16 * 64 * 2 - 1), dict(ws=P((1 << 20) + 8), wb=need)):
+        assert f(n=65536, **bad) == WORKSPACE, bad
 
 
 def test_swiglu(nvq):
