@@ -641,13 +641,16 @@ def moe_combine_backward(dout, Y, pos, weights=None, dY=None, need_dY=True, need
 
 def _mxfp4(codes, scales, name, dev):
     """(rows, k) of MXFP4 codes [rows, k/2] and scales [rows, k/32] on device number dev (None: any)."""
-    _want(codes, name, (_U8,), (None, None), dev)
+    if not (isinstance(codes, torch.Tensor) and codes.is_cuda and codes.dtype is _U8 and codes.dim() == 2
+            and (dev is None or codes.get_device() == dev) and codes.is_contiguous()):
+        _want(codes, name, (_U8,), (None, None), dev)
+        raise ValueError(f"{name} must be contiguous")
     rows, kh = codes.shape
     if kh % 16:
         raise ValueError(f"{name} has {kh} bytes per row, not a multiple of 16 (blocks of 32)")
-    dev = codes.get_device()
-    _dense(codes, name, _U8, (rows, kh), dev)
-    _dense(scales, f"{name}' scales", _U8, (rows, kh // 16), dev)
+    if not (isinstance(scales, torch.Tensor) and scales.dtype is _U8 and scales.shape == (rows, kh // 16)
+            and scales.get_device() == codes.get_device() and scales.is_contiguous()):
+        _dense(scales, f"{name}' scales", _U8, (rows, kh // 16), codes.get_device())
     return rows, 2 * kh
 
 

@@ -56,6 +56,7 @@ struct MoeMlp {
   int32_t* count;     // entries
   float* bad;         // per token: 0, or NaN from the weight of a slot without an expert
   Entry* entries;
+  float* scales;      // of each entry: g of its expert in the second product
   uint16_t* act;      // activations, act_row(h) elements per row
 };
 
@@ -149,21 +150,17 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Tokens before t.
-__device__ __forceinline__ int before(uint64_t tokens, int t) { return __popcll(tokens & ((1ull << t) - 1)); }
-// An entry, the same for the whole wave, and its expert's g.  A lane's column
+// An entry, the same for the whole wave.  A lane's column
 // stands for token number 4 g + (l % 16) / 4 of the entry in group g (-1 for none).
 template <int NG>
 struct Columns {
   Entry e;
-  float scale;
   int token[NG];
-  __device__ __forceinline__ void set(const Entry& in, float g, int lane) {
+  __device__ __forceinline__ void set(const Entry& in, int lane) {
     e.expert = __builtin_amdgcn_readfirstlane(in.expert);
     e.row = __builtin_amdgcn_readfirstlane(in.row);
     e.tokens = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)in.tokens) |
                (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(in.tokens >> 32)) << 32;
-    scale = g;
     const int mine = (lane >> 2) & 3;
     uint64_t left = e.tokens;
 #pragma unroll
@@ -254,6 +251,10 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(const MoeMlp a) {
   for (int i = tid; i < used; i += 64 * MW) {
     const Entry e = list[i];
     scale[i] = a.ug[e.expert];
+    if (blockIdx.x == 0) {
+      a.entries[i] = e;
+      a.scales[i] = a.dg[e.expert];
+    }
     int row = e.row;
     for (uint64_t left = e.tokens; left; left &= left - 1, ++row) {
       const int t = __builtin_ctzll(left);
@@ -265,7 +266,6 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(const MoeMlp a) {
   __syncthreads();
   if (blockIdx.x == 0) {
     if (tid == 0) *a.count = used;
-    for (int i = tid; i < used; i += 64 * MW) a.entries[i] = list[i];
     if (tid < a.T) {
       float nan = 0.0f;
       for (int s = 0; s < a.K; ++s) {
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(const MoeMlp a) {
   Columns<NG> cur;
   auto enter = [&](int it, Columns<NG>& cols) NVQ_INLINE {
     it = min(it, items - 1);
-    cols.set(list[it / nt], scale[it / nt], lane);
+    cols.set(list[it / nt], lane);
   };
   u32x4 x[NG][4];
   auto load_x = [&](const Columns<NG>& of, int ch) NVQ_INLINE {   // zeros where there is no token and from k on
@@ -326,6 +326,7 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(const MoeMlp a) {
   };
   auto finish = [&]() NVQ_INLINE {   // the item's activations
     const int o0 = 16 * (item % nt), n = __popcll(cur.e.tokens);
+    const float g1 = scale[item / nt];
 #pragma unroll
     for (int g = 0; g < NG; ++g)
       if (4 * g < n) part[wave][4 * g + ((lane >> 2) & 3)][4 * (lane >> 4) + (lane & 3)] = quad_sum(acc[g], lane);
@@ -339,8 +340,8 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(const MoeMlp a) {
         gate += part[w][t][ch];
         up += part[w + 1][t][ch];
       }
-      gate *= cur.scale;
-      up *= cur.scale;
+      gate *= g1;
+      up *= g1;
       const float z = expf(-fabsf(gate)), one = 1.0f / (1.0f + z);
       const float v = gate * (gate >= 0.0f ? one : z * one) * up * wrow[cur.e.row + t];
       const __bf16 hi = (__bf16)v;
@@ -424,19 +425,19 @@ __global__ __launch_bounds__(64 * down_waves(NG), NG == 1 ? 4 : 3) void moe_down
   float* totals = (float*)dyn;   // [wave][token][16]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t o0 = (int64_t)blockIdx.x * 16, stride = act_row(a.h);
-  const int used = *a.count, per = (int)((a.h + kChunk - 1) / kChunk), units = used * per;
-  int at = (int)((int64_t)units * wave / DW);
-  const int end = (int)((int64_t)units * (wave + 1) / DW);
+  const int used = *a.count, per = (int)((a.h + kChunk - 1) / kChunk);
   Entry* list = (Entry*)(totals + DW * a.T * 16);
   float* scale = (float*)(list + most_entries(a.T, a.E, a.K, 4 * NG));
-  for (int i = tid; i < used; i += 64 * DW) {
-    const Entry e = a.entries[i];
-    list[i] = e;
-    scale[i] = a.dg[e.expert];
+  for (int i = tid; i < (int)most_entries(a.T, a.E, a.K, 4 * NG); i += 64 * DW) {   // (without waiting for the count)
+    list[i] = a.entries[i];
+    scale[i] = a.scales[i];
   }
   for (int i = tid; i < DW * a.T * 16; i += 64 * DW) totals[i] = 0.0f;
   float* mine = totals + wave * a.T * 16 + 4 * (lane >> 4) + (lane & 3);
   __syncthreads();
+  const int units = used * per;
+  int at = (int)((int64_t)units * wave / DW);
+  const int end = (int)((int64_t)units * (wave + 1) / DW);
 
   if (at < end) {
     int ea = at / per, ep = at - ea * per, la = ea, lp = ep;   // unit ep of entry ea; the next to load
@@ -478,7 +479,8 @@ __global__ __launch_bounds__(64 * down_waves(NG), NG == 1 ? 4 : 3) void moe_down
     };
     clear();
     Columns<NG> cur;
-    cur.set(list[ea], scale[ea], lane);
+    cur.set(list[ea], lane);
+    float g2 = scale[ea];
     Chunk buf[FD];
     locate(la);
     // (in the loop's order, as in the first kernel)
@@ -506,9 +508,11 @@ __global__ __launch_bounds__(64 * down_waves(NG), NG == 1 ? 4 : 3) void moe_down
       ++at;
       const bool cross = ep + 1 == per;
       Columns<NG> next = cur;
+      float gnext = g2;
       if (cross) {
         ea = min(ea + 1, used - 1);
-        next.set(list[ea], scale[ea], lane);
+        next.set(list[ea], lane);
+        gnext = scale[ea];
       }
       ep = cross ? 0 : ep + 1;
       load_act(next, ep);
@@ -520,11 +524,12 @@ __global__ __launch_bounds__(64 * down_waves(NG), NG == 1 ? 4 : 3) void moe_down
         for (int g = 0; g < NG; ++g) {
           if (4 * g >= __popcll(cur.e.tokens)) break;
           const float v = quad_sum(acc[g], lane);
-          if (cur.token[g] >= 0) mine[cur.token[g] * 16] += v * cur.scale;
+          if (cur.token[g] >= 0) mine[cur.token[g] * 16] += v * g2;
         }
         clear();
       }
       cur = next;
+      g2 = gnext;
     };
     int left = end - at;
     for (; left >= FD; left -= FD) {
@@ -590,9 +595,9 @@ hipError_t launch(MoeMlp& a, int logits_bf16, int out_bf16, hipStream_t s) {
 
 }  // namespace
 
-// Layout: count, the tokens' `bad`, the entries, the activations.
+// Layout: count, the tokens' `bad`, the entries, their scales, the activations.
 size_t nvfp4_moe_mlp_workspace(int64_t T, int64_t E, int64_t K, int64_t h) {
-  return 512 + up256(most_entries(T, E, K, 4) * sizeof(Entry)) + (size_t)(T * K) * act_row(h) * 2;
+  return 512 + up256(most_entries(T, E, K, 4) * sizeof(Entry)) + up256(most_entries(T, E, K, 4) * sizeof(float)) + (size_t)(T * K) * act_row(h) * 2;
 }
 
 hipError_t nvfp4_moe_mlp_launch(const uint16_t* X, int64_t T, int64_t d, int64_t ldx, const void* logits, int logits_bf16, int64_t E,
@@ -609,7 +614,8 @@ hipError_t nvfp4_moe_mlp_launch(const uint16_t* X, int64_t T, int64_t d, int64_t
   a.count = (int32_t*)p;
   a.bad = (float*)(p + 256);
   a.entries = (Entry*)(p + 512);
-  a.act = (uint16_t*)(p + 512 + up256(most_entries(T, E, K, 4) * sizeof(Entry)));
+  a.scales = (float*)((char*)a.entries + up256(most_entries(T, E, K, 4) * sizeof(Entry)));
+  a.act = (uint16_t*)((char*)a.scales + up256(most_entries(T, E, K, 4) * sizeof(float)));
   if (logits && T > kRoutedTokens) {
     const hipError_t e = moe_topk_launch(logits, logits_bf16, T, E, ldl, K, renorm, ids, weights, s);
     if (e != hipSuccess) return e;
