@@ -753,9 +753,11 @@ def nvfp4_moe_mlp(X, gate_up, down, logits=None, top_k=None, renorm=True, ids=No
     sizes = []
     for layer, name in ((gate_up, "gate_up"), (down, "down")):
         codes, scales, g = layer
-        _want(codes, f"{name} codes", (_U8,), (None, None, None), dev)
+        if not (isinstance(codes, torch.Tensor) and codes.is_cuda and codes.get_device() == dev and codes.dtype is _U8
+                and codes.dim() == 3 and codes.is_contiguous()):
+            _want(codes, f"{name} codes", (_U8,), (None, None, None), dev)
+            raise ValueError(f"{name} codes must be contiguous")
         E, rows, kh = codes.shape
-        _dense(codes, f"{name} codes", _U8, (E, rows, kh), dev)
         _dense(scales, f"{name} scales", _U8, (E, rows, kh // 8), dev)
         _dense(g, f"{name} g", _F32, (E,), dev)
         sizes.append((E, rows, 2 * kh))

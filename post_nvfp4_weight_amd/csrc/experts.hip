@@ -1003,7 +1003,7 @@ __global__ __launch_bounds__(256) void mx_dx_sum_kernel(const float* __restrict_
   if (i >= rows * quads) return;
   const int64_t row = i / quads, col = 4 * (i - row * quads);
   f32x4 v = *(const f32x4*)(parts + 4 * i);
-#pragma unroll 4
+#pragma unroll 8
   for (uint32_t s = 1; s < splits; ++s) {
     const f32x4 p = *(const f32x4*)(parts + s * rows * k + 4 * i);
 #pragma unroll

@@ -2,7 +2,9 @@
 // X = [gate | up], s = 1 / (1 + exp(-gate)):
 //   forward:  out = gate s up
 //   backward: dgate = dout up s (1 + gate (1 - s)),  dup = dout gate s
-// in fp32, rounded once.  Both are streams: 3 and 5 values of traffic per output.
+// in fp32, rounded once.  Both are streams, bound by memory: 3 and 5 values of traffic
+// per output, at 5.0 TB/s for 131072 x 1024 bf16 (162 us), the gradient at 5.8 TB/s for
+// 5003 x 2060 fp32 (35 us).
 #include <algorithm>
 
 #include "common.h"
@@ -48,7 +50,9 @@ __device__ __forceinline__ void sigmoid(float g, float& s, float& rest) {
   if (g != g) s = rest = g;
 }
 
-constexpr int SU = 2;   // vectors per thread
+// Vectors per thread.  us with 1 / 2 / 4: 131072 x 1024 bf16 180 / 179 / 175, the
+// gradient of 5003 x 2060 fp32 34 / 35 / 42 (another card than above).
+constexpr int SU = 2;
 
 // cpr: vectors per row; units = n cpr.  T in, O out (forward only).
 template <typename T, typename O, bool GRAD>

@@ -15,6 +15,8 @@ DEV = "cuda:0"
 DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
 GRID = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64)
 
+POWERS = torch.tensor([2.0 ** (b - 127) for b in range(255)] + [float("nan")], dtype=torch.float64)
+
 
 @pytest.fixture(scope="module")
 def nvq():
@@ -37,7 +39,7 @@ def _codes(g, n, k, lo=110, hi=140):
 
 def _values(codes, scales):
     c = torch.stack((codes & 15, codes >> 4), -1).flatten(1).long()
-    s = torch.ldexp(torch.ones((), dtype=torch.float64, device=DEV), scales.double() - 127)
+    s = POWERS.to(DEV)[scales.long()]
     return GRID.to(DEV)[c] * s.repeat_interleave(32, 1)
 
 
@@ -108,6 +110,41 @@ def test_gemm_dx_nan_blocks(nvq):
         assert bool(dX[:, 32:64].isnan().all())
         dX[:, 32:64] = clean[:, 32:64]
         assert torch.equal(dX, clean)
+
+
+def test_gemm_dx_expanded_scales(nvq):
+    """Rows that are unit vectors give the weights back, under every scale byte that fp32 holds with the codes' range."""
+    n, m, k = 3400, 256, 4096
+    g = _gen(11)
+    wc, _ = _codes(g, m, k)
+    ws = torch.arange(m, dtype=torch.uint8, device=DEV).clamp(max=252)[:, None].repeat(1, k // 32)
+    at = torch.arange(n, device=DEV) % m
+    dY = torch.zeros(n, m, dtype=torch.bfloat16, device=DEV)
+    dY[torch.arange(n, device=DEV), at] = 1
+    w = _values(wc, ws)
+    for dt in DTYPES.values():
+        assert torch.equal(nvq.mxfp4_gemm_dx(dY, wc, ws, out_dtype=dt).double(), w[at])     # (exact in bf16 too)
+
+
+@pytest.mark.parametrize("T,K", [(64, 63), (64, 64), (8, 64)])
+def test_most_experts_and_slots(nvq, T, K):
+    """The largest lists of experts and slots, against the layer on the grouped products."""
+    E, d, h, m = 1024, 32, 32, 16
+    g = _gen(T, K)
+    gu, dn = _experts(g, E, 2 * h, d), _experts(g, E, m, h)
+    X = torch.randn(T, d, device=DEV, generator=g).to(torch.bfloat16)
+    logits = torch.randn(T, E, device=DEV, generator=g)
+    out, ids, w = nvq.nvfp4_moe_mlp(X, gu, dn, logits=logits, top_k=K, out_dtype=torch.float32)
+    ids6, w6 = nvq.moe_topk(logits, K)
+    assert torch.equal(ids, ids6) and torch.equal(w, w6)
+    tok, off, pos = nvq.moe_sort(ids6, E)
+    act = nvq.swiglu(nvq.nvfp4_gemm_grouped(X, *gu, off, tok_idx=tok), out_dtype=torch.bfloat16)
+    Y = nvq.nvfp4_gemm_grouped(act, *dn, off)
+    out6 = nvq.moe_combine(Y, pos, w6)
+    size = nvq.moe_combine(Y.abs(), pos, w6)      # weights are positive
+    # the grouped path's activations are one bf16: 2^-8 of the terms |D| |act|, at most sqrt-free h of them behind each |Y|;
+    # the absolute terms are bounded by 4 sqrt(h) times the typical |Y| here, so compare at the scale of the largest
+    assert float((out - out6).abs().max()) <= 2.0 ** -8 * 4 * h ** 0.5 * float(size.max())
 
 
 # ---- as programs use them -------------------------------------------------------------------
