@@ -1102,6 +1102,8 @@ hipError_t nvfp4_gemm_grouped_dx_launch(const uint16_t* dY, int64_t rows, int64_
 // Tiles of 128 or 64 rows x 256 columns, and parts of m: as many as give the
 // device's 512 places a tile each, of at least four steps of 64, whose sums are at
 // most 64 MiB.  (Without parts 64 rows x 28672 x 4096 took 518 us, with them 43.)
+// (Parts of at least 128 / 256 / 512: 333 x 1004 x 1056 18.4 / 17.1 / 19.6 us, 16 x 4096 x 4096
+// 17.7 / 15.1 / 17.6, 256 rows 30.8 / 31.0 / 28.4.)
 // 128 rows where there are more than 512, or where more than 64 have parts of at
 // least 1024 to share the expansion over.  us with 64 / 128 rows: 513 x 4096 x 4096 49 /
 // 41, 2048 rows 105 / 93, 512 rows 42 / 47 (parts of 512), 256 rows 29 / 32, 512 x 14336 x

@@ -139,12 +139,14 @@ def test_most_experts_and_slots(nvq, T, K):
     assert torch.equal(ids, ids6) and torch.equal(w, w6)
     tok, off, pos = nvq.moe_sort(ids6, E)
     act = nvq.swiglu(nvq.nvfp4_gemm_grouped(X, *gu, off, tok_idx=tok), out_dtype=torch.bfloat16)
-    Y = nvq.nvfp4_gemm_grouped(act, *dn, off)
-    out6 = nvq.moe_combine(Y, pos, w6)
-    size = nvq.moe_combine(Y.abs(), pos, w6)      # weights are positive
-    # the grouped path's activations are one bf16: 2^-8 of the terms |D| |act|, at most sqrt-free h of them behind each |Y|;
-    # the absolute terms are bounded by 4 sqrt(h) times the typical |Y| here, so compare at the scale of the largest
-    assert float((out - out6).abs().max()) <= 2.0 ** -8 * 4 * h ** 0.5 * float(size.max())
+    out6 = nvq.moe_combine(nvq.nvfp4_gemm_grouped(act, *dn, off), pos, w6)
+    # Each path's activation is off by at most 64 roundings of 2^-23 of |G||x| and of |U||x| (silu's slope is below 1.1, so
+    # 2 * 2.2 * 64 * 2^-23 < 2^-14 of their product for both together), the grouped one by 2^-8 of itself as well; the
+    # second sums add 2^-16 of |D||act| or less, which the factor 1.05 covers with the bound's own roundings.
+    mag = nvq.nvfp4_gemm_grouped(X.abs(), gu[0] & 0x77, *gu[1:], off, tok_idx=tok)
+    err = 1.05 * (2.0 ** -8 * act.float().abs() + 2.0 ** -14 * mag[:, :h] * mag[:, h:])
+    bound = nvq.moe_combine(nvq.nvfp4_gemm_grouped(err.to(torch.bfloat16), dn[0] & 0x77, *dn[1:], off), pos, w6)
+    assert bool(((out - out6).abs() <= 1.05 * bound + 1e-30).all())
 
 
 # ---- as programs use them -------------------------------------------------------------------
@@ -266,6 +268,86 @@ def test_two_streams_at_once(nvq):
             _equal(outs, want[j % 2])
 
 
+# ---- the largest widths -------------------------------------------------------------------------
+def _sparse(g, n, k, dtype=torch.bfloat16):
+    """[n, k], zero but for 40 columns, the first and the last ones: small sums wherever they lie."""
+    X = torch.zeros(n, k, dtype=dtype, device=DEV)
+    at = torch.cat((torch.tensor([0, 1, k - 2, k - 1], device=DEV), torch.randint(0, k, (36,), device=DEV, generator=g))).unique()
+    X[:, at] = torch.randn(n, len(at), device=DEV, generator=g).to(dtype)
+    return X, at
+
+
+@pytest.mark.parametrize("n", [1, 7, 40, 150])
+def test_widest_products(nvq, n):
+    g = _gen(n, 21)
+    k, m = 3999968, 9
+    wc, ws = _codes(g, m, k)
+    X, at = _sparse(g, n, k)
+    xc, xs = nvq.mxfp4_quantize(X)
+    blocks = (at // 32).unique()
+    cols = (blocks[:, None] * 32 + torch.arange(32, device=DEV)).flatten()
+    x = torch.cat([_values(xc[:, 16 * b:16 * b + 16], xs[:, b:b + 1]) for b in blocks.tolist()], 1)
+    w = torch.cat([_values(wc[:, 16 * b:16 * b + 16], ws[:, b:b + 1]) for b in blocks.tolist()], 1)
+    assert int((xc != 0).sum()) == int((xc[:, (cols[::2] // 2)] != 0).sum())
+    for Y in (nvq.mxfp4_gemm(X, wc, ws), nvq.mxfp4_gemm(xc, wc, ws, x_scales=xs)):
+        _close(Y, x, w.T, len(cols) / 32)                   # (zeros add nothing)
+    m, k = 4000000, 32
+    wc, ws = _codes(g, m, k)
+    xc, xs = _codes(g, n, k)
+    Y = nvq.mxfp4_gemm(xc, wc, ws, x_scales=xs, out_dtype=torch.bfloat16)
+    for rows in (slice(0, 500), slice(m - 500, m)):
+        _close(Y[:, rows], _values(xc, xs), _values(wc[rows], ws[rows]).T, k / 32)
+    dY, at = _sparse(g, n, m)
+    _close(nvq.mxfp4_gemm_dx(dY, wc, ws), dY[:, at].double(), _values(wc[at], ws[at]), len(at) / 16)
+    wc, ws = _codes(g, 16, 3999968)
+    dY = torch.randn(n, 16, device=DEV, generator=g).to(torch.bfloat16)
+    dX = nvq.mxfp4_gemm_dx(dY, wc, ws, out_dtype=torch.bfloat16)
+    _close(dX[:, -640:], dY.double(), _values(wc[:, -320:].contiguous(), ws[:, -20:].contiguous()), 1)
+
+
+E4M3 = torch.arange(128, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+
+
+def _expert_values(layer, e, rows, cols):
+    codes, scales, gs = layer
+    c = (codes[e][rows][:, cols // 2].long() >> (4 * (cols % 2))) & 15
+    return GRID.to(DEV)[c] * E4M3.to(DEV)[scales[e][rows][:, cols // 16].long()] * gs[e].double()
+
+
+@pytest.mark.parametrize("T", [1, 30])
+@pytest.mark.parametrize("d,h,m", [(3999984, 32, 8), (32, 3999984, 8), (32, 32, 4000000)])
+def test_widest_expert_mlp(nvq, T, d, h, m):
+    """At most 48 terms that are not zero per sum: 64 roundings of 2^-23 cover each, as in the operator's own tests."""
+    g = _gen(T, d, h)
+    gu, dn = _experts(g, 2, 2 * h, d), _experts(g, 2, m, h)
+    keep = torch.arange(h, device=DEV)
+    if h > 32:                                             # all but some of the activations zero
+        keep = torch.cat((torch.tensor([0, h - 1], device=DEV), torch.randint(0, h, (30,), device=DEV, generator=g))).unique()
+        codes = torch.zeros_like(gu[0])
+        for part in (keep, keep + h):
+            codes[:, part] = gu[0][:, part]
+        gu = (codes,) + gu[1:]
+    gu, dn = ((c, s, v * k ** 0.5) for (c, s, v), k in ((gu, d), (dn, h)))      # (a term's size, not a long sum's)
+    X, at = _sparse(g, T, d) if d > 32 else (torch.randn(T, d, device=DEV, generator=g).to(torch.bfloat16), torch.arange(d, device=DEV))
+    logits = torch.randn(T, 2, device=DEV, generator=g)
+    out, ids, w = nvq.nvfp4_moe_mlp(X, gu, dn, logits=logits, top_k=1, out_dtype=torch.float32)
+    assert torch.equal(ids[:, 0].long(), logits.argmax(1)) and bool((w == 1).all())
+    some = torch.arange(m, device=DEV) if m < 1000 else torch.cat((torch.arange(500, device=DEV), torch.arange(m - 500, m, device=DEV)))
+    u = 64 * 2.0 ** -23
+    for e in (0, 1):
+        mine = ids[:, 0] == e
+        x = X[mine][:, at].double()
+        gate, up = (x @ _expert_values(gu, e, part, at).T for part in (keep, keep + h))
+        eg, eu = (u * (x.abs() @ _expert_values(gu, e, part, at).abs().T) for part in (keep, keep + h))
+        silu = gate * torch.sigmoid(gate)
+        act = silu * up
+        ea = 1.1 * eg * up.abs() + silu.abs() * eu + 1.1 * eg * eu + act.abs() * (2.0 ** -16 + 32 * 2.0 ** -24)
+        D = _expert_values(dn, e, some, keep).T
+        bound = ea @ D.abs() + 2 * u * ((act.abs() + ea) @ D.abs()) + 1e-30
+        assert bool(((out[mine][:, some].double() - act @ D).abs() <= bound).all())
+    assert float(out.abs().max()) > 0
+
+
 # ---- beyond 32-bit offsets ---------------------------------------------------------------------
 def test_quantize_and_swiglu_past_32_bits(nvq):
     n, k = 70001, 65536                                    # 4.6e9 values
@@ -328,6 +410,12 @@ def test_experts_past_32_bits(nvq, T):
     last = [tuple(t[E - 6:].contiguous() for t in x) for x in (gu, dn)]
     small, _, _ = nvq.nvfp4_moe_mlp(X, *last, ids=ids, weights=w, out_dtype=torch.float32)
     large, _, _ = nvq.nvfp4_moe_mlp(X, gu, dn, ids=ids + (E - 6), weights=w, out_dtype=torch.float32)
-    size = small.abs().max()
-    assert bool(small.isfinite().all()) and float(size) > 0
-    assert float((small - large).abs().max()) <= 2.0 ** -12 * float(size)      # (entries may be grouped otherwise)
+    # Both are within the operator's bound of the exact layer (a wave's share of the second sum may differ): activations by
+    # 2 * 2.2 * (d / 16 + 16) 2^-23 < 2^-12 of |G||x| |U||x| and 2^-16 of themselves, below 1.05 * 2^-12 of that together; second
+    # sums by (2 * 3 h / 16 + 48) 2^-23 < 2^-13 of |D||act|.  Twice that for two results.
+    tok, off, pos = nvq.moe_sort(ids, 6)
+    mag = nvq.nvfp4_gemm_grouped(X.abs(), last[0][0] & 0x77, *last[0][1:], off, tok_idx=tok)
+    err = 2 * (1.05 * 2.0 ** -12 + 2.0 ** -13) * 1.02 * mag[:, :h] * mag[:, h:]      # (1.02: the bound's own bf16 and sums)
+    bound = nvq.moe_combine(nvq.nvfp4_gemm_grouped(err.to(torch.bfloat16), last[1][0] & 0x77, *last[1][1:], off), pos, w)
+    assert bool(small.isfinite().all()) and float(small.abs().max()) > 0
+    assert bool(((small - large).abs() <= bound).all())
