@@ -656,7 +656,8 @@ int mxfp4_gemm(const void* X, int x_dtype, const uint8_t* x_scales, int64_t n, i
 /*
  * mxfp4_gemm_dx -- gradient of mxfp4_gemm with respect to its quantized
  * activations, taken as that of X: dX = dY W (the weights are frozen).  W is
- * exact in bf16; bf16 matrix cores, fp32 sums.
+ * exact in bf16; bf16 matrix cores (one or two rows: fp32 in vector units), fp32
+ * sums.
  *   dY      device bf16 [n x lddy], lddy >= m, aligned by its elements.
  *   dX      device [n x lddx] of dx_dtype (fp32 or bf16, RNE), lddx >= k.
  *   ws      device workspace of mxfp4_gemm_dx_workspace_size(n, m, k) bytes

@@ -971,11 +971,13 @@ int mxfp4_gemm(const void* X, int x_dtype, const uint8_t* x_scales, int64_t n, i
 }
 
 // The first rows on expanded weights, the rest after them in the same workspace; or
-// all in the second form, if dY's alignment asks for it.
+// none on expanded weights, if dY's alignment asks for it.
+static size_t dx_rest_workspace(int64_t n, int64_t m, int64_t k) {
+  return n == 0 ? 0 : mxfp4_gemm_dx_few(n) ? mxfp4_gemm_dx_few_workspace(n, m, k) : mxfp4_gemm_dx_split_workspace(n, m, k);
+}
 static size_t dx_workspace(int64_t n, int64_t m, int64_t k) {
   const int64_t rows = mxfp4_gemm_dx_expanded_rows(n, m, k);
-  return std::max({rows ? (size_t)m * k * 2 : 0, n > rows ? mxfp4_gemm_dx_split_workspace(n - rows, m, k) : 0,
-                   mxfp4_gemm_dx_split_workspace(n, m, k)});
+  return std::max({rows ? (size_t)m * k * 2 : 0, dx_rest_workspace(n - rows, m, k), dx_rest_workspace(n, m, k)});
 }
 
 size_t mxfp4_gemm_dx_workspace_size(int64_t n, int64_t m, int64_t k) {
@@ -1009,8 +1011,9 @@ int mxfp4_gemm_dx(const void* dY, int dy_dtype, int64_t n, int64_t m, int64_t ld
         tiles_status(mxfp4_gemm_dx_expanded_launch(d, rows, m, lddy, codes, scales, k, dX, bf16, lddx, ws, (hipStream_t)stream), fn, n, k);
     if (rc != NVQ_OK || rows == n) return rc;
   }
-  return tiles_status(mxfp4_gemm_dx_launch(d + rows * lddy, n - rows, m, lddy, codes, scales, k,
-                                           (char*)dX + rows * lddx * (bf16 ? 2 : 4), bf16, lddx, ws, (hipStream_t)stream), fn, n, k);
+  const auto rest = mxfp4_gemm_dx_few(n - rows) ? mxfp4_gemm_dx_few_launch : mxfp4_gemm_dx_launch;
+  return tiles_status(rest(d + rows * lddy, n - rows, m, lddy, codes, scales, k, (char*)dX + rows * lddx * (bf16 ? 2 : 4), bf16, lddx, ws,
+                           (hipStream_t)stream), fn, n, k);
 }
 
 int swiglu(const void* X, int x_dtype, int64_t n, int64_t h, int64_t ldx, void* out, int out_dtype, int64_t ldo, void* stream) {

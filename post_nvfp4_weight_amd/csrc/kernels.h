@@ -227,6 +227,11 @@ hipError_t mxfp4_gemm_launch(const void* X, int x_codes, int x_bf16, const uint8
 size_t mxfp4_gemm_dx_split_workspace(int64_t rows, int64_t m, int64_t k);
 hipError_t mxfp4_gemm_dx_launch(const uint16_t* dY, int64_t rows, int64_t m, int64_t lddy, const uint8_t* codes,
                                 const uint8_t* scales, int64_t k, void* dX, int out_bf16, int64_t lddx, void* ws, hipStream_t s);
+// The same for few rows (mxfp4_gemm_dx_few).
+bool mxfp4_gemm_dx_few(int64_t n);
+size_t mxfp4_gemm_dx_few_workspace(int64_t n, int64_t m, int64_t k);
+hipError_t mxfp4_gemm_dx_few_launch(const uint16_t* dY, int64_t n, int64_t m, int64_t lddy, const uint8_t* codes, const uint8_t* scales,
+                                    int64_t k, void* dX, int out_bf16, int64_t lddx, void* ws, hipStream_t s);
 // The same on weights that are expanded into ws (2 m k bytes) first; how many of n
 // rows it is meant for.  dY 16-byte aligned, lddy a multiple of 8 below 2^22.
 int64_t mxfp4_gemm_dx_expanded_rows(int64_t n, int64_t m, int64_t k);

@@ -615,6 +615,128 @@ __global__ __launch_bounds__(256) void mx_transpose_kernel(const uint8_t* __rest
   }
 }
 
+// The gradient of one or two rows: dX[t][c] = sum_m dY[t][m] W[m][c], bound by reading W.
+// A lane holds 16 columns (8 bytes of codes under one scale), a wave 1024, and
+// adds row after row of W, expanded in fp32, to its sums for NR rows of dX;
+// the 8 waves of a workgroup take the rows of its part of m in turn, DB at a time,
+// and add their sums in wave order.  The parts' sums go to `out` [part][row][k] and
+// are added in their order by the second kernel, or with one part are the result.
+// us with this / on the matrix cores' tiles of 64 rows, which want W transposed: one
+// row x 4096 x 4096 8.5 / 12.9, 28672 x 4096 21 / 31, 1000 x 1056 6.8 / 8.9; two rows 9.9 /
+// 13.5, 26 / 32; four, for which each code is expanded once too, 13.5 / 13.4, 36 / 33.
+constexpr int DB = 8, kDxPart = 1024;   // rows of W at a time; most of a part
+
+template <int NR, int OUT>   // OUT: 0 fp32, 1 bf16
+__global__ __launch_bounds__(512) void mx_dx_few_kernel(const uint16_t* __restrict__ dY, int64_t m, int64_t lddy,
+                                                        const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t k,
+                                                        int64_t mper, void* __restrict__ out, int64_t ldo) {
+  __shared__ float dy[NR][kDxPart];
+  __shared__ __attribute__((aligned(16))) float part[8][1024];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t c0 = (int64_t)blockIdx.x * 1024 + 16 * lane, m0 = (int64_t)blockIdx.y * mper;
+  const int rows = (int)min(mper, m - m0);
+  const bool in = c0 < k;
+  const uint8_t* cp = codes + m0 * (k / 2) + (in ? c0 / 2 : 0);
+  const uint8_t* sp = scales + m0 * (k / 32) + (in ? c0 / 32 : 0);
+#pragma unroll
+  for (int t = 0; t < NR; ++t)
+    for (int r = tid; r < rows; r += 512) dy[t][r] = __uint_as_float((uint32_t)dY[t * lddy + m0 + r] << 16);
+  float acc[NR][16];
+#pragma unroll
+  for (int t = 0; t < NR; ++t)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[t][e] = 0.0f;
+  u32x2 w[DB];
+  uint8_t s[DB];
+  auto load = [&](int r0) __attribute__((always_inline)) {   // (rows past the part repeat its last one, under scale 0)
+#pragma unroll
+    for (int j = 0; j < DB; ++j) {
+      const int64_t r = min(r0 + 8 * j, rows - 1);
+      w[j] = *(const u32x2*)(cp + r * (k / 2));
+      s[j] = sp[r * (k / 32)];
+    }
+  };
+  load(wave);
+  __syncthreads();
+  for (int r0 = wave; r0 < rows; r0 += 8 * DB) {
+#pragma unroll
+    for (int j = 0; j < DB; ++j) {
+      const int r = r0 + 8 * j;
+      const float sv = r < rows ? scale_value(s[j]) : 0.0f;
+      float d[NR];
+#pragma unroll
+      for (int t = 0; t < NR; ++t) d[t] = r < rows ? dy[t][min(r, rows - 1)] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t v = w[j][i];
+        const f32x2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 1),
+                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 3)};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = (e & 1 ? p[e / 2].y : p[e / 2].x) * sv;
+#pragma unroll
+          for (int t = 0; t < NR; ++t) acc[t][8 * i + e] = fmaf(x, d[t], acc[t][8 * i + e]);
+        }
+      }
+    }
+    if (r0 + 8 * DB < rows) load(r0 + 8 * DB);
+  }
+#pragma unroll
+  for (int t = 0; t < NR; ++t) {
+    // (piece e of a lane at 256 e + 4 lane: neighbouring lanes side by side)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *(f32x4*)&part[wave][256 * e + 4 * lane] = f32x4{acc[t][4 * e], acc[t][4 * e + 1], acc[t][4 * e + 2], acc[t][4 * e + 3]};
+    __syncthreads();
+    for (int i = tid; i < 1024; i += 512) {
+      const int l = (i & 255) >> 2;
+      const int64_t c = (int64_t)blockIdx.x * 1024 + 16 * l + 4 * (i >> 8) + (i & 3);
+      float v = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v += part[q][i];
+      if (c < k) {
+        const int64_t at = ((int64_t)blockIdx.y * NR + t) * ldo + c;
+        if (OUT) ((__bf16*)out)[at] = (__bf16)v;
+        else ((float*)out)[at] = v;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// The parts' sums: 32 times four columns per workgroup, eight threads' shares of the parts each.
+template <int OUT>
+__global__ __launch_bounds__(256) void mx_dx_parts_kernel(const float* __restrict__ parts, int64_t n, int64_t k, int count,
+                                                          void* __restrict__ dX, int64_t lddx) {
+  __shared__ __attribute__((aligned(16))) f32x4 sums[8][32];
+  const int q = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int64_t i = (int64_t)blockIdx.x * 32 + q, total = n * k;
+  f32x4 v{0.f, 0.f, 0.f, 0.f};
+  if (4 * i < total) {
+#pragma unroll 8
+    for (int p = g; p < count; p += 8) {
+      const f32x4 x = *(const f32x4*)(parts + p * total + 4 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += x[e];
+    }
+  }
+  sums[g][q] = v;
+  __syncthreads();
+  if (g != 0 || 4 * i >= total) return;
+#pragma unroll
+  for (int p = 1; p < 8; ++p) {
+    const f32x4 x = sums[p][q];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += x[e];
+  }
+  const int64_t row = 4 * i / k, at = row * lddx + 4 * i - row * k;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (OUT) ((__bf16*)dX)[at + e] = (__bf16)v[e];
+    else ((float*)dX)[at + e] = v[e];
+  }
+}
+
 // Tiles of 32 output channels x 32 FB rows for sizes that make few tiles: the
 // four waves of a workgroup share k instead, in pairs of stages of 256 in turn, in
 // LDS of their own, so that none waits for another (with the waves at the four
@@ -913,6 +1035,45 @@ hipError_t mxfp4_gemm_launch(const void* X, int x_codes, int x_bf16, const uint8
 #undef NVQ_FEW_BY
 #undef NVQ_FEW
 #undef NVQ_FEW_
+}
+
+// One or two rows of the gradient: parts of m of at least 64 and at most kDxPart, for
+// 256 workgroups where m allows it.  (us with 256 / 512 / 1024, one row x 28672 x 4096
+// 21.0 / 23.6 / 24.2, 4096 x 14336 15.0 / 15.7 / 15.6.)
+namespace {
+int64_t dx_few_part(int64_t m, int64_t k) {
+  const int64_t parts = std::max<int64_t>(1, 256 / ((k + 1023) / 1024));
+  return std::min<int64_t>(kDxPart, std::max<int64_t>(64, ((m + parts - 1) / parts + 63) / 64 * 64));
+}
+}  // namespace
+bool mxfp4_gemm_dx_few(int64_t n) { return n <= 2; }
+size_t mxfp4_gemm_dx_few_workspace(int64_t n, int64_t m, int64_t k) {
+  const int64_t mper = dx_few_part(m, k), parts = (m + mper - 1) / mper;
+  return parts > 1 ? (size_t)(parts * n * k * 4) : 0;
+}
+hipError_t mxfp4_gemm_dx_few_launch(const uint16_t* dY, int64_t n, int64_t m, int64_t lddy, const uint8_t* codes, const uint8_t* scales,
+                                    int64_t k, void* dX, int out_bf16, int64_t lddx, void* ws, hipStream_t s) {
+  const int64_t mper = dx_few_part(m, k), parts = (m + mper - 1) / mper;
+  const bool one = parts == 1;
+  const dim3 grid((unsigned)((k + 1023) / 1024), (unsigned)parts);   // (at most 3907 each)
+#define NVQ_DX_(NR, OUT)                                                                                                         \
+  hipLaunchKernelGGL((mx_dx_few_kernel<NR, OUT>), grid, dim3(512), 0, s, dY, m, lddy, codes, scales, k, mper, one ? dX : ws, \
+                     one ? lddx : k)
+#define NVQ_DX(NR)                           \
+  do {                                       \
+    if (one && out_bf16) NVQ_DX_(NR, 1);     \
+    else NVQ_DX_(NR, 0);                     \
+  } while (0)
+  if (n == 1) NVQ_DX(1);
+  else NVQ_DX(2);
+#undef NVQ_DX
+#undef NVQ_DX_
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || one) return e;
+  const dim3 sums((unsigned)((n * k / 4 + 31) / 32));
+  if (out_bf16) hipLaunchKernelGGL((mx_dx_parts_kernel<1>), sums, dim3(256), 0, s, (const float*)ws, n, k, (int)parts, dX, lddx);
+  else hipLaunchKernelGGL((mx_dx_parts_kernel<0>), sums, dim3(256), 0, s, (const float*)ws, n, k, (int)parts, dX, lddx);
+  return hipGetLastError();
 }
 
 // The gradient of many rows: the weights are expanded and transposed once, into

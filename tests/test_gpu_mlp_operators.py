@@ -78,7 +78,8 @@ def test_gemm_forms(nvq, n, m, k, xtype, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("n,m,k", [(1, 4100, 96), (2, 1000, 512), (64, 2049, 288), (65, 9000, 64), (200, 20000, 32), (512, 12345, 288),   # parts of m
+@pytest.mark.parametrize("n,m,k", [(1, 1, 32), (2, 7, 1056), (1, 64, 2080), (2, 65, 4096), (1, 300000, 32), (2, 2055, 1056),          # one or two rows
+                                   (1, 4100, 96), (2, 1000, 512), (3, 1000, 512), (64, 2049, 288), (65, 9000, 64), (200, 20000, 32), (512, 12345, 288),   # parts of m
                                    (513, 700, 1056), (130, 264, 32992),                                              # none
                                    (3400, 72, 4128), (3400, 200, 4096), (8900, 136, 4096), (13400, 64, 1024),   # expanded
                                    (3400, 77, 4128)])                                                                # rows that rule it out
@@ -99,7 +100,7 @@ def test_gemm_dx_forms(nvq, n, m, k, dtype):
 
 def test_gemm_dx_nan_blocks(nvq):
     """A NaN block makes its 32 columns NaN in every form, nothing else changes."""
-    for n, m, k in ((3, 2000, 96), (600, 128, 64), (3400, 64, 4096)):
+    for n, m, k in ((1, 2000, 96), (3, 2000, 96), (600, 128, 64), (3400, 64, 4096)):
         g = _gen(n)
         wc, ws = _codes(g, m, k)
         dY = torch.randn(n, m, device=DEV, generator=g).to(torch.bfloat16)
@@ -124,6 +125,23 @@ def test_gemm_dx_expanded_scales(nvq):
     w = _values(wc, ws)
     for dt in DTYPES.values():
         assert torch.equal(nvq.mxfp4_gemm_dx(dY, wc, ws, out_dtype=dt).double(), w[at])     # (exact in bf16 too)
+
+
+def test_gemm_dx_single_row_scales(nvq):
+    """One row, a unit vector: every scale byte that fp32 holds, and one whose values leave it beside zero codes (no NaN)."""
+    m, k = 253, 64
+    g = _gen(12)
+    wc, _ = _codes(g, m, k)
+    ws = torch.arange(m, dtype=torch.uint8, device=DEV)[:, None].repeat(1, 2)
+    w = _values(wc, ws)
+    for i in (0, 1, 2, 100, 251, 252):
+        dY = torch.zeros(1, m, dtype=torch.bfloat16, device=DEV)
+        dY[0, i] = 1
+        assert torch.equal(nvq.mxfp4_gemm_dx(dY, wc, ws)[0].double(), w[i])
+    wc[-1], ws[-1] = 0, 254
+    dY = torch.full((2, m), 8.0, dtype=torch.bfloat16, device=DEV)
+    dY[:, :-1] = 0
+    assert bool((nvq.mxfp4_gemm_dx(dY, wc, ws) == 0).all())
 
 
 @pytest.mark.parametrize("T,K", [(64, 63), (64, 64), (8, 64)])
@@ -182,7 +200,7 @@ def _programs(nvq, seed):
     def draw(n):
         return lambda: [torch.randn(n, d, device=DEV).to(torch.bfloat16), torch.randn(n, d, device=DEV).to(torch.bfloat16)]
 
-    progs = [(f"dense {n}", lambda X, dout: _dense_step(nvq, X, dout, W1, W2), draw(n)) for n in (1, 40, 600)]
+    progs = [(f"dense {n}", lambda X, dout: _dense_step(nvq, X, dout, W1, W2), draw(n)) for n in (1, 2, 40, 600)]
     progs += [(f"experts {T}", lambda X, logits: _moe_step(nvq, X, logits, gu, dn),
                lambda T=T: [torch.randn(T, d, device=DEV).to(torch.bfloat16), torch.randn(T, 20, device=DEV)]) for T in (1, 8, 9, 64)]
     progs += [("expanded", lambda dY: [nvq.mxfp4_gemm_dx(dY, *wide)], lambda: [torch.randn(3400, 64, device=DEV).to(torch.bfloat16)])]
