@@ -780,8 +780,10 @@ __device__ __forceinline__ void gradient_step(const char* __restrict__ yb, const
       __builtin_amdgcn_sched_barrier(0);
     }
     if (j == 3) {
-      // The next step's copies: behind them were issued this step's and at least one register load.
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(NY + NC + 1));
+      // The next step's copies: behind them were issued this step's.  The register loads
+      // between them do not count: the compiler may put them under a branch, which a wave
+      // without a row inside m skips.
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(NY + NC));
       asm volatile("s_barrier" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
       read_grad_codes<CF, F>(cn, sn, 0, crd, srd, q);
