@@ -359,9 +359,9 @@ __global__ __launch_bounds__(256) void nvfp4_gemm_big_kernel(const uint16_t* __r
   __syncthreads();   // waits for every load so far, X steps 0 and 1 included
 
   const int arow = wr * 128 + (lane & 31), brow = wc * 128 + (lane & 31), kc = lane >> 5;
-  // Per step st: 4 loads of X step st+2 (first), 4 loads of codes step st+3
+  // Per step st: 4 loads of X step st+2 (first), 2 loads of codes and scales step st+3
   // (product 20).  At the end, X step st+1 must have landed: after it were
-  // issued the codes of st+2, X of st+2 and the codes of st+3, 12 loads.
+  // issued the codes of st+2, X of st+2 and the codes of st+3, 8 loads.
   auto body = [&](const uint16_t* __restrict__ Xs, const uint16_t* __restrict__ Qs, uint16_t* __restrict__ nq,
                   int64_t st, u32x2 (&cv)[2], uint32_t (&sv)[2]) {
     bf16x8 a[2][4], b[2][4];
@@ -391,7 +391,7 @@ __global__ __launch_bounds__(256) void nvfp4_gemm_big_kernel(const uint16_t* __r
         if (g == 20) load_q(st + 3, cv, sv);
         __builtin_amdgcn_sched_barrier(0);
       }
-    __builtin_amdgcn_s_waitcnt(12 | (7 << 4) | (0 << 8));   // vmcnt(12), lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt(8 | (7 << 4) | (0 << 8));   // vmcnt(8), lgkmcnt(0)
     asm volatile("s_barrier" ::: "memory");
   };
   // Steps go in pairs with no branch between them (a join would make the

@@ -99,3 +99,22 @@ def test_gradient_waits_for_the_next_step(kernels, part):
         assert any(0 < out for _, out in waits), name
         for fewest, out in waits:
             assert out <= fewest, (name, fewest, out)
+
+
+def test_weight_only_product_waits_for_the_next_step(kernels):
+    """The step's activations were issued first of the step before, four copies; behind them in that step and in this one all else."""
+    for name, code in _some(kernels, "nvfp4_gemm_big_kernel"):
+        steps = [(fewest, out) for fewest, out in _waits(code) if out > 0]
+        assert steps, name
+        least = min(fewest for fewest, _ in steps)
+        for _, out in steps:
+            assert out <= 2 * least - 4, (name, least, out)
+
+
+# mx_tile_kernel's ring of R buffers: the copies of R - 2 steps may stay out.
+@pytest.mark.parametrize("tile,ring", [("Li2ELi4ELi4ELi2ELi2E", 2), ("Li2ELi2ELi2ELi2ELi2E", 2), ("Li2ELi2ELi2ELi1ELi4E", 4),
+                                       ("Li2ELi2ELi1ELi1ELi6E", 6)])
+def test_block_scaled_product_waits_for_its_step(kernels, tile, ring):
+    for name, code in _some(kernels, "mx_tile_kernelI" + tile):
+        for fewest, out in _waits(code):
+            assert out <= (ring - 2) * fewest, (name, fewest, out)
