@@ -575,11 +575,19 @@ hipError_t launch(MoeMlp& a, int logits_bf16, int out_bf16, hipStream_t s) {
     if (a.d % kChunk) hipLaunchKernelGGL((moe_up_kernel<L, EPL, NG, true>), up, dim3(64 * MW), lds, s, a);      \
     else hipLaunchKernelGGL((moe_up_kernel<L, EPL, NG, false>), up, dim3(64 * MW), lds, s, a);                  \
   } while (0)
+  // (elements per lane as moe_topk takes them: the sum over all experts has their order)
+#define NVQ_UP_BY(L)                   \
+  do {                                 \
+    if (a.E <= 64) NVQ_UP(L, 1);       \
+    else if (a.E <= 128) NVQ_UP(L, 2); \
+    else if (a.E <= 256) NVQ_UP(L, 4); \
+    else if (a.E <= 512) NVQ_UP(L, 8); \
+    else NVQ_UP(L, 16);                \
+  } while (0)
   if (!a.logits) NVQ_UP(float, 1);
-  else if (logits_bf16 && a.E <= 256) NVQ_UP(uint16_t, 4);
-  else if (logits_bf16) NVQ_UP(uint16_t, 16);
-  else if (a.E <= 256) NVQ_UP(float, 4);
-  else NVQ_UP(float, 16);
+  else if (logits_bf16) NVQ_UP_BY(uint16_t);
+  else NVQ_UP_BY(float);
+#undef NVQ_UP_BY
 #undef NVQ_UP
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
