@@ -697,7 +697,8 @@ int swiglu_backward(const void* dout, int64_t ldd, const void* X, int dtype, int
  *   out[t] = sum_s weights[t][s] D_e (silu(G_e x_t) * (U_e x_t)),  e = ids[t][s],
  * in two kernels, where moe_topk .. moe_combine with swiglu between two
  * nvfp4_gemm_grouped take six.  NVFP4 weights expanded to bf16, fp32 sums; the
- * activation between the products keeps at least 16 significant bits.
+ * activation between the products (times its weight) keeps fp32's 24 bits for an fp32
+ * result, as long as it is above 2^-102, and at least 16 for a bf16 one, above 2^-110.
  *
  *   X        device bf16 [T x ldx], 16-byte aligned, 0 <= T <= 64; d >= 32, d %
  *            16 == 0, ldx >= d, ldx % 8 == 0, (T - 1) ldx + d <= 2^30.

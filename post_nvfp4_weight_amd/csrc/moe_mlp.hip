@@ -4,9 +4,12 @@
 //      and each of its tokens  act = w silu(G x) (U x),  w the token's weight;
 //   2. out[t] = sum over its experts of g_e D act.
 // Q = e2m1 * e4m3 is exact in bf16 and g is applied to the sums.  The
-// activation between the products is held as two bf16 parts, hi + lo (16 or more
-// significant bits as long as it is above 2^-110): as one bf16 it would be the one value
-// that the layer rounds to 8 bits before its end, for a product that waits for weights anyway.
+// activation between the products is held as a sum of bf16 parts: two where the
+// result is bf16 (16 or more significant bits as long as it is above 2^-110), as one
+// bf16 it would be the one value that the layer rounds to 8 bits before its end, for a
+// product that waits for weights anyway; three where the result is fp32 (all 24
+// bits above 2^-102): against 64 bits 2.1e-7 where two gave 2.4e-6 and fp32 throughout
+// gives 1.9e-7 (4096 x 1024), for 64 x 2 of 8 experts 141 us instead of 126, one token 25.4 instead of 24.6.
 //
 // What bounds it is reading the weights of the experts in use once, and the
 // instructions that expand them: 37 tokens x 8 of 256 experts, 2048 x 4096 and 4096 x
@@ -55,6 +58,7 @@ struct MoeMlp {
   void* out;
   int64_t ldx, ldl, d, h, m, ldo;
   int T, E, K, renorm;
+  int parts;          // of an activation
   // workspace
   int32_t* count;     // entries
   float* bad;         // per token: 0, or NaN from the weight of a slot without an expert
@@ -63,10 +67,15 @@ struct MoeMlp {
   uint16_t* act;      // activations, act_row(h) elements per row
 };
 
+// Bf16 parts that an activation is the sum of.
+constexpr int act_parts(bool out_bf16) { return out_bf16 ? 2 : 3; }
 // A row of the activations: chunks of 512, and in each, for each j of a piece's
-// four times 8 and for hi, then lo, the 16 pieces' 8: what one load takes is 256 bytes in a row.
-__host__ __device__ __forceinline__ int64_t act_row(int64_t h) { return (h + kChunk - 1) / kChunk * kChunk * 2; }
-__device__ __forceinline__ int64_t act_at(int k) { return (int64_t)(k >> 9) * 1024 + ((k >> 3) & 3) * 256 + ((k >> 5) & 15) * 8 + (k & 7); }   // hi; lo 128 behind
+// four times 8 and for each part, the 16 pieces' 8: what one load takes is 256 bytes in a row.
+__host__ __device__ __forceinline__ int64_t act_row(int64_t h, int parts) { return (h + kChunk - 1) / kChunk * kChunk * parts; }
+// The first part; the others 128 behind each other.
+__device__ __forceinline__ int64_t act_at(int k, int parts) {
+  return ((int64_t)(k >> 9) * 512 + ((k >> 3) & 3) * 128) * parts + ((k >> 5) & 15) * 8 + (k & 7);
+}
 
 // 512 k of 16 channels.  s[i]: two scales, of the piece's halves (16 bits wide, as
 // loaded: a conversion would wait for the load at the loop's end).
@@ -347,12 +356,13 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(const MoeMlp a) {
       up *= g1;
       const float z = expf(-fabsf(gate)), one = 1.0f / (1.0f + z);
       const float v = gate * (gate >= 0.0f ? one : z * one) * up * wrow[cur.e.row + t];
-      const __bf16 hi = (__bf16)v;
-      const float rest = v - (float)hi;
-      const __bf16 lo = (__bf16)(fabsf((float)hi) < __builtin_inff() ? rest : 0.0f);   // (an infinity or NaN is in hi alone)
-      uint16_t* to = a.act + (cur.e.row + t) * act_row(a.h) + act_at(k);
-      to[0] = __builtin_bit_cast(uint16_t, hi);
-      to[128] = __builtin_bit_cast(uint16_t, lo);
+      uint16_t* to = a.act + (cur.e.row + t) * act_row(a.h, a.parts) + act_at(k, a.parts);
+      float rest = v;
+      for (int q = 0; q < a.parts; ++q, to += 128) {
+        const __bf16 b = (__bf16)rest;
+        *to = __builtin_bit_cast(uint16_t, b);
+        rest = fabsf((float)b) < __builtin_inff() ? rest - (float)b : 0.0f;   // (an infinity or NaN is in the first part alone)
+      }
     }
     __syncthreads();
   };
@@ -422,12 +432,12 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(const MoeMlp a) {
 // [token][channel]; the waves' totals are added in wave order.  Columns without
 // a token are added nowhere (a rejected weight row makes them NaN).
 template <int OUT_BF16, int NG, bool REST>
-__global__ __launch_bounds__(64 * down_waves(NG), NG == 1 ? 4 : 3) void moe_down_kernel(const MoeMlp a) {
-  constexpr int DW = down_waves(NG), FD = 1;
+__global__ __launch_bounds__(64 * down_waves(NG), NG == 1 ? 4 : OUT_BF16 ? 3 : 2) void moe_down_kernel(const MoeMlp a) {
+  constexpr int DW = down_waves(NG), FD = 1, PARTS = act_parts(OUT_BF16);
   extern __shared__ __attribute__((aligned(16))) char dyn[];
   float* totals = (float*)dyn;   // [wave][token][16]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t o0 = (int64_t)blockIdx.x * 16, stride = act_row(a.h);
+  const int64_t o0 = (int64_t)blockIdx.x * 16, stride = act_row(a.h, PARTS);
   const int used = *a.count, per = (int)((a.h + kChunk - 1) / kChunk);
   Entry* list = (Entry*)(totals + DW * a.T * 16);
   float* scale = (float*)(list + most_entries(a.T, a.E, a.K, 4 * NG));
@@ -458,18 +468,18 @@ __global__ __launch_bounds__(64 * down_waves(NG), NG == 1 ? 4 : 3) void moe_down
       }
     };
     const int piece = 4 * (lane >> 4) + (lane & 3);
-    u32x4 x[NG][4][2];
+    u32x4 x[NG][4][PARTS];
     auto load_act = [&](const Columns<NG>& of, int p) NVQ_INLINE {   // zeros where there is no token and from h on
       const __amdgpu_buffer_rsrc_t rs = buffer_of(a.act + of.e.row * stride, (uint32_t)(__popcll(of.e.tokens) * stride * 2));
       const int k0 = p * kChunk + 32 * piece;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const uint32_t row = of.token[g] >= 0 ? (uint32_t)((4 * g + ((lane >> 2) & 3)) * stride * 2 + p * 2048 + piece * 16) : kNone;
+        const uint32_t row = of.token[g] >= 0 ? (uint32_t)((4 * g + ((lane >> 2) & 3)) * stride * 2 + p * (1024 * PARTS) + piece * 16) : kNone;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t off = !REST || k0 + 8 * j < a.h ? row + j * 512 : kNone;
-          x[g][j][0] = load16(rs, off);
-          x[g][j][1] = load16(rs, off + 256);
+          const uint32_t off = !REST || k0 + 8 * j < a.h ? row + j * (256 * PARTS) : kNone;
+#pragma unroll
+          for (int q = 0; q < PARTS; ++q) x[g][j][q] = load16(rs, off + 256 * q);
         }
       }
     };
@@ -502,10 +512,9 @@ __global__ __launch_bounds__(64 * down_waves(NG), NG == 1 ? 4 : 3) void moe_down
         for (int j = 0; j < 4; ++j) {
           const bf16x8 v = expand(b.w[n], b.s[n], j);
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            acc[g][n] = mfma(v, x[g][j][0], acc[g][n]);
-            acc[g][n] = mfma(v, x[g][j][1], acc[g][n]);
-          }
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) acc[g][n] = mfma(v, x[g][j][q], acc[g][n]);
         }
       __builtin_amdgcn_sched_barrier(0);
       ++at;
@@ -606,9 +615,9 @@ hipError_t launch(MoeMlp& a, int logits_bf16, int out_bf16, hipStream_t s) {
 
 }  // namespace
 
-// Layout: count, the tokens' `bad`, the entries, their scales, the activations.
+// Layout: count, the tokens' `bad`, the entries, their scales, the activations (of as many parts as any result takes).
 size_t nvfp4_moe_mlp_workspace(int64_t T, int64_t E, int64_t K, int64_t h) {
-  return 512 + up256(most_entries(T, E, K, 4) * sizeof(Entry)) + up256(most_entries(T, E, K, 4) * sizeof(float)) + (size_t)(T * K) * act_row(h) * 2;
+  return 512 + up256(most_entries(T, E, K, 4) * sizeof(Entry)) + up256(most_entries(T, E, K, 4) * sizeof(float)) + (size_t)(T * K) * act_row(h, act_parts(false)) * 2;
 }
 
 hipError_t nvfp4_moe_mlp_launch(const uint16_t* X, int64_t T, int64_t d, int64_t ldx, const void* logits, int logits_bf16, int64_t E,
@@ -621,6 +630,7 @@ hipError_t nvfp4_moe_mlp_launch(const uint16_t* X, int64_t T, int64_t d, int64_t
   a.dcodes = dcodes; a.dscales = dscales; a.dg = dg;
   a.out = out; a.ldx = ldx; a.ldl = ldl; a.d = d; a.h = h; a.m = m; a.ldo = ldo;
   a.T = (int)T; a.E = (int)E; a.K = K; a.renorm = renorm;
+  a.parts = act_parts(out_bf16);
   char* p = (char*)ws;
   a.count = (int32_t*)p;
   a.bad = (float*)(p + 256);
