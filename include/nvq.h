@@ -656,8 +656,8 @@ int mxfp4_gemm(const void* X, int x_dtype, const uint8_t* x_scales, int64_t n, i
 /*
  * mxfp4_gemm_dx -- gradient of mxfp4_gemm with respect to its quantized
  * activations, taken as that of X: dX = dY W (the weights are frozen).  W is
- * exact in bf16; bf16 matrix cores (one or two rows: fp32 in vector units), fp32
- * sums.
+ * exact in bf16 (an infinity above its range, as mxfp4_dequantize gives it);
+ * bf16 matrix cores (one or two rows: fp32 in vector units), fp32 sums.
  *   dY      device bf16 [n x lddy], lddy >= m, aligned by its elements.
  *   dX      device [n x lddx] of dx_dtype (fp32 or bf16, RNE), lddx >= k.
  *   ws      device workspace of mxfp4_gemm_dx_workspace_size(n, m, k) bytes
@@ -695,10 +695,11 @@ int swiglu_backward(const void* dout, int64_t ldd, const void* X, int dtype, int
  * nvfp4_moe_mlp -- a whole mixture-of-experts MLP for a few tokens (decode): the
  * router, each token's experts and their weighted sum,
  *   out[t] = sum_s weights[t][s] D_e (silu(G_e x_t) * (U_e x_t)),  e = ids[t][s],
- * in two kernels, where moe_topk .. moe_combine with swiglu between two
- * nvfp4_gemm_grouped take six.  NVFP4 weights expanded to bf16, fp32 sums; the
- * activation between the products (times its weight) keeps fp32's 24 bits for an fp32
- * result, as long as it is above 2^-102, and at least 16 for a bf16 one, above 2^-110.
+ * in two kernels (three where it routes more than 8 tokens), where moe_topk ..
+ * moe_combine with swiglu between two nvfp4_gemm_grouped take six.  NVFP4
+ * weights expanded to bf16, fp32 sums; the activation between the products (times
+ * its weight) keeps fp32's 24 bits for an fp32 result, as long as it is above
+ * 2^-102, and at least 16 for a bf16 one, above 2^-110.
  *
  *   X        device bf16 [T x ldx], 16-byte aligned, 0 <= T <= 64; d >= 32, d %
  *            16 == 0, ldx >= d, ldx % 8 == 0, (T - 1) ldx + d <= 2^30.

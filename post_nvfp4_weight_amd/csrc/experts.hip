@@ -667,6 +667,9 @@ __global__ __launch_bounds__(64 * FW, 4) void grouped_few_kernel(const uint16_t*
 // The two weight formats differ in their scales alone.  F::kBlock: codes per
 // scale.  A scale is staged as it is multiplied by: an E4M3 byte, or the bf16
 // of an E8M0 byte (2^-127 is a bf16 below the normal range, NaN stays NaN).
+// MXFP4's two bytes are converted where they are loaded, so that a step waits for
+// each and, as loads return in order, for the copies ahead of it: 333 x 1004 x 1056
+// takes 14 us for its four steps, 64 rows x 4096 x 4096 16.7 for four.
 struct Nvfp4 {
   static constexpr int kBlock = 16, kBytes = 1;
   // Of the scales of 16 m, those of m = 8 v + 2 piece and the next.

@@ -1,5 +1,5 @@
 // A whole mixture-of-experts MLP with NVFP4 experts for a few tokens (at most
-// 64), in two kernels:
+// 64), in two kernels (more than 8 tokens are routed by moe_topk's kernel before them):
 //   1. routing (moe_topk's choice, or the caller's), then for each expert in use
 //      and each of its tokens  act = w silu(G x) (U x),  w the token's weight;
 //   2. out[t] = sum over its experts of g_e D act.
